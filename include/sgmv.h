@@ -452,6 +452,102 @@ sgmv_status_t sgmv_base_lora_apply_partial(const sgmv_problem_t* problem, const 
                                            const void* const* B_ptrs, float* Yp, const int32_t* seg_indptr,
                                            const int32_t* lora_idx, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Whole layers of any number of rows, and their gradients ----
+ *
+ * Punica README, LoRA paragraph: a row x gets x@W + x@A@B; multi-LoRA
+ * paragraph: every row of a batch brings its own LoRA.  sgmv_base_lora_apply
+ * computes that for decode-sized batches.  The entry points below take any
+ * number of rows (a single token, a decode batch, prompts, a training
+ * micro-batch), the ranks and scales of sgmv_projection_t, and add the backward pass and
+ * the gated feed-forward block, whose gate and up projections are two such layers
+ * that read the same X:
+ *
+ *   sgmv_dense_lora_apply     Y[i, :] = X[i, :] @ W + s_k (X[i, :] @ A_k) @ B_k
+ *   sgmv_gated_lora_apply     G, U = two such outputs;  H = act(G) * U
+ *   sgmv_dense_lora_backward  from dY:  dX = dY @ W^T + s_k (dY @ B_k^T) @ A_k^T
+ *                             dA_k = s_k sum_i X[i, :]^T (dY[i, :] @ B_k^T)
+ *                             dB_k = s_k sum_i (X[i, :] @ A_k)^T dY[i, :]
+ *                             dW   = X^T @ dY
+ *   sgmv_gated_lora_backward  from dH:  dG = dH * U * act'(G), dU = dH * act(G), then
+ *                             the above for both projections, dX their sum
+ * with k = lora_idx[s], i in segment s; rows no segment covers have no LoRA
+ * term.  problem->h_in is the width of X, h_out the width of Y (G, U, H);
+ * problem->variant and splits are not used.
+ *
+ * Layouts (device, row-major, contiguous, 16-byte aligned, in the problem's
+ * 16-bit format): X, dX [n_rows, h_in]; Y, dY, G, U, H, dH [n_rows, h_out];
+ * W, Wg, Wu, dW [h_in, h_out]; A_k, dA_k [h_in, r_k]; B_k, dB_k [r_k, h_out], reached
+ * through device tables of num_loras pointers.  Outputs may not alias inputs
+ * or each other.  seg_indptr, lora_idx: device, preconditions as for
+ * sgmv_lora_apply (they and the tables may be NULL when num_segs == 0 or max_seg_len == 0).
+ *
+ * sgmv_projection_t: A_ptrs, B_ptrs, ranks and scales as in
+ * sgmv_lora_apply_batched; entries of LoRAs no segment uses are not read, a
+ * null A_k or B_k of a used LoRA counts as rank 0.  Y: the output of
+ * sgmv_dense_lora_apply (written); for sgmv_gated_lora_apply where to store G
+ * (U), or NULL; for sgmv_gated_lora_backward the stored G (U), read; not used by
+ * sgmv_dense_lora_backward.
+ *
+ * Precision: sums are fp32; every output is rounded once, from fp32 (H from
+ * the unrounded G and U).  X @ A_k and dY @ B_k^T stay fp32.  The gated backward
+ * rounds dG and dU to the 16-bit format once, since they are operands of the matrix
+ * cores.  Results do not depend on timing: no atomics, sums in a fixed order.
+ *
+ * Gradients (sgmv_projection_grad_t): each of dX, dW, dA_ptrs, dB_ptrs may be
+ * NULL (not wanted), and so may entries of the dA and dB tables and the whole
+ * struct.  dX is always written.  accumulate = 0: dW and every wanted dA_k, dB_k are
+ * written (zero for a LoRA without rows); accumulate = 1: the gradient is added to what is there
+ * in fp32 and rounded once, and LoRAs without rows are not touched.
+ * Gradients of different LoRAs may not overlap.
+ *
+ * ws: device workspace of sgmv_layer_workspace_bytes(problem, op) bytes (any
+ * contents); calls that share one must not overlap.  All launches go to
+ * `stream`; the calls can be captured into a graph.  n_rows = 0: the forward
+ * calls do nothing, the backward calls write zero gradients (accumulate = 0).  Errors
+ * as for sgmv_lora_apply; SGMV_ERR_INVALID_ARG for an act, op or accumulate
+ * outside its values. */
+typedef enum sgmv_act {
+  SGMV_ACT_SILU = 0,      /* g / (1 + e^-g) */
+  SGMV_ACT_GELU_TANH = 1  /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+} sgmv_act_t;
+
+/* Entry point a workspace is for. */
+typedef enum sgmv_layer_op {
+  SGMV_DENSE_FORWARD = 0,
+  SGMV_DENSE_BACKWARD = 1,
+  SGMV_GATED_FORWARD = 2,
+  SGMV_GATED_BACKWARD = 3
+} sgmv_layer_op_t;
+
+/* Where the gradients of one projection go (device pointers). */
+typedef struct sgmv_projection_grad {
+  void* dW;               /* [h_in, h_out], or NULL */
+  void* const* dA_ptrs;   /* [num_loras] pointers to dA_k [h_in, r_k], or NULL */
+  void* const* dB_ptrs;   /* [num_loras] pointers to dB_k [r_k, h_out], or NULL */
+} sgmv_projection_grad_t;
+
+/* Workspace bytes of the entry point `op` (sgmv_layer_op_t) for *problem; may be 0. */
+sgmv_status_t sgmv_layer_workspace_bytes(const sgmv_problem_t* problem, int32_t op, size_t* bytes);
+
+sgmv_status_t sgmv_dense_lora_apply(const sgmv_problem_t* problem, const void* X, const void* W,
+                                    const sgmv_projection_t* proj, const int32_t* seg_indptr,
+                                    const int32_t* lora_idx, void* ws, size_t ws_bytes, void* stream);
+sgmv_status_t sgmv_gated_lora_apply(const sgmv_problem_t* problem, const void* X, const void* Wg, const void* Wu,
+                                    const sgmv_projection_t* gate, const sgmv_projection_t* up, int32_t act, void* H,
+                                    const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
+                                    void* stream);
+sgmv_status_t sgmv_dense_lora_backward(const sgmv_problem_t* problem, const void* X, const void* W,
+                                       const sgmv_projection_t* proj, const void* dY, void* dX,
+                                       const sgmv_projection_grad_t* grad, int32_t accumulate,
+                                       const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
+                                       void* stream);
+sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* problem, const void* X, const void* Wg, const void* Wu,
+                                       const sgmv_projection_t* gate, const sgmv_projection_t* up, int32_t act,
+                                       const void* dH, void* dX, const sgmv_projection_grad_t* gate_grad,
+                                       const sgmv_projection_grad_t* up_grad, int32_t accumulate,
+                                       const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
+                                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -35,11 +35,15 @@ ENTRY_POINTS = ("sgmv_status_str", "sgmv_build_segments", "sgmv_check_problem",
                 "sgmv_expand", "sgmv_lora_apply", "sgmv_lora_apply_batched", "sgmv_base_workspace_bytes",
                 "sgmv_base_lora_apply", "sgmv_base_packed_weight_bytes", "sgmv_base_pack_weight",
                 "sgmv_base_lora_apply_packed", "sgmv_set_wait_limit", "sgmv_take_device_errors",
-                "sgmv_lora_apply_noalloc", "sgmv_base_lora_apply_partial", "sgmv_lora_apply_host_meta")
+                "sgmv_lora_apply_noalloc", "sgmv_base_lora_apply_partial", "sgmv_lora_apply_host_meta",
+                "sgmv_layer_workspace_bytes", "sgmv_dense_lora_apply", "sgmv_gated_lora_apply",
+                "sgmv_dense_lora_backward", "sgmv_gated_lora_backward")
 SGMV_DEVICE_ERR_WAIT_TIMEOUT = 1
 SGMV_NOALLOC_MAX_WORKSPACE = 16 << 20
 SGMV_BASE_MAX_ROWS = 128
 SGMV_HOST_META_MAX_SEGS = 64
+SGMV_ACT_SILU, SGMV_ACT_GELU_TANH = range(2)
+SGMV_DENSE_FORWARD, SGMV_DENSE_BACKWARD, SGMV_GATED_FORWARD, SGMV_GATED_BACKWARD = range(4)
 
 
 class SgmvError(RuntimeError):
@@ -69,6 +73,10 @@ class sgmv_plan_info_t(ctypes.Structure):
 class sgmv_projection_t(ctypes.Structure):
     _fields_ = [("A_ptrs", ctypes.c_void_p), ("B_ptrs", ctypes.c_void_p), ("Y", ctypes.c_void_p),
                 ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class sgmv_projection_grad_t(ctypes.Structure):
+    _fields_ = [("dW", ctypes.c_void_p), ("dA_ptrs", ctypes.c_void_p), ("dB_ptrs", ctypes.c_void_p)]
 
 
 _lib = None
@@ -114,6 +122,12 @@ def load_library(path: str = LIB_PATH):
     lib.sgmv_lora_apply_noalloc.argtypes = [prob, P, P, P, P, P, P, P]
     lib.sgmv_base_lora_apply_partial.argtypes = [prob, P, P, I32, P, P, P, P, P, P, SZ, P]
     lib.sgmv_lora_apply_host_meta.argtypes = [prob, P, P, P, P, P, P, P, SZ, P]
+    proj, grad = ctypes.POINTER(sgmv_projection_t), ctypes.POINTER(sgmv_projection_grad_t)
+    lib.sgmv_layer_workspace_bytes.argtypes = [prob, I32, ctypes.POINTER(SZ)]
+    lib.sgmv_dense_lora_apply.argtypes = [prob, P, P, proj, P, P, P, SZ, P]
+    lib.sgmv_gated_lora_apply.argtypes = [prob, P, P, P, proj, proj, I32, P, P, P, P, SZ, P]
+    lib.sgmv_dense_lora_backward.argtypes = [prob, P, P, proj, P, P, grad, I32, P, P, P, SZ, P]
+    lib.sgmv_gated_lora_backward.argtypes = [prob, P, P, P, proj, proj, I32, P, P, grad, grad, I32, P, P, P, SZ, P]
     for name in ENTRY_POINTS[1:]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -421,6 +435,117 @@ def sgmv_base_lora_apply_packed(problem, X, Wp, A_ptrs, B_ptrs, Y, seg_indptr, l
     """sgmv_base_lora_apply with Wp, the packed copy of W, in place of W."""
     _base_apply("sgmv_base_lora_apply_packed", problem, X, Wp, A_ptrs, B_ptrs, Y, seg_indptr, lora_idx, ws,
                 stream)
+
+
+# ------------------------------------------------- whole layers of any number of rows
+
+def sgmv_layer_workspace_bytes(problem: sgmv_problem_t, op: int) -> int:
+    """Workspace bytes of one of the layer entry points; ``op`` is SGMV_DENSE_FORWARD, _BACKWARD,
+    SGMV_GATED_FORWARD or _BACKWARD."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().sgmv_layer_workspace_bytes(ctypes.byref(problem), int(op), ctypes.byref(out)),
+           "sgmv_layer_workspace_bytes")
+    return int(out.value)
+
+
+def new_layer_workspace(problem: sgmv_problem_t, op: int, device="cuda"):
+    """Device workspace of sgmv_layer_workspace_bytes(problem, op) bytes (any contents will do)."""
+    import torch
+    return torch.empty(sgmv_layer_workspace_bytes(problem, op), dtype=torch.uint8, device=device)
+
+
+def _need_shape(t, name, shape):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _layer_inputs(problem, X, weights, seg_indptr, lora_idx, ws, others=()):
+    """Checks what every layer call takes; ``others``: (tensor or None, name, width) in the problem's format."""
+    import torch
+    dt, n = _torch_dtype(problem), problem.n_rows
+    _need(X, "X", dt); _need_shape(X, "X", (n, problem.h_in))
+    for W, name in weights:
+        _need(W, name, dt); _need_shape(W, name, (problem.h_in, problem.h_out))
+    for t, name, width in others:
+        _need(t, name, dt); _need_shape(t, name, (n, width))
+    _need(seg_indptr, "seg_indptr", torch.int32); _need(lora_idx, "lora_idx", torch.int32)
+    _need(ws, "ws")
+
+
+def _layer_projection(problem, pj, name):
+    import torch
+    A_ptrs, B_ptrs, Y, ranks, scales = (tuple(pj) + (None,) * 5)[:5]
+    _need(A_ptrs, f"{name} A_ptrs", torch.int64); _need(B_ptrs, f"{name} B_ptrs", torch.int64)
+    _need(Y, f"{name} Y", _torch_dtype(problem)); _need_shape(Y, f"{name} Y", (problem.n_rows, problem.h_out))
+    _need(ranks, f"{name} ranks", torch.int32); _need(scales, f"{name} scales", torch.float32)
+    return sgmv_projection_t(_ptr(A_ptrs), _ptr(B_ptrs), _ptr(Y), _ptr(ranks), _ptr(scales))
+
+
+def _layer_grad(problem, grad, name):
+    import torch
+    dW, dA_ptrs, dB_ptrs = (tuple(grad) + (None,) * 3)[:3] if grad is not None else (None,) * 3
+    _need(dW, f"{name} dW", _torch_dtype(problem)); _need_shape(dW, f"{name} dW", (problem.h_in, problem.h_out))
+    _need(dA_ptrs, f"{name} dA_ptrs", torch.int64); _need(dB_ptrs, f"{name} dB_ptrs", torch.int64)
+    return sgmv_projection_grad_t(_ptr(dW), _ptr(dA_ptrs), _ptr(dB_ptrs))
+
+
+def _ws_bytes(ws):
+    return ws.numel() * ws.element_size() if ws is not None else 0
+
+
+def sgmv_dense_lora_apply(problem, X, W, proj, seg_indptr, lora_idx, ws, stream=None):
+    """Y[i] = X[i] @ W + s_k * (X[i] @ A_k) @ B_k for any number of rows (Y written, rounded once);
+    asynchronous.  `proj` is (A_ptrs, B_ptrs, Y) or (A_ptrs, B_ptrs, Y, ranks, scales), as in
+    sgmv_lora_apply_batched; `ws` from new_layer_workspace(problem, SGMV_DENSE_FORWARD)."""
+    _layer_inputs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws)
+    pj = _layer_projection(problem, proj, "proj")
+    st = load_library().sgmv_dense_lora_apply(ctypes.byref(problem), _ptr(X), _ptr(W), ctypes.byref(pj),
+                                              _ptr(seg_indptr), _ptr(lora_idx), _ptr(ws), _ws_bytes(ws),
+                                              _stream(stream))
+    _check(st, "sgmv_dense_lora_apply")
+
+
+def sgmv_gated_lora_apply(problem, X, Wg, Wu, gate, up, H, seg_indptr, lora_idx, ws, act=SGMV_ACT_SILU, stream=None):
+    """H[i] = act(G[i]) * U[i], G and U the outputs of two projections of X with their LoRA terms;
+    asynchronous.  `gate` and `up` are projections as in sgmv_dense_lora_apply whose Y is where to
+    store G and U (what sgmv_gated_lora_backward reads), or None; `ws` from
+    new_layer_workspace(problem, SGMV_GATED_FORWARD)."""
+    _layer_inputs(problem, X, [(Wg, "Wg"), (Wu, "Wu")], seg_indptr, lora_idx, ws, [(H, "H", problem.h_out)])
+    g, u = _layer_projection(problem, gate, "gate"), _layer_projection(problem, up, "up")
+    st = load_library().sgmv_gated_lora_apply(ctypes.byref(problem), _ptr(X), _ptr(Wg), _ptr(Wu), ctypes.byref(g),
+                                              ctypes.byref(u), int(act), _ptr(H), _ptr(seg_indptr), _ptr(lora_idx),
+                                              _ptr(ws), _ws_bytes(ws), _stream(stream))
+    _check(st, "sgmv_gated_lora_apply")
+
+
+def sgmv_dense_lora_backward(problem, X, W, proj, dY, seg_indptr, lora_idx, ws, dX=None, grad=None, accumulate=False,
+                             stream=None):
+    """Gradients of sgmv_dense_lora_apply from dY: dX (written), and `grad` = (dW, dA_ptrs, dB_ptrs), each or
+    None; accumulate adds dW, dA and dB to what is there, else they are written (zero for a LoRA without rows).
+    `ws` from new_layer_workspace(problem, SGMV_DENSE_BACKWARD).  Asynchronous."""
+    _layer_inputs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws,
+                  [(dY, "dY", problem.h_out), (dX, "dX", problem.h_in)])
+    pj, g = _layer_projection(problem, proj, "proj"), _layer_grad(problem, grad, "grad")
+    st = load_library().sgmv_dense_lora_backward(ctypes.byref(problem), _ptr(X), _ptr(W), ctypes.byref(pj), _ptr(dY),
+                                                 _ptr(dX), ctypes.byref(g), int(accumulate), _ptr(seg_indptr),
+                                                 _ptr(lora_idx), _ptr(ws), _ws_bytes(ws), _stream(stream))
+    _check(st, "sgmv_dense_lora_backward")
+
+
+def sgmv_gated_lora_backward(problem, X, Wg, Wu, gate, up, dH, seg_indptr, lora_idx, ws, dX=None, gate_grad=None,
+                             up_grad=None, accumulate=False, act=SGMV_ACT_SILU, stream=None):
+    """Gradients of sgmv_gated_lora_apply from dH and the stored G and U (the Y of `gate` and `up`): dX (written),
+    and per projection (dW, dA_ptrs, dB_ptrs), each or None, accumulated or written as in
+    sgmv_dense_lora_backward.  `ws` from new_layer_workspace(problem, SGMV_GATED_BACKWARD).  Asynchronous."""
+    _layer_inputs(problem, X, [(Wg, "Wg"), (Wu, "Wu")], seg_indptr, lora_idx, ws,
+                  [(dH, "dH", problem.h_out), (dX, "dX", problem.h_in)])
+    g, u = _layer_projection(problem, gate, "gate"), _layer_projection(problem, up, "up")
+    gg, ug = _layer_grad(problem, gate_grad, "gate_grad"), _layer_grad(problem, up_grad, "up_grad")
+    st = load_library().sgmv_gated_lora_backward(ctypes.byref(problem), _ptr(X), _ptr(Wg), _ptr(Wu), ctypes.byref(g),
+                                                 ctypes.byref(u), int(act), _ptr(dH), _ptr(dX), ctypes.byref(gg),
+                                                 ctypes.byref(ug), int(accumulate), _ptr(seg_indptr), _ptr(lora_idx),
+                                                 _ptr(ws), _ws_bytes(ws), _stream(stream))
+    _check(st, "sgmv_gated_lora_backward")
 
 
 def batched_workspace_bytes(problem: sgmv_problem_t, num_projections: int) -> int:

@@ -1,0 +1,567 @@
+// sgmv_dense.hip - dense products of a layer with the LoRA term (gfx950), for
+// any number of rows.
+//
+// The LoRA paragraph of the Punica README (page "Punica：多 LoRA 模型统一服务框架")
+// gives a row x the output x@W + x@A@B.  Four products share one kernel:
+//     forward  Y  = X @ W + V @ B_k                       V = s_k X @ A_k
+//     gated    G, U = two forwards, H = act(G) * U
+//     dX       dX = sum_p (dY_p @ W_p^T + V_p @ A_{p,k}^T) V_p = s_k dY_p @ B_{p,k}^T
+//     dW       dW_p = X^T @ dY_p
+// A workgroup owns one output tile and walks the contraction in steps of 64.
+// Both operand tiles go from memory straight into LDS (no registers), one ring
+// slot per step; lanes past the matrix ask for an offset beyond the buffer
+// descriptor and get zeros.  An operand whose contraction index is contiguous
+// in memory is kept row by row, its 16-byte groups at group ^ (row & 7), and read
+// with 128-bit reads.  An operand stored the other way round (W in the forward,
+// both in dW) is kept as it lies and read with the transposing 64-bit read:
+// the four rows that one 16-lane group reads lie in different banks, because
+// group g of row k is stored at g ^ f(k).  Tiles multiply as D^T = B^T A^T, so that
+// a lane ends up with four consecutive columns of one row.
+// The LoRA term joins in the epilogue: per run of rows that share a LoRA, V
+// (fp32, split into hi + lo 16-bit halves) times E_k on the matrix cores, added
+// to the accumulators in fp32; outputs are rounded once.
+#include "sgmv_layer_ops.h"
+
+namespace sgmv {
+namespace {
+
+constexpr int kXcds = 8;
+constexpr int kGroupRows = 8;  // row tiles that walk the columns together (they share W tiles in an XCD's L2)
+
+template <int N>
+__device__ inline void wait_loads_and_lds() {
+  // All but the N newest of this wave's loads have landed, and its LDS reads are
+  // done (the slot they read is refilled after the barrier that follows).
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
+}
+
+template <int MODE, int BM_, int BN_, int WM_, int WN_, int STAGES_>
+struct DenseShape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
+  static constexpr int NW = WM * WN;                  // waves
+  static constexpr int TM = BM / WM / 16;             // 16-row tiles per wave
+  static constexpr int TN = BN / WN / 16;             // 16-column tiles per wave
+  static constexpr bool GATED = MODE == kDenseGated;
+  static constexpr bool A_T = MODE == kDenseDw;       // stored with the contraction index as row
+  static constexpr bool B_T = MODE != kDenseDx;
+  static constexpr int NB = GATED ? 2 : 1;            // column sub-tiles (gate, up)
+  static constexpr int C = BN / NB;                   // columns of one sub-tile
+  static constexpr int LA = BM / 8 / NW;              // 1 KiB loads per wave and step
+  static constexpr int LB = BN / 8 / NW;
+  static constexpr int TNP = TN / NB;                 // 16-column tiles of one projection per wave
+  static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN, "tile loads split evenly over the waves");
+  static_assert(TM * 16 * WM == BM && TNP * NB * 16 * WN == BN, "tile splits evenly over the waves");
+};
+
+// Column swizzle of a tile stored [k][cols]: f(k) of the kernel's header comment, in
+// 16-byte groups, for rows of at least 16 (or 8) groups.
+template <int COLS>
+__device__ inline int swizzle_k(int k) {
+  return (((k & 3) | ((k >> 1) & 4)) << 1) & (COLS / 8 - 1);
+}
+
+// One operand tile of R rows (or columns) x 64 contraction steps.
+template <int R, int LOADS, int NW, bool T>
+struct TileLoader {
+  uint32_t voff[LOADS];
+  __device__ inline void init(int wave, int lane, int ld) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int L = wave * LOADS + j;  // 1 KiB piece of the tile
+      if constexpr (T) {
+        constexpr int G = R / 8;  // 16-byte groups per k row
+        const int k = L * (64 / G) + lane / G;
+        const int g = (lane % G) ^ swizzle_k<R>(k);
+        voff[j] = (uint32_t)(k * ld + g * 8) * 2u;
+      } else {
+        const int r = L * 8 + (lane >> 3);
+        const int g = (lane & 7) ^ (r & 7);
+        voff[j] = (uint32_t)(r * ld + g * 8) * 2u;
+      }
+    }
+  }
+  // base: the operand; r0: first row (column) of the tile, rows: how many the
+  // matrix has; k0: first contraction index of the step, K: how many there are.
+  __device__ inline void issue(const uint16_t* base, int ld, int r0, int rows, int k0, int K, uint16_t* lds, int wave,
+                               int lane) const {
+    lds += wave * LOADS * 512;
+    if constexpr (T) {
+      const int kv = K - k0 < kDenseK ? K - k0 : kDenseK;
+      const uint32_t bytes = kv > 0 ? (uint32_t)((kv - 1) * ld + (rows - r0)) * 2u : 0u;
+      const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)k0 * ld + r0), 0,
+                                                        (int)bytes, kRawBuffer);
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + j * 512), 16, (int)voff[j], 0, 0, 0);
+    } else {
+      const int rv = rows - r0 < R ? rows - r0 : R;
+      const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)r0 * ld), 0,
+                                                        rv * ld * 2, kRawBuffer);
+      if (k0 + kDenseK <= K) {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + j * 512), 16, (int)voff[j], k0 * 2, 0, 0);
+      } else {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+          const int g = (lane & 7) ^ (lane >> 3);  // 8 rows per piece: row & 7 == lane / 8
+          const uint32_t off = k0 + g * 8 < K ? voff[j] : kOutOfRange;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + j * 512), 16, (int)off, k0 * 2, 0, 0);
+        }
+      }
+    }
+  }
+};
+
+// Operand of 16 rows (columns) x 32 contraction steps at kk (0, 1) of an LDS tile.
+template <int R, bool T>
+struct FragReader {
+  // tile: first row / column of the fragment inside the tile (a multiple of 16)
+  __device__ static inline u32x4 read(const uint16_t* lds, int tile, int kk, int lane) {
+    const int q = lane >> 4, i = lane & 15;
+    if constexpr (T) {
+      const int k = kk * 32 + q * 8 + (i >> 2);
+      const int g = (tile / 8 + ((i & 3) >> 1)) ^ swizzle_k<R>(k);
+      const uint16_t* a = lds + k * R + g * 8 + (i & 1) * 4;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)a);
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(a + 4 * R));  // same swizzle: k + 4
+      const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
+      return u32x4{l[0], l[1], h[0], h[1]};
+    } else {
+      return load_vec(lds + (tile + i) * 64 + (((kk * 4 + q) ^ (i & 7)) << 3));
+    }
+  }
+};
+
+// Adds the LoRA term of projection `t` to the accumulators acc[0..TM)[J0..J0+TNP)
+// of a wave's rows [m0, m0 + 16 TM) and columns c0 + 16 j.
+template <class T, int MODE, int TM, int TN, int J0, int TNP>
+__device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x4 (&acc)[TM][TN], int m0, int c0) {
+  const int lane = threadIdx.x & 63;
+  const int q = lane >> 4, ml = lane & 15;
+  const SegMeta& sm = p.meta;
+  if (t.V == nullptr || sm.num_segs <= 0) return;
+  const int mend = m0 + 16 * TM < p.M ? m0 + 16 * TM : p.M;
+  const int R = p.rank;
+  const int steps = R > 32 ? 2 : 1;
+  for (int s0 = first_segment_past(sm, m0); s0 < sm.num_segs; s0 += 64) {
+    // Metadata of 64 segments at a time, one per lane.
+    const int sl = s0 + lane < sm.num_segs ? s0 + lane : sm.num_segs - 1;
+    const int lo_l = sm.seg_indptr[sl], hi_l = sm.seg_indptr[sl + 1];
+    int k_l = sm.lora_idx[sl];
+    if (k_l < 0 || k_l >= sm.num_loras) k_l = -1;
+    const uint64_t e_l = k_l >= 0 ? t.ptrs[k_l] : 0ull;
+    const int r_l = k_l >= 0 ? rank_of(t.ranks, R, k_l) : 0;
+    const int ns = sm.num_segs - s0 < 64 ? sm.num_segs - s0 : 64;
+    for (int u = 0; u < ns; ++u) {
+      const int lo = __builtin_amdgcn_readlane(lo_l, u), hi_s = __builtin_amdgcn_readlane(hi_l, u);
+      if (lo >= mend) return;
+      const int r0 = lo > m0 ? lo : m0, r1 = hi_s < mend ? hi_s : mend;
+      const int rk = __builtin_amdgcn_readlane(r_l, u);
+      const uint32_t e_lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e_l, u);
+      const uint32_t e_hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(e_l >> 32), u);
+      const uint16_t* E = reinterpret_cast<const uint16_t*>(((uint64_t)e_hi << 32) | e_lo);
+      if (r1 <= r0 || rk <= 0 || E == nullptr) continue;
+      // E_k operands of the wave's columns: lane holds E[32 s + 8 q + e][c0 + 16 j + ml].
+      u32x4 ef[2][TNP];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int j = 0; j < TNP; ++j) {
+          ef[s][j] = u32x4{0u, 0u, 0u, 0u};
+          const int c = c0 + 16 * j + ml, r = 32 * s + 8 * q;
+          if (s < steps && r < rk && c < p.N) {
+            if constexpr (MODE == kDenseDx) {
+              ef[s][j] = load_vec(E + (int64_t)c * rk + r);
+            } else {
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t a = ((global_u16_ptr)E)[(int64_t)(r + 2 * w) * p.N + c];
+                const uint32_t b = ((global_u16_ptr)E)[(int64_t)(r + 2 * w + 1) * p.N + c];
+                ef[s][j][w] = a | (b << 16);
+              }
+            }
+          }
+        }
+#pragma unroll
+      for (int mi = 0; mi < TM; ++mi) {
+        const int mb = m0 + 16 * mi;
+        if (mb + 16 <= r0 || mb >= r1) continue;
+        const int row = mb + ml;
+        const bool in = row >= r0 && row < r1;
+        float v[2][8];
+        float big = 0.f;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const bool ok = in && s < steps && 32 * s + 8 * q < rk;
+          const float* vp = t.V + (ok ? (int64_t)row * R + 32 * s + 8 * q : 0);
+          const f32x4 a = *reinterpret_cast<const f32x4*>(vp), b = *reinterpret_cast<const f32x4*>(vp + 4);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[s][e] = ok ? a[e] : 0.f;
+            v[s][4 + e] = ok ? b[e] : 0.f;
+            big = fmaxf(big, fmaxf(fabsf(v[s][e]), fabsf(v[s][4 + e])));
+          }
+        }
+        // fp16 halves hold V only below 65504: a row beyond 32768 goes through the
+        // matrix cores scaled down by a power of two (exact) and back up.
+        float up = 1.f;
+        if constexpr (T::kMaxFinite < 1e6f) {
+          big = fmaxf(big, shfl_xor(big, 16));
+          big = fmaxf(big, shfl_xor(big, 32));
+          if (big > 32768.f && big < 3.4e38f) {
+            const int e = ((int)(__float_as_uint(big) >> 23) & 255) - 127 - 14;  // 1 .. 113
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+            up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int e8 = 0; e8 < 8; ++e8) v[s][e8] *= down;
+          }
+        }
+        u32x4 vh[2], vl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) split8<T>(v[s], vh[s], vl[s]);
+#pragma unroll
+        for (int j = 0; j < TNP; ++j) {
+          f32x4 d = {0.f, 0.f, 0.f, 0.f};
+          d = mfma<T>(ef[0][j], vl[0], d);
+          d = mfma<T>(ef[0][j], vh[0], d);
+          if (steps > 1) {
+            d = mfma<T>(ef[1][j], vl[1], d);
+            d = mfma<T>(ef[1][j], vh[1], d);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            acc[mi][J0 + j][i] = in ? __builtin_fmaf(d[i], up, acc[mi][J0 + j][i]) : acc[mi][J0 + j][i];
+        }
+      }
+    }
+  }
+}
+
+template <class T>
+__device__ inline u32x2 round4(const f32x4& v) {
+  return u32x2{(uint32_t)T::round(v[0]) | ((uint32_t)T::round(v[1]) << 16),
+               (uint32_t)T::round(v[2]) | ((uint32_t)T::round(v[3]) << 16)};
+}
+
+template <class T, int MODE, class S>
+__global__ __launch_bounds__(S::NW * 64, 2) void sgmv_dense_kernel(DenseParams p) {
+  constexpr int STAGES = S::STAGES, TM = S::TM, TN = S::TN, TNP = S::TNP;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds_a[STAGES][S::BM * kDenseK];
+  __shared__ __attribute__((aligned(1024))) uint16_t lds_b[STAGES][S::BN * kDenseK];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int q = lane >> 4, ml = lane & 15;
+
+  // Tile of this workgroup: workgroup b runs on XCD b % 8; each XCD takes a
+  // contiguous run of the tile order, in which kGroupRows row tiles walk the
+  // columns together.
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int total = tiles * p.ksplit;
+  const int per_xcd = (total + kXcds - 1) / kXcds;
+  const int idx = ((int)blockIdx.x % kXcds) * per_xcd + (int)blockIdx.x / kXcds;
+  if (idx >= total || (int)blockIdx.x / kXcds >= per_xcd) return;
+  const int g = idx / tiles;
+  const int t = idx - g * tiles;
+  const int group = t / (kGroupRows * p.tiles_n);
+  const int gr = p.tiles_m - group * kGroupRows < kGroupRows ? p.tiles_m - group * kGroupRows : kGroupRows;
+  const int in_group = t - group * kGroupRows * p.tiles_n;
+  const int m0 = (group * kGroupRows + in_group % gr) * S::BM;
+  const int n0 = (in_group / gr) * S::C;
+  const int proj = MODE == kDenseDw ? (int)blockIdx.y : 0;
+
+  // Steps of the contraction: all of pair 0, then all of pair 1.
+  const int kt = (p.K + kDenseK - 1) / kDenseK;
+  const int steps_all = kt * (MODE == kDenseDx ? p.pairs : 1);
+  const int first = g * p.ktiles_per_split;
+  const int last = first + p.ktiles_per_split < steps_all ? first + p.ktiles_per_split : steps_all;
+
+  TileLoader<S::BM, S::LA, S::NW, S::A_T> la;
+  // A gated tile's columns are two sub-tiles; each wave loads pieces of one of them.
+  TileLoader<S::C, S::LB, S::NW / S::NB, S::B_T> lb;
+  constexpr int WB = S::NW / S::NB;  // waves that load one sub-tile
+  const int sub = wave / WB;
+  la.init(wave, lane, p.lda);
+  lb.init(wave - sub * WB, lane, p.ldb);
+
+  auto issue = [&](int step, int slot) {
+    // Past the end nothing is wanted: K = k0 leaves every lane out of range.
+    const int s = step < last ? step : last - 1;
+    const int pair = MODE == kDenseDx && s >= kt ? 1 : 0;
+    const int k0 = (s - pair * kt) * kDenseK;
+    const int bi = MODE == kDenseDw ? proj : S::GATED ? sub : pair;
+    const uint16_t* A = MODE == kDenseDx && pair ? p.A[1] : p.A[0];
+    const uint16_t* B = bi ? p.B[1] : p.B[0];
+    la.issue(A, p.lda, m0, p.M, k0, p.K, lds_a[slot], wave, lane);
+    lb.issue(B, p.ldb, n0, p.N, k0, p.K, lds_b[slot] + sub * S::C * kDenseK, wave - sub * WB, lane);
+  };
+
+  f32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto compute = [&](int slot) {
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      u32x4 bf[TN];
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int sb = j / TNP;  // sub-tile
+        bf[j] = FragReader<S::C, S::B_T>::read(lds_b[slot] + sb * S::C * kDenseK, (wn * TNP + j % TNP) * 16, kk, lane);
+      }
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        const u32x4 af = FragReader<S::BM, S::A_T>::read(lds_a[slot], (wm * TM + i) * 16, kk, lane);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(bf[j], af, acc[i][j]);
+      }
+    }
+  };
+
+  if (last > first) {
+    constexpr int kPerStep = S::LA + S::LB;  // loads of one wave per step
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) issue(first + s, s);
+    // A step past the end refills its slot with the last step again (its
+    // product is skipped): every wave keeps the same count of loads in flight.
+    for (int step = first; step < last; step += STAGES) {
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) {
+        if (s > 0 && step + s >= last) break;
+        wait_loads_and_lds<kPerStep*(STAGES - 2)>();
+        __builtin_amdgcn_s_barrier();
+        issue(step + s + STAGES - 1, (s + STAGES - 1) % STAGES);
+        compute(s);
+      }
+    }
+    wait_loads_and_lds<0>();  // no load may be in flight when the workgroup ends
+  }
+
+  // Epilogue.  acc[i][j][e]: row m0 + (wm TM + i) 16 + ml, column 16-tile j, 4 q + e.
+  const int mw = m0 + wm * TM * 16;
+  const int cw = n0 + wn * TNP * 16;
+  if (MODE != kDenseDw && p.term_in_tile && g == 0) {
+    // Two column tiles at a time: four of E_k's operands would not fit the
+    // registers beside a 256 x 256 tile's accumulators.
+    if constexpr (S::GATED) {
+      add_term<T, MODE, TM, TN, 0, TNP>(p, p.term[0], acc, mw, cw);
+      add_term<T, MODE, TM, TN, TNP, TNP>(p, p.term[1], acc, mw, cw);
+    } else {
+      constexpr int J = TN < 2 ? TN : 2;
+      for (int t = 0; t < (MODE == kDenseDx ? p.pairs : 1); ++t) {
+        add_term<T, MODE, TM, TN, 0, J>(p, t ? p.term[1] : p.term[0], acc, mw, cw);
+        if constexpr (TN > 2) add_term<T, MODE, TM, TN, 2, 2>(p, t ? p.term[1] : p.term[0], acc, mw, cw + 32);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = mw + i * 16 + ml;
+#pragma unroll
+    for (int j = 0; j < TNP; ++j) {
+      const int c = cw + j * 16 + q * 4;
+      if (m >= p.M || c >= p.N) continue;
+      const int64_t o = (int64_t)m * p.N + c;
+      if (p.to_planes) {
+        const int64_t pl = (int64_t)(proj * p.ksplit + g) * p.plane_stride + o;
+        *reinterpret_cast<f32x4*>(p.planes + pl) = acc[i][j];
+        if constexpr (S::GATED)
+          *reinterpret_cast<f32x4*>(p.planes + pl + (int64_t)p.ksplit * p.plane_stride) = acc[i][TNP + j];
+      } else if constexpr (S::GATED) {
+        const f32x4 gv = acc[i][j], uv = acc[i][TNP + j];
+        f32x4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) h[e] = act_value(p.act, gv[e]) * uv[e];
+        if (p.out[0]) *reinterpret_cast<u32x2*>(p.out[0] + o) = round4<T>(gv);
+        if (p.out[1]) *reinterpret_cast<u32x2*>(p.out[1] + o) = round4<T>(uv);
+        *reinterpret_cast<u32x2*>(p.out[2] + o) = round4<T>(h);
+      } else {
+        f32x4 v = acc[i][j];
+        uint16_t* dst = (MODE == kDenseDw && proj ? p.out[1] : p.out[0]);
+        if (MODE == kDenseDw && p.accumulate) {
+          const u32x2 old = *reinterpret_cast<const u32x2*>(dst + o);
+          v[0] += T::lo(old[0]);
+          v[1] += T::hi(old[0]);
+          v[2] += T::lo(old[1]);
+          v[3] += T::hi(old[1]);
+        }
+        *reinterpret_cast<u32x2*>(dst + o) = round4<T>(v);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- epilogue of the partial planes
+// One wave per (row i, 512 columns): lane l owns columns c .. c+7.  Sums the
+// planes in plane order; when the tiles did not add the LoRA term, adds
+// V[i] @ E_k with vector FMA in fp32 (short segments: a row brings its own E_k).
+template <class T, int MODE>
+__device__ inline void plane_sum(const DenseParams& p, int proj, int64_t o, float (&y)[8]) {
+  constexpr int kBatch = 4;
+  const float* src = p.planes + (int64_t)proj * p.ksplit * p.plane_stride + o;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = 0.f;
+  for (int g0 = 0; g0 < p.ksplit; g0 += kBatch) {
+    f32x4 a[kBatch], b[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t g = g0 + u < p.ksplit ? g0 + u : p.ksplit - 1;
+      a[u] = *reinterpret_cast<const f32x4*>(src + g * p.plane_stride);
+      b[u] = *reinterpret_cast<const f32x4*>(src + g * p.plane_stride + 4);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const bool live = g0 + u < p.ksplit;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[e] = live ? y[e] + a[u][e] : y[e];
+        y[4 + e] = live ? y[4 + e] + b[u][e] : y[4 + e];
+      }
+    }
+  }
+}
+
+template <class T, int MODE>
+__device__ inline void row_term(const DenseParams& p, const LowRankTerm& t, int i, int k, int c, float (&y)[8]) {
+  const uint16_t* E = reinterpret_cast<const uint16_t*>(t.ptrs[k]);
+  const int rk = rank_of(t.ranks, p.rank, k);
+  if (E == nullptr) return;
+  const float* v = t.V + (int64_t)i * p.rank;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if constexpr (MODE == kDenseDx) {
+    for (int j = 0; j < rk; j += 8) {  // A_k [N, r_k]: eight columns' ranks j .. j+7
+      u32x4 a[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[e] = load_stream(E + (int64_t)(c + e) * rk + j);
+      const f32x4 v0 = *reinterpret_cast<const f32x4*>(v + j), v1 = *reinterpret_cast<const f32x4*>(v + j + 4);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float f[8];
+        unpack8<T>(a[e], f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          s[e] = __builtin_fmaf(v0[w], f[w], s[e]);
+          s[e] = __builtin_fmaf(v1[w], f[4 + w], s[e]);
+        }
+      }
+    }
+  } else {
+    for (int j = 0; j < rk; j += 8) {  // B_k [r_k, N]
+      u32x4 b[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) b[w] = load_stream(E + (int64_t)(j + w) * p.N + c);
+      const f32x4 v0 = *reinterpret_cast<const f32x4*>(v + j), v1 = *reinterpret_cast<const f32x4*>(v + j + 4);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        float f[8];
+        unpack8<T>(b[w], f);
+        const float vj = w < 4 ? v0[w & 3] : v1[w & 3];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(vj, f[e], s[e]);
+      }
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] += s[e];
+}
+
+template <class T, int MODE>
+__global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) {
+  const int lane = threadIdx.x;
+  const int i = blockIdx.x;
+  const int c = blockIdx.y * 512 + lane * 8;
+  if (i >= p.M) return;
+  int k = -1;
+  if (!p.term_in_tile && p.meta.num_segs > 0) {
+    const int s = first_segment_past(p.meta, i);
+    if (s < p.meta.num_segs && p.meta.seg_indptr[s] <= i) k = p.meta.lora_idx[s];
+    if (k >= p.meta.num_loras) k = -1;
+  }
+  if (c >= p.N) return;
+  const int64_t o = (int64_t)i * p.N + c;
+  float y[8];
+  plane_sum<T, MODE>(p, 0, o, y);
+  if (k >= 0 && p.term[0].V != nullptr) row_term<T, MODE>(p, p.term[0], i, k, c, y);
+  if constexpr (MODE == kDenseGated) {
+    float u[8], h[8];
+    plane_sum<T, MODE>(p, 1, o, u);
+    if (k >= 0 && p.term[1].V != nullptr) row_term<T, MODE>(p, p.term[1], i, k, c, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = act_value(p.act, y[e]) * u[e];
+    if (p.out[0]) store_vec(p.out[0] + o, pack8<T>(y));
+    if (p.out[1]) store_vec(p.out[1] + o, pack8<T>(u));
+    store_vec(p.out[2] + o, pack8<T>(h));
+  } else {
+    if constexpr (MODE == kDenseDx) {
+      if (k >= 0 && p.pairs > 1 && p.term[1].V != nullptr) row_term<T, MODE>(p, p.term[1], i, k, c, y);
+    }
+    store_vec(p.out[0] + o, pack8<T>(y));
+  }
+}
+
+template <class T, int MODE, int BM, int BN, int WM, int WN, int STAGES>
+hipError_t launch_tile(const DenseParams& p, hipStream_t s) {
+  using S = DenseShape<MODE, BM, BN, WM, WN, STAGES>;
+  const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.ksplit;
+  const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
+  if (grid <= 0 || grid > 0x7fffffff || p.ktiles_per_split < 0) return hipErrorInvalidValue;
+  const unsigned gy = MODE == kDenseDw ? (unsigned)p.projections : 1u;
+  hipLaunchKernelGGL((sgmv_dense_kernel<T, MODE, S>), dim3((unsigned)grid, gy), dim3(S::NW * 64), 0, s, p);
+  return hipGetLastError();
+}
+
+template <class T, int MODE>
+hipError_t launch_mode(int cfg, const DenseParams& p, hipStream_t s) {
+  switch (cfg) {
+    case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 2>(p, s);
+    case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 2>(p, s);
+    case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 3>(p, s);
+    case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 3>(p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <class T>
+hipError_t launch_t(int mode, int cfg, const DenseParams& p, hipStream_t s) {
+  switch (mode) {
+    case kDenseForward: return launch_mode<T, kDenseForward>(cfg, p, s);
+    case kDenseGated: return launch_mode<T, kDenseGated>(cfg, p, s);
+    case kDenseDx: return launch_mode<T, kDenseDx>(cfg, p, s);
+    case kDenseDw:
+      return cfg == kTile256 ? launch_tile<T, kDenseDw, 256, 256, 2, 4, 2>(p, s)
+                             : launch_tile<T, kDenseDw, 128, 128, 2, 2, 2>(p, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+template <class T>
+hipError_t launch_epilogue_t(int mode, const DenseParams& p, hipStream_t s) {
+  const dim3 grid((unsigned)p.M, (unsigned)((p.N + 511) / 512));
+  switch (mode) {
+    case kDenseForward: hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, kDenseForward>), grid, dim3(64), 0, s, p); break;
+    case kDenseGated: hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, kDenseGated>), grid, dim3(64), 0, s, p); break;
+    case kDenseDx: hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, kDenseDx>), grid, dim3(64), 0, s, p); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_dense(int dtype, int mode, int cfg, const DenseParams& p, hipStream_t stream) {
+  if (p.M <= 0 || p.N <= 0) return hipSuccess;
+  return dtype == 1 ? launch_t<BF16>(mode, cfg, p, stream) : launch_t<F16>(mode, cfg, p, stream);
+}
+
+hipError_t launch_dense_epilogue(int dtype, int mode, const DenseParams& p, hipStream_t stream) {
+  if (p.M <= 0 || p.N <= 0) return hipSuccess;
+  return dtype == 1 ? launch_epilogue_t<BF16>(mode, p, stream) : launch_epilogue_t<F16>(mode, p, stream);
+}
+
+}  // namespace sgmv

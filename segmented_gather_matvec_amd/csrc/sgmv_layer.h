@@ -1,0 +1,102 @@
+// sgmv_layer.h - host-side interface of the layer kernels (sgmv_dense.hip,
+// sgmv_lowrank.hip): a shared projection of any number of rows with the LoRA
+// term, the gated feed-forward block made of two of them, and their gradients.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "sgmv_layer_shapes.h"
+
+namespace sgmv {
+
+// Segment metadata shared by the layer kernels (device arrays, as elsewhere).
+struct SegMeta {
+  const int32_t* seg_indptr;
+  const int32_t* lora_idx;
+  int32_t num_segs;   // 0: no LoRA term
+  int32_t num_loras;
+  int32_t n_rows;
+};
+
+// The LoRA side of one projection as a product's epilogue reads it:
+//   out[i, c] += sum_j V[i, j] * E_k[j, c]
+// forward: V = s_k X @ A_k, E_k = B_k; dX: V = s_k dY @ B_k^T, E_k = A_k^T.
+struct LowRankTerm {
+  const float* V;          // [n_rows][rank] fp32 (null: no term)
+  const uint64_t* ptrs;    // [num_loras] -> B_k [r_k, N], or A_k [N, r_k] for dX
+  const int32_t* ranks;    // null, or rank of each LoRA
+};
+
+enum DenseMode : int {
+  kDenseForward = 0,  // Y = X @ W + term                  A: X, B[0]: W
+  kDenseGated = 1,    // G, U two forwards, H = act(G) * U A: X, B[0], B[1]: Wg, Wu
+  kDenseDx = 2,       // dX = sum_p dY_p @ W_p^T + terms    A[p]: dY_p, B[p]: W_p
+  kDenseDw = 3        // dW_p = X^T @ dY_p                  A[0]: X, B[p]: dY_p, p = blockIdx.y
+};
+
+struct DenseParams {
+  int32_t M, N, K;       // output rows and columns, contraction length (of one operand pair)
+  int32_t lda, ldb;      // row strides (elements) of the operands as stored
+  int32_t pairs;         // dX: operand pairs summed (1 or 2)
+  int32_t projections;   // dW: projections (grid y)
+  int32_t tiles_m, tiles_n;
+  int32_t ksplit;        // workgroups sharing one output tile
+  int32_t ktiles_per_split;
+  int32_t rank;
+  int32_t act;
+  int32_t accumulate;    // dW: add to what is there
+  int32_t to_planes;     // 1: fp32 partial planes instead of the outputs (ksplit > 1, or a term added by the epilogue kernel)
+  int32_t term_in_tile;  // 1: split 0 of every tile adds the LoRA term
+  int64_t plane_stride;  // floats between planes of one projection's output (M * N)
+  const uint16_t* A[2];
+  const uint16_t* B[2];
+  uint16_t* out[3];      // forward: Y; gated: G, U (both may be null), H; dX: dX; dW: dW_0, dW_1
+  float* planes;         // [projection][ksplit][M][N] (gated: projections g, u)
+  SegMeta meta;
+  LowRankTerm term[2];
+};
+
+// cfg: DenseTile of sgmv_layer_shapes.h.
+hipError_t launch_dense(int dtype, int mode, int cfg, const DenseParams& p, hipStream_t stream);
+// Sums the partial planes, adds the LoRA term when term_in_tile is 0, applies
+// the activation (gated) and writes the outputs.
+hipError_t launch_dense_epilogue(int dtype, int mode, const DenseParams& p, hipStream_t stream);
+
+// Thin products of the LoRA term: V[i, :] = s_k Z[i, :] @ D_k for every covered
+// row, with D_k = A_k ([K, r_k]) or B_k^T (B_k [r_k, K], transposed = 1).
+struct ThinParams {
+  const uint16_t* Z;      // [n_rows, K]
+  const uint64_t* ptrs;
+  const int32_t* ranks;
+  const float* scales;
+  float* V;               // [n_rows][rank]
+  float* planes;          // [ksplit][n_rows][rank] (ksplit > 1)
+  int32_t K, rank, transposed;
+  int32_t units, direct;  // units of <= kThinRows rows of one segment
+  int32_t ksplit, kc;     // K per split, a multiple of 128
+  SegMeta meta;
+};
+// count products on grid y (at most 2); the plane sum follows when ksplit > 1.
+hipError_t launch_thin(int dtype, const ThinParams* p, int count, hipStream_t stream);
+
+// Gradients of the LoRA matrices, out[c, j] = sum_{rows i of LoRA k} Z[i, c] * Q[i, j]
+// stored [C, r_k] (dA_k: Z = X, Q = s_k dY @ B_k^T) or [r_k, C] (dB_k: Z = dY, Q = s_k X @ A_k).
+struct LoraGradParams {
+  const uint16_t* Z;      // [n_rows, C]
+  const float* Q;         // [n_rows][rank]
+  const uint64_t* out;    // [num_loras] -> gradient (0: not wanted)
+  const int32_t* ranks;
+  float* planes;          // [nsplit][num_loras][C][rank] or [nsplit][num_loras][rank][C] (nsplit > 1)
+  int32_t C, rank, rank_major;  // rank_major: stored [r_k, C]
+  int32_t nsplit;
+  int32_t accumulate;
+  SegMeta meta;
+};
+hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipStream_t stream);
+
+// dG = dH * U * act'(G), dU = dH * act(G), rounded once to the 16-bit format.
+hipError_t launch_gate_backward(int dtype, int act, const uint16_t* G, const uint16_t* U, const uint16_t* dH,
+                                uint16_t* dG, uint16_t* dU, int64_t n, hipStream_t stream);
+
+}  // namespace sgmv

@@ -1,0 +1,165 @@
+// sgmv_layer_host.cpp - plans, workspace sizes and checks of the layer entry
+// points.  No HIP calls.
+#include "sgmv_layer_host.h"
+
+#include <algorithm>
+
+namespace sgmv_host {
+
+namespace {
+
+constexpr int64_t kCus = 256;                          // compute units of an MI355X
+constexpr int64_t kGradPlaneBytes = (int64_t)256 << 20;  // most the splits of a LoRA gradient may take
+constexpr int kShortRun = 16;  // rows per segment from which the tiles' matrix cores add the LoRA term
+
+// Workgroups of a tile shape that run at once on one CU (LDS).
+int resident(int cfg) { return cfg == sgmv::kTile256 ? 1 : 2; }
+
+// Microseconds of one contraction step of every workgroup resident on a CU,
+// and the bytes per microsecond that partial planes move at: the model that
+// picks between tile shapes and splits (only their ratios matter).
+double step_us(int cfg) {
+  switch (cfg) {
+    case sgmv::kTile256: return 1.1;
+    case sgmv::kTile128: return 0.75;
+    case sgmv::kTile64: return 0.5;
+    default: return 0.4;
+  }
+}
+constexpr double kPlaneBytesPerUs = 4.0e6;
+
+DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, bool may_split) {
+  // columns_per_n: 2 for a gated tile (gate and up columns side by side).
+  DensePlan best;
+  double best_cost = -1;
+  for (int cfg = sgmv::kTile256; cfg <= sgmv::kTile32; ++cfg) {
+    const int bm = sgmv::dense_tile_rows(cfg);
+    // A tile with more than half of its rows empty only where none is smaller.
+    if (cfg == sgmv::kTile256 && M <= 128) continue;
+    if (cfg == sgmv::kTile128 && M <= 64 && may_split) continue;  // dW has no smaller tile
+    if (cfg == sgmv::kTile64 && (M <= 32 || M > 64)) continue;
+    if (cfg == sgmv::kTile32 && M > 32) continue;
+    if (!may_split && cfg > sgmv::kTile128) continue;
+    const int64_t tm = ceil_div(M, bm), tn = ceil_div(N, sgmv::dense_tile_cols(cfg) / columns_per_n);
+    const int64_t slots = kCus * resident(cfg);
+    const int64_t most = may_split ? std::max<int64_t>(1, std::min<int64_t>(16, steps / 4)) : 1;
+    for (int64_t ks = 1; ks <= most; ++ks) {
+      const int64_t per = ceil_div(std::max<int64_t>(steps, 1), ks);
+      const int64_t used = ceil_div(std::max<int64_t>(steps, 1), per);
+      if (used != ks) continue;
+      const int64_t rounds = ceil_div(tm * tn * ks, slots);
+      double cost = (double)rounds * ((double)per * step_us(cfg) + 4.0);
+      if (ks > 1) cost += 3.0 + 2.0 * (double)ks * (double)M * (double)N * columns_per_n * 4 / kPlaneBytesPerUs;
+      if (best_cost < 0 || cost < best_cost) {
+        best_cost = cost;
+        best.cfg = cfg;
+        best.tiles_m = (int)tm;
+        best.tiles_n = (int)tn;
+        best.ksplit = (int)ks;
+        best.ktiles_per_split = (int)per;
+      }
+    }
+  }
+  return best;
+}
+
+ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products) {
+  ThinPlan t;
+  if (p.max_seg_len <= sgmv::kThinRows) {
+    t.units = p.num_segs;
+    t.direct = 1;
+  } else {
+    t.direct = 0;
+    t.units = (int)std::min<int64_t>((int64_t)p.num_segs * ceil_div(p.max_seg_len, sgmv::kThinRows),
+                                     ceil_div(p.n_rows, sgmv::kThinRows) + p.num_segs);
+  }
+  const int64_t want = ceil_div(512, std::max<int64_t>(1, (int64_t)t.units * products));
+  const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(want, ceil_div(K, 256)));
+  t.kc = (int)round_up(ceil_div(K, ks), 128);
+  t.ksplit = (int)ceil_div(K, t.kc);
+  t.plane_bytes = t.ksplit > 1 ? (size_t)t.ksplit * p.n_rows * p.rank * sizeof(float) : 0;
+  return t;
+}
+
+int plan_grad_split(const sgmv_problem_t& p, int64_t C, int products) {
+  const int64_t wgs = (int64_t)p.num_loras * ceil_div(C, sgmv::kLoraGradCols) * products;
+  const int64_t bytes = (int64_t)p.num_loras * C * p.rank * 4 * products;
+  const int64_t fill = ceil_div(1024, std::max<int64_t>(1, wgs));
+  const int64_t steps = ceil_div(p.n_rows, 4 * sgmv::kLoraGradRows);  // at least four steps each
+  const int64_t longest = ceil_div(p.max_seg_len, 32 * sgmv::kLoraGradRows);  // one long segment alone
+  const int64_t n = std::min<int64_t>({std::max(fill, longest), steps, kGradPlaneBytes / std::max<int64_t>(1, bytes), 64});
+  return (int)std::max<int64_t>(1, n);
+}
+
+}  // namespace
+
+LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
+  LayerPlan l;
+  l.projections = layer_gated(op) ? 2 : 1;
+  l.lora = !nothing_to_do(p);
+  const int64_t n = p.n_rows;
+  const bool back = layer_backward(op);
+  size_t at = 0;
+  const auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (size_t)round_up((int64_t)bytes, 256);
+    return here;
+  };
+  if (l.lora) {
+    const size_t v = (size_t)n * p.rank * sizeof(float);
+    l.down = plan_thin(p, p.h_in, l.projections);
+    size_t planes = l.down.plane_bytes;
+    if (back) {
+      l.up = plan_thin(p, p.h_out, l.projections);
+      planes = std::max(planes, l.up.plane_bytes);
+    }
+    for (int i = 0; i < l.projections; ++i) {
+      l.v_off[i] = take(v);
+      if (back) l.dv_off[i] = take(v);
+      l.thin_off[i] = take(planes);
+    }
+  }
+  if (op == SGMV_GATED_BACKWARD)
+    for (int i = 0; i < 2; ++i) l.gate_off[i] = take((size_t)n * p.h_out * 2);
+  // The LoRA term joins in the tiles where segments are long enough for a
+  // matrix instruction's 16 rows; else the epilogue launch adds it row by row.
+  const bool in_tile = l.lora && n >= (int64_t)kShortRun * p.num_segs;
+  const int64_t M = n, N = back ? p.h_in : p.h_out;
+  const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK);
+  const int cols = op == SGMV_GATED_FORWARD ? 2 : 1;
+  l.out = plan_dense(M, N, kt * (op == SGMV_GATED_BACKWARD ? 2 : 1), cols, true);
+  l.out.term_in_tile = in_tile ? 1 : 0;
+  l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile);
+  if (l.out.to_planes) l.out.plane_bytes = (size_t)l.out.ksplit * M * N * cols * sizeof(float);
+  size_t area = l.out.plane_bytes;
+  if (back) {
+    l.dw = plan_dense(p.h_in, p.h_out, ceil_div(n, sgmv::kDenseK), 1, false);
+    if (l.lora) {
+      l.nsplit_a = plan_grad_split(p, p.h_in, l.projections);
+      l.nsplit_b = plan_grad_split(p, p.h_out, l.projections);
+      const auto bytes = [&](int ns, int64_t C) {
+        return ns > 1 ? (size_t)ns * p.num_loras * C * p.rank * sizeof(float) * l.projections : (size_t)0;
+      };
+      area = std::max({area, bytes(l.nsplit_a, p.h_in), bytes(l.nsplit_b, p.h_out)});
+    }
+  }
+  l.planes_off = take(area);
+  l.total = at;
+  return l;
+}
+
+}  // namespace sgmv_host
+
+using namespace sgmv_host;
+
+extern "C" {
+
+sgmv_status_t sgmv_layer_workspace_bytes(const sgmv_problem_t* p, int32_t op, size_t* bytes) {
+  const sgmv_status_t st = sgmv_check_problem(p);
+  if (st != SGMV_OK) return st;
+  if (!bytes || op < SGMV_DENSE_FORWARD || op > SGMV_GATED_BACKWARD) return SGMV_ERR_INVALID_ARG;
+  *bytes = plan_layer(*p, op).total;
+  return SGMV_OK;
+}
+
+}  // extern "C"

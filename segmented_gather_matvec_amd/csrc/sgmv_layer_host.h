@@ -1,0 +1,44 @@
+// sgmv_layer_host.h - host-only plans and workspace layout of the layer entry
+// points (plain C++, no HIP).
+#pragma once
+
+#include "sgmv_host.h"
+#include "sgmv_layer_shapes.h"
+
+namespace sgmv_host {
+
+// One dense product: output M x N per projection, `steps` contraction steps of 64.
+struct DensePlan {
+  int cfg = sgmv::kTile256;
+  int tiles_m = 0, tiles_n = 0;
+  int ksplit = 1;
+  int ktiles_per_split = 1;
+  int to_planes = 0;     // fp32 planes and an epilogue launch
+  int term_in_tile = 0;  // the tiles add the LoRA term
+  size_t plane_bytes = 0;
+};
+
+struct ThinPlan {
+  int units = 0, direct = 1, ksplit = 1, kc = 128;
+  size_t plane_bytes = 0;  // of one product
+};
+
+struct LayerPlan {
+  bool lora = false;
+  int projections = 1;
+  DensePlan out;       // forward, or dX
+  DensePlan dw;        // dW
+  ThinPlan down;       // V = s_k X @ A_k        (K = h_in)
+  ThinPlan up;         // dV = s_k dY @ B_k^T    (K = h_out)
+  int nsplit_a = 1, nsplit_b = 1;  // row splits of the gradients of A_k and B_k
+  // Byte offsets into the workspace.
+  size_t v_off[2] = {0, 0}, dv_off[2] = {0, 0}, thin_off[2] = {0, 0}, gate_off[2] = {0, 0};
+  size_t planes_off = 0;  // partial planes of the dense product, then of the LoRA gradients (never both live)
+  size_t total = 0;
+};
+
+inline bool layer_gated(int op) { return op == SGMV_GATED_FORWARD || op == SGMV_GATED_BACKWARD; }
+inline bool layer_backward(int op) { return op == SGMV_DENSE_BACKWARD || op == SGMV_GATED_BACKWARD; }
+LayerPlan plan_layer(const sgmv_problem_t& p, int op);
+
+}  // namespace sgmv_host
