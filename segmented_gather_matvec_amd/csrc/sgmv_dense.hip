@@ -35,8 +35,9 @@ __device__ inline void wait_loads_and_lds() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
 }
 
-template <int MODE, int BM_, int BN_, int WM_, int WN_, int STAGES_>
+template <int MODE, int BM_, int BN_, int WM_, int WN_, int STAGES_, int WAVES_PER_SIMD_>
 struct DenseShape {
+  static constexpr int WAVES_PER_SIMD = WAVES_PER_SIMD_;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, STAGES = STAGES_;
   static constexpr int NW = WM * WN;                  // waves
   static constexpr int TM = BM / WM / 16;             // 16-row tiles per wave
@@ -50,6 +51,7 @@ struct DenseShape {
   static constexpr int LB = BN / 8 / NW;
   static constexpr int TNP = TN / NB;                 // 16-column tiles of one projection per wave
   static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN, "tile loads split evenly over the waves");
+  static_assert(TNP == 1 || TNP == 2 || (TNP == 4 && !GATED), "the LoRA term joins two column tiles at a time");
   static_assert(TM * 16 * WM == BM && TNP * NB * 16 * WN == BN, "tile splits evenly over the waves");
 };
 
@@ -82,12 +84,14 @@ struct TileLoader {
   }
   // base: the operand; r0: first row (column) of the tile, rows: how many the
   // matrix has; k0: first contraction index of the step, K: how many there are.
-  __device__ inline void issue(const uint16_t* base, int ld, int r0, int rows, int k0, int K, uint16_t* lds, int wave,
-                               int lane) const {
+  // live = false: every lane is out of range (nothing is fetched, the slot is
+  // filled with zeros), so that each step counts the same loads.
+  __device__ inline void issue(const uint16_t* base, int ld, int r0, int rows, int k0, int K, bool live, uint16_t* lds,
+                               int wave, int lane) const {
     lds += wave * LOADS * 512;
     if constexpr (T) {
       const int kv = K - k0 < kDenseK ? K - k0 : kDenseK;
-      const uint32_t bytes = kv > 0 ? (uint32_t)((kv - 1) * ld + (rows - r0)) * 2u : 0u;
+      const uint32_t bytes = (uint32_t)((kv - 1) * ld + (rows - r0)) * (2u * (uint32_t)live);
       const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)k0 * ld + r0), 0,
                                                         (int)bytes, kRawBuffer);
 #pragma unroll
@@ -96,19 +100,12 @@ struct TileLoader {
     } else {
       const int rv = rows - r0 < R ? rows - r0 : R;
       const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)r0 * ld), 0,
-                                                        rv * ld * 2, kRawBuffer);
-      if (k0 + kDenseK <= K) {
+                                                        rv * ld * (2 * (int)live), kRawBuffer);
+      const int g = (lane & 7) ^ (lane >> 3);  // 8 rows per piece: row & 7 == lane / 8
+      const uint32_t past = k0 + g * 8 < K ? 0u : kOutOfRange;
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + j * 512), 16, (int)voff[j], k0 * 2, 0, 0);
-      } else {
-#pragma unroll
-        for (int j = 0; j < LOADS; ++j) {
-          const int g = (lane & 7) ^ (lane >> 3);  // 8 rows per piece: row & 7 == lane / 8
-          const uint32_t off = k0 + g * 8 < K ? voff[j] : kOutOfRange;
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + j * 512), 16, (int)off, k0 * 2, 0, 0);
-        }
-      }
+      for (int j = 0; j < LOADS; ++j)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + j * 512), 16, (int)(voff[j] | past), k0 * 2, 0, 0);
     }
   }
 };
@@ -247,7 +244,7 @@ __device__ inline u32x2 round4(const f32x4& v) {
 }
 
 template <class T, int MODE, class S>
-__global__ __launch_bounds__(S::NW * 64, 2) void sgmv_dense_kernel(DenseParams p) {
+__global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kernel(DenseParams p) {
   constexpr int STAGES = S::STAGES, TM = S::TM, TN = S::TN, TNP = S::TNP;
   __shared__ __attribute__((aligned(1024))) uint16_t lds_a[STAGES][S::BM * kDenseK];
   __shared__ __attribute__((aligned(1024))) uint16_t lds_b[STAGES][S::BN * kDenseK];
@@ -289,15 +286,15 @@ __global__ __launch_bounds__(S::NW * 64, 2) void sgmv_dense_kernel(DenseParams p
   lb.init(wave - sub * WB, lane, p.ldb);
 
   auto issue = [&](int step, int slot) {
-    // Past the end nothing is wanted: K = k0 leaves every lane out of range.
-    const int s = step < last ? step : last - 1;
+    const bool live = step < last;
+    const int s = live ? step : last - 1;
     const int pair = MODE == kDenseDx && s >= kt ? 1 : 0;
     const int k0 = (s - pair * kt) * kDenseK;
     const int bi = MODE == kDenseDw ? proj : S::GATED ? sub : pair;
     const uint16_t* A = MODE == kDenseDx && pair ? p.A[1] : p.A[0];
     const uint16_t* B = bi ? p.B[1] : p.B[0];
-    la.issue(A, p.lda, m0, p.M, k0, p.K, lds_a[slot], wave, lane);
-    lb.issue(B, p.ldb, n0, p.N, k0, p.K, lds_b[slot] + sub * S::C * kDenseK, wave - sub * WB, lane);
+    la.issue(A, p.lda, m0, p.M, k0, p.K, live, lds_a[slot], wave, lane);
+    lb.issue(B, p.ldb, n0, p.N, k0, p.K, live, lds_b[slot] + sub * S::C * kDenseK, wave - sub * WB, lane);
   };
 
   f32x4 acc[TM][TN];
@@ -306,38 +303,64 @@ __global__ __launch_bounds__(S::NW * 64, 2) void sgmv_dense_kernel(DenseParams p
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto compute = [&](int slot) {
+  // Operands of half a step (32 of its 64 contraction steps).
+  u32x4 a[TM], b0[TN], b1[TN];
+  auto read_a = [&](int slot, int kk, int i) {
+    a[i] = FragReader<S::BM, S::A_T>::read(lds_a[slot], (wm * TM + i) * 16, kk, lane);
+  };
+  auto read_b = [&](int slot, int kk, u32x4 (&b)[TN]) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      u32x4 bf[TN];
+    for (int j = 0; j < TN; ++j)
+      b[j] = FragReader<S::C, S::B_T>::read(lds_b[slot] + (j / TNP) * S::C * kDenseK, (wn * TNP + j % TNP) * 16, kk, lane);
+  };
+  auto multiply = [&](int i, const u32x4 (&b)[TN]) {
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int sb = j / TNP;  // sub-tile
-        bf[j] = FragReader<S::C, S::B_T>::read(lds_b[slot] + sb * S::C * kDenseK, (wn * TNP + j % TNP) * 16, kk, lane);
-      }
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-        const u32x4 af = FragReader<S::BM, S::A_T>::read(lds_a[slot], (wm * TM + i) * 16, kk, lane);
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(bf[j], af, acc[i][j]);
-      }
-    }
+    for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(b[j], a[i], acc[i][j]);
   };
 
   if (last > first) {
+    // One step: the products of its first half, while the second half's
+    // operands replace the first's in the registers, row tile by row tile;
+    // then the second half's.  After the first HB row tiles of the second half
+    // every wave has read all of the step's slot and the next step's tile has
+    // landed: behind that one barrier the slot is refilled, a whole ring ahead,
+    // and the next step's first operands are read.  (The ring turns whole:
+    // steps past the end multiply zeros.)
     constexpr int kPerStep = S::LA + S::LB;  // loads of one wave per step
+    constexpr int HB = TM / 2;               // row tiles ahead of the barrier
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) issue(first + s, s);
-    // A step past the end refills its slot with the last step again (its
-    // product is skipped): every wave keeps the same count of loads in flight.
+    for (int s = 0; s < STAGES; ++s) issue(first + s, s);
+    wait_loads_and_lds<kPerStep*(STAGES - 1)>();
+    __builtin_amdgcn_s_barrier();
+    read_b(0, 0, b0);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) read_a(0, 0, i);
     for (int step = first; step < last; step += STAGES) {
 #pragma unroll
       for (int s = 0; s < STAGES; ++s) {
-        if (s > 0 && step + s >= last) break;
+        read_b(s, 1, b1);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          multiply(i, b0);
+          read_a(s, 1, i);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = 0; i < HB; ++i) multiply(i, b1);
         wait_loads_and_lds<kPerStep*(STAGES - 2)>();
         __builtin_amdgcn_s_barrier();
-        issue(step + s + STAGES - 1, (s + STAGES - 1) % STAGES);
-        compute(s);
+        __builtin_amdgcn_sched_barrier(0);
+        const int next = (s + 1) % STAGES;  // (past the end: zeros, not used)
+        read_b(next, 0, b0);
+        issue(step + s + STAGES, s);
+#pragma unroll
+        for (int i = HB; i < TM; ++i) {
+          if (i - HB < HB) read_a(next, 0, i - HB);
+          multiply(i, b1);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int i = TM - HB; i < TM; ++i) read_a(next, 0, i);
       }
     }
     wait_loads_and_lds<0>();  // no load may be in flight when the workgroup ends
@@ -347,13 +370,12 @@ __global__ __launch_bounds__(S::NW * 64, 2) void sgmv_dense_kernel(DenseParams p
   const int mw = m0 + wm * TM * 16;
   const int cw = n0 + wn * TNP * 16;
   if (MODE != kDenseDw && p.term_in_tile && g == 0) {
-    // Two column tiles at a time: four of E_k's operands would not fit the
-    // registers beside a 256 x 256 tile's accumulators.
+    // Two column tiles of E_k's operands at a time (registers).
+    constexpr int J = TNP < 2 ? TNP : 2;
     if constexpr (S::GATED) {
-      add_term<T, MODE, TM, TN, 0, TNP>(p, p.term[0], acc, mw, cw);
-      add_term<T, MODE, TM, TN, TNP, TNP>(p, p.term[1], acc, mw, cw);
+      add_term<T, MODE, TM, TN, 0, J>(p, p.term[0], acc, mw, cw);
+      add_term<T, MODE, TM, TN, TNP, J>(p, p.term[1], acc, mw, cw);
     } else {
-      constexpr int J = TN < 2 ? TN : 2;
       for (int t = 0; t < (MODE == kDenseDx ? p.pairs : 1); ++t) {
         add_term<T, MODE, TM, TN, 0, J>(p, t ? p.term[1] : p.term[0], acc, mw, cw);
         if constexpr (TN > 2) add_term<T, MODE, TM, TN, 2, 2>(p, t ? p.term[1] : p.term[0], acc, mw, cw + 32);
@@ -505,9 +527,9 @@ __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) 
   }
 }
 
-template <class T, int MODE, int BM, int BN, int WM, int WN, int STAGES>
+template <class T, int MODE, int BM, int BN, int WM, int WN, int STAGES, int WPS>
 hipError_t launch_tile(const DenseParams& p, hipStream_t s) {
-  using S = DenseShape<MODE, BM, BN, WM, WN, STAGES>;
+  using S = DenseShape<MODE, BM, BN, WM, WN, STAGES, WPS>;
   const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.ksplit;
   const int64_t grid = (total + kXcds - 1) / kXcds * kXcds;
   if (grid <= 0 || grid > 0x7fffffff || p.ktiles_per_split < 0) return hipErrorInvalidValue;
@@ -519,10 +541,10 @@ hipError_t launch_tile(const DenseParams& p, hipStream_t s) {
 template <class T, int MODE>
 hipError_t launch_mode(int cfg, const DenseParams& p, hipStream_t s) {
   switch (cfg) {
-    case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 2>(p, s);
-    case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 2>(p, s);
-    case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 3>(p, s);
-    case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 3>(p, s);
+    case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 2, 2>(p, s);
+    case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 2, 2>(p, s);
+    case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 3, 2>(p, s);
+    case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 3, 2>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -534,8 +556,8 @@ hipError_t launch_t(int mode, int cfg, const DenseParams& p, hipStream_t s) {
     case kDenseGated: return launch_mode<T, kDenseGated>(cfg, p, s);
     case kDenseDx: return launch_mode<T, kDenseDx>(cfg, p, s);
     case kDenseDw:
-      return cfg == kTile256 ? launch_tile<T, kDenseDw, 256, 256, 2, 4, 2>(p, s)
-                             : launch_tile<T, kDenseDw, 128, 128, 2, 2, 2>(p, s);
+      return cfg == kTile256 ? launch_tile<T, kDenseDw, 256, 256, 2, 4, 2, 2>(p, s)
+                             : launch_tile<T, kDenseDw, 128, 128, 2, 2, 2, 2>(p, s);
   }
   return hipErrorInvalidValue;
 }
