@@ -7,12 +7,12 @@
 //     gated    G, U = two forwards, H = act(G) * U
 //     dX       dX = sum_p (dY_p @ W_p^T + V_p @ A_{p,k}^T) V_p = s_k dY_p @ B_{p,k}^T
 //     dW       dW_p = X^T @ dY_p
-// A workgroup owns one output tile and walks the contraction in steps of 64.
+// A workgroup owns one output tile and walks the contraction in steps of 32.
 // Both operand tiles go from memory straight into LDS (no registers), one ring
 // slot per step; lanes past the matrix ask for an offset beyond the buffer
 // descriptor and get zeros.  An operand whose contraction index is contiguous
-// in memory is kept row by row, its 16-byte groups at group ^ (row & 7), and read
-// with 128-bit reads.  An operand stored the other way round (W in the forward,
+// in memory is kept row by row, its 16-byte groups at group ^ (row / 4 % 4), and
+// read with 128-bit reads.  An operand stored the other way round (W in the forward,
 // both in dW) is kept as it lies and read with the transposing 64-bit read:
 // the four rows that one 16-lane group reads lie in different banks, because
 // group g of row k is stored at g ^ f(k).  Tiles multiply as D^T = B^T A^T, so that
@@ -47,10 +47,12 @@ struct DenseShape {
   static constexpr bool B_T = MODE != kDenseDx;
   static constexpr int NB = GATED ? 2 : 1;            // column sub-tiles (gate, up)
   static constexpr int C = BN / NB;                   // columns of one sub-tile
-  static constexpr int LA = BM / 8 / NW;              // 1 KiB loads per wave and step
-  static constexpr int LB = BN / 8 / NW;
+  // 1 KiB loads per wave and step.  (A 32-row tile is two of them: two waves
+  // load each, the same bytes twice, so that every wave counts alike.)
+  static constexpr int LA = BM / 16 < NW ? 1 : BM / 16 / NW;
+  static constexpr int LB = BN / 16 / NW;
   static constexpr int TNP = TN / NB;                 // 16-column tiles of one projection per wave
-  static_assert(LA * 8 * NW == BM && LB * 8 * NW == BN, "tile loads split evenly over the waves");
+  static_assert((LA * 16 * NW) % BM == 0 && LB * 16 * NW == BN, "tile loads split evenly over the waves");
   static_assert(TNP == 1 || TNP == 2 || (TNP == 4 && !GATED), "the LoRA term joins two column tiles at a time");
   static_assert(TM * 16 * WM == BM && TNP * NB * 16 * WN == BN, "tile splits evenly over the waves");
 };
@@ -62,33 +64,36 @@ __device__ inline int swizzle_k(int k) {
   return (((k & 3) | ((k >> 1) & 4)) << 1) & (COLS / 8 - 1);
 }
 
-// One operand tile of R rows (or columns) x 64 contraction steps.
-template <int R, int LOADS, int NW, bool T>
+// One operand tile of R rows (or columns) x 32 contraction steps.
+template <int R, int LOADS, bool T>
 struct TileLoader {
+  static constexpr int PIECES = R / 16;  // of 1 KiB
   uint32_t voff[LOADS];
+  uint32_t lds_off[LOADS];  // uniform
+  uint32_t g8;              // first contraction index (of 8) of this lane within the step (row-major operand)
   __device__ inline void init(int wave, int lane, int ld) {
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      const int L = wave * LOADS + j;  // 1 KiB piece of the tile
+      const int L = (wave * LOADS + j) % PIECES;
+      lds_off[j] = (uint32_t)L * 512;
       if constexpr (T) {
         constexpr int G = R / 8;  // 16-byte groups per k row
         const int k = L * (64 / G) + lane / G;
         const int g = (lane % G) ^ swizzle_k<R>(k);
         voff[j] = (uint32_t)(k * ld + g * 8) * 2u;
       } else {
-        const int r = L * 8 + (lane >> 3);
-        const int g = (lane & 7) ^ (r & 7);
-        voff[j] = (uint32_t)(r * ld + g * 8) * 2u;
+        const int r = L * 16 + (lane >> 2);
+        voff[j] = (uint32_t)(r * ld + ((lane & 3) ^ ((lane >> 4) & 3)) * 8) * 2u;
       }
     }
+    g8 = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;
   }
   // base: the operand; r0: first row (column) of the tile, rows: how many the
   // matrix has; k0: first contraction index of the step, K: how many there are.
   // live = false: every lane is out of range (nothing is fetched, the slot is
   // filled with zeros), so that each step counts the same loads.
-  __device__ inline void issue(const uint16_t* base, int ld, int r0, int rows, int k0, int K, bool live, uint16_t* lds,
-                               int wave, int lane) const {
-    lds += wave * LOADS * 512;
+  __device__ inline void issue(const uint16_t* base, int ld, int r0, int rows, int k0, int K, bool live,
+                               uint16_t* lds) const {
     if constexpr (T) {
       const int kv = K - k0 < kDenseK ? K - k0 : kDenseK;
       const uint32_t bytes = (uint32_t)((kv - 1) * ld + (rows - r0)) * (2u * (uint32_t)live);
@@ -96,39 +101,35 @@ struct TileLoader {
                                                         (int)bytes, kRawBuffer);
 #pragma unroll
       for (int j = 0; j < LOADS; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + j * 512), 16, (int)voff[j], 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + lds_off[j]), 16, (int)voff[j], 0, 0, 0);
     } else {
       const int rv = rows - r0 < R ? rows - r0 : R;
       const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)r0 * ld), 0,
                                                         rv * ld * (2 * (int)live), kRawBuffer);
-      const int g = (lane & 7) ^ (lane >> 3);  // 8 rows per piece: row & 7 == lane / 8
-      const uint32_t past = k0 + g * 8 < K ? 0u : kOutOfRange;
+      const uint32_t past = k0 + (int)g8 < K ? 0u : kOutOfRange;
 #pragma unroll
       for (int j = 0; j < LOADS; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + j * 512), 16, (int)(voff[j] | past), k0 * 2, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + lds_off[j]), 16, (int)(voff[j] | past), k0 * 2,
+                                                 0, 0);
     }
   }
 };
 
-// Operand of 16 rows (columns) x 32 contraction steps at kk (0, 1) of an LDS tile.
+// Operand of 16 rows (columns) x 32 contraction steps of an LDS tile; tile: its
+// first row / column inside the tile (a multiple of 16).
 template <int R, bool T>
-struct FragReader {
-  // tile: first row / column of the fragment inside the tile (a multiple of 16)
-  __device__ static inline u32x4 read(const uint16_t* lds, int tile, int kk, int lane) {
-    const int q = lane >> 4, i = lane & 15;
-    if constexpr (T) {
-      const int k = kk * 32 + q * 8 + (i >> 2);
-      const int g = (tile / 8 + ((i & 3) >> 1)) ^ swizzle_k<R>(k);
-      const uint16_t* a = lds + k * R + g * 8 + (i & 1) * 4;
-      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)a);
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(a + 4 * R));  // same swizzle: k + 4
-      const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
-      return u32x4{l[0], l[1], h[0], h[1]};
-    } else {
-      return load_vec(lds + (tile + i) * 64 + (((kk * 4 + q) ^ (i & 7)) << 3));
-    }
+__device__ inline u32x4 read_operand(const uint16_t* lds, int tile, int lane) {
+  const int q = lane >> 4, i = lane & 15;
+  if constexpr (T) {
+    const int k = q * 8 + (i >> 2);
+    const int g = (tile / 8 + ((i & 3) >> 1)) ^ swizzle_k<R>(k);
+    const uint16_t* a = lds + k * R + g * 8 + (i & 1) * 4;
+    const u32x2 l = read_transposed(a), h = read_transposed(a + 4 * R);  // k + 4 has the same swizzle
+    return u32x4{l[0], l[1], h[0], h[1]};
+  } else {
+    return load_vec(lds + (tile + i) * kDenseK + ((q ^ (i >> 2)) << 3));
   }
-};
+}
 
 // Adds the LoRA term of projection `t` to the accumulators acc[0..TM)[J0..J0+TNP)
 // of a wave's rows [m0, m0 + 16 TM) and columns c0 + 16 j.
@@ -246,8 +247,8 @@ __device__ inline u32x2 round4(const f32x4& v) {
 template <class T, int MODE, class S>
 __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kernel(DenseParams p) {
   constexpr int STAGES = S::STAGES, TM = S::TM, TN = S::TN, TNP = S::TNP;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds_a[STAGES][S::BM * kDenseK];
-  __shared__ __attribute__((aligned(1024))) uint16_t lds_b[STAGES][S::BN * kDenseK];
+  constexpr int B0 = S::BM * kDenseK;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES][(S::BM + S::BN) * kDenseK];  // a slot: A, then B
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -277,9 +278,9 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
   const int first = g * p.ktiles_per_split;
   const int last = first + p.ktiles_per_split < steps_all ? first + p.ktiles_per_split : steps_all;
 
-  TileLoader<S::BM, S::LA, S::NW, S::A_T> la;
+  TileLoader<S::BM, S::LA, S::A_T> la;
   // A gated tile's columns are two sub-tiles; each wave loads pieces of one of them.
-  TileLoader<S::C, S::LB, S::NW / S::NB, S::B_T> lb;
+  TileLoader<S::C, S::LB, S::B_T> lb;
   constexpr int WB = S::NW / S::NB;  // waves that load one sub-tile
   const int sub = wave / WB;
   la.init(wave, lane, p.lda);
@@ -293,8 +294,8 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
     const int bi = MODE == kDenseDw ? proj : S::GATED ? sub : pair;
     const uint16_t* A = MODE == kDenseDx && pair ? p.A[1] : p.A[0];
     const uint16_t* B = bi ? p.B[1] : p.B[0];
-    la.issue(A, p.lda, m0, p.M, k0, p.K, live, lds_a[slot], wave, lane);
-    lb.issue(B, p.ldb, n0, p.N, k0, p.K, live, lds_b[slot] + sub * S::C * kDenseK, wave - sub * WB, lane);
+    la.issue(A, p.lda, m0, p.M, k0, p.K, live, lds[slot]);
+    lb.issue(B, p.ldb, n0, p.N, k0, p.K, live, lds[slot] + B0 + sub * S::C * kDenseK);
   };
 
   f32x4 acc[TM][TN];
@@ -303,64 +304,55 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // Operands of half a step (32 of its 64 contraction steps).
-  u32x4 a[TM], b0[TN], b1[TN];
-  auto read_a = [&](int slot, int kk, int i) {
-    a[i] = FragReader<S::BM, S::A_T>::read(lds_a[slot], (wm * TM + i) * 16, kk, lane);
-  };
-  auto read_b = [&](int slot, int kk, u32x4 (&b)[TN]) {
+  u32x4 a[TM], b[2][TN];
+  auto read_a = [&](int slot, int i) { a[i] = read_operand<S::BM, S::A_T>(lds[slot], (wm * TM + i) * 16, lane); };
+  auto read_b = [&](int slot, u32x4 (&v)[TN]) {
 #pragma unroll
     for (int j = 0; j < TN; ++j)
-      b[j] = FragReader<S::C, S::B_T>::read(lds_b[slot] + (j / TNP) * S::C * kDenseK, (wn * TNP + j % TNP) * 16, kk, lane);
+      v[j] = read_operand<S::C, S::B_T>(lds[slot] + B0 + (j / TNP) * S::C * kDenseK, (wn * TNP + j % TNP) * 16, lane);
   };
-  auto multiply = [&](int i, const u32x4 (&b)[TN]) {
+  auto multiply = [&](int i, const u32x4 (&v)[TN]) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(b[j], a[i], acc[i][j]);
+    for (int j = 0; j < TN; ++j) acc[i][j] = mfma<T>(v[j], a[i], acc[i][j]);
   };
 
   if (last > first) {
-    // One step: the products of its first half, while the second half's
-    // operands replace the first's in the registers, row tile by row tile;
-    // then the second half's.  After the first HB row tiles of the second half
-    // every wave has read all of the step's slot and the next step's tile has
-    // landed: behind that one barrier the slot is refilled, a whole ring ahead,
-    // and the next step's first operands are read.  (The ring turns whole:
-    // steps past the end multiply zeros.)
+    // A step's operands are read while the step before it multiplies, row tile
+    // by row tile into the registers that its products leave.  After the first
+    // HB row tiles of a step every wave holds all of the step's operands and the
+    // next step's tile has landed: behind that one barrier the slot is refilled, a whole
+    // ring ahead, and the reads of the next step begin.  (Steps past the end
+    // are zeros, so the ring may turn whole.)
     constexpr int kPerStep = S::LA + S::LB;  // loads of one wave per step
-    constexpr int HB = TM / 2;               // row tiles ahead of the barrier
+    constexpr int HB = TM / 2;
+    constexpr int TURN = STAGES % 2 ? 2 * STAGES : STAGES;  // steps per loop: slots and b[] at fixed places
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) issue(first + s, s);
     wait_loads_and_lds<kPerStep*(STAGES - 1)>();
     __builtin_amdgcn_s_barrier();
-    read_b(0, 0, b0);
+    read_b(0, b[0]);
 #pragma unroll
-    for (int i = 0; i < TM; ++i) read_a(0, 0, i);
-    for (int step = first; step < last; step += STAGES) {
+    for (int i = 0; i < TM; ++i) read_a(0, i);
+    for (int step = first; step < last; step += TURN) {
 #pragma unroll
-      for (int s = 0; s < STAGES; ++s) {
-        read_b(s, 1, b1);
+      for (int s = 0; s < TURN; ++s) {
+        constexpr int kAhead = kPerStep * (STAGES - 2);
+        const int slot = s % STAGES, next = (s + 1) % STAGES;
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          multiply(i, b0);
-          read_a(s, 1, i);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-#pragma unroll
-        for (int i = 0; i < HB; ++i) multiply(i, b1);
-        wait_loads_and_lds<kPerStep*(STAGES - 2)>();
+        for (int i = 0; i < HB; ++i) multiply(i, b[s % 2]);
+        wait_loads_and_lds<kAhead>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        const int next = (s + 1) % STAGES;  // (past the end: zeros, not used)
-        read_b(next, 0, b0);
-        issue(step + s + STAGES, s);
+        read_b(next, b[(s + 1) % 2]);
+        issue(step + s + STAGES, slot);
 #pragma unroll
         for (int i = HB; i < TM; ++i) {
-          if (i - HB < HB) read_a(next, 0, i - HB);
-          multiply(i, b1);
+          read_a(next, i - HB);
+          multiply(i, b[s % 2]);
           __builtin_amdgcn_sched_barrier(0);
         }
 #pragma unroll
-        for (int i = TM - HB; i < TM; ++i) read_a(next, 0, i);
+        for (int i = TM - HB; i < TM; ++i) read_a(next, i);
       }
     }
     wait_loads_and_lds<0>();  // no load may be in flight when the workgroup ends
@@ -541,10 +533,10 @@ hipError_t launch_tile(const DenseParams& p, hipStream_t s) {
 template <class T, int MODE>
 hipError_t launch_mode(int cfg, const DenseParams& p, hipStream_t s) {
   switch (cfg) {
-    case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 2, 2>(p, s);
-    case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 2, 2>(p, s);
-    case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 3, 2>(p, s);
-    case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 3, 2>(p, s);
+    case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 5, 2>(p, s);
+    case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 4, 2>(p, s);
+    case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 5, 2>(p, s);
+    case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 6, 2>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -556,8 +548,8 @@ hipError_t launch_t(int mode, int cfg, const DenseParams& p, hipStream_t s) {
     case kDenseGated: return launch_mode<T, kDenseGated>(cfg, p, s);
     case kDenseDx: return launch_mode<T, kDenseDx>(cfg, p, s);
     case kDenseDw:
-      return cfg == kTile256 ? launch_tile<T, kDenseDw, 256, 256, 2, 4, 2, 2>(p, s)
-                             : launch_tile<T, kDenseDw, 128, 128, 2, 2, 2, 2>(p, s);
+      return cfg == kTile256 ? launch_tile<T, kDenseDw, 256, 256, 2, 4, 5, 2>(p, s)
+                             : launch_tile<T, kDenseDw, 128, 128, 2, 2, 4, 2>(p, s);
   }
   return hipErrorInvalidValue;
 }

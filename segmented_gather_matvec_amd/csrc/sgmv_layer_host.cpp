@@ -20,10 +20,10 @@ int resident(int cfg) { return cfg == sgmv::kTile256 ? 1 : 2; }
 // picks between tile shapes and splits (only their ratios matter).
 double step_us(int cfg) {
   switch (cfg) {
-    case sgmv::kTile256: return 1.1;
-    case sgmv::kTile128: return 0.75;
-    case sgmv::kTile64: return 0.5;
-    default: return 0.4;
+    case sgmv::kTile256: return 0.55;
+    case sgmv::kTile128: return 0.37;
+    case sgmv::kTile64: return 0.25;
+    default: return 0.2;
   }
 }
 constexpr double kPlaneBytesPerUs = 4.0e6;
@@ -42,7 +42,7 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
     if (!may_split && cfg > sgmv::kTile128) continue;
     const int64_t tm = ceil_div(M, bm), tn = ceil_div(N, sgmv::dense_tile_cols(cfg) / columns_per_n);
     const int64_t slots = kCus * resident(cfg);
-    const int64_t most = may_split ? std::max<int64_t>(1, std::min<int64_t>(16, steps / 4)) : 1;
+    const int64_t most = may_split ? std::max<int64_t>(1, std::min<int64_t>(16, steps / 8)) : 1;
     for (int64_t ks = 1; ks <= most; ++ks) {
       const int64_t per = ceil_div(std::max<int64_t>(steps, 1), ks);
       const int64_t used = ceil_div(std::max<int64_t>(steps, 1), per);

@@ -7,7 +7,7 @@
 
 namespace sgmv_host {
 
-// One dense product: output M x N per projection, `steps` contraction steps of 64.
+// One dense product: output M x N per projection, `steps` contraction steps of kDenseK.
 struct DensePlan {
   int cfg = sgmv::kTile256;
   int tiles_m = 0, tiles_n = 0;

@@ -18,6 +18,15 @@ constexpr int kRawBuffer = 0x00020000;
 // Byte offset beyond every descriptor made here: such a lane's load returns 0.
 constexpr uint32_t kOutOfRange = 0x80000000u;
 
+// Transposing LDS read: of the 4 rows x 16 columns that a group of 16 lanes
+// addresses (lane i: 4 values of row i / 4 from column 4 (i % 4)), lane i gets
+// column i.  __restrict: without it the compiler takes the read for one that may
+// see any load to LDS in flight, and waits for all of them; callers wait for
+// the tile that they read.
+__device__ inline u32x2 read_transposed(const uint16_t* __restrict p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)p));
+}
+
 // v as hi + lo, two 16-bit values: about 16 (bf16) or 22 (fp16) significant
 // bits.  A hi that is not finite stands alone (its lo would be NaN).
 template <class T>

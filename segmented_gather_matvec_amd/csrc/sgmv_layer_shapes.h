@@ -4,7 +4,7 @@
 
 namespace sgmv {
 
-constexpr int kDenseK = 64;  // contraction length of one tile step
+constexpr int kDenseK = 32;  // contraction length of one tile step
 
 // Output tiles of the dense products (rows x columns; a gated tile's columns
 // are half gate, half up).

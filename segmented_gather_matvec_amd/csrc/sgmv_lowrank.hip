@@ -255,9 +255,7 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradParams
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint16_t* a = &lds_z[(q * 8 + (ml >> 2)) * ZST + wave * 64 + i * 16 + (ml & 3) * 4];
-          const s16x4 lo4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)a);
-          const s16x4 hi4 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4_ptr)(a + 4 * ZST));
-          const u32x2 l2 = __builtin_bit_cast(u32x2, lo4), h2 = __builtin_bit_cast(u32x2, hi4);
+          const u32x2 l2 = read_transposed(a), h2 = read_transposed(a + 4 * ZST);
           const u32x4 zf = {l2[0], l2[1], h2[0], h2[1]};
 #pragma unroll
           for (int j = 0; j < JT; ++j) {
