@@ -10,30 +10,18 @@
 // A workgroup owns one output tile and walks the contraction in steps of 32.
 // Both operand tiles go from memory straight into LDS (no registers), one ring
 // slot per step; lanes past the matrix ask for an offset beyond the buffer
-// descriptor and get zeros.  An operand whose contraction index is contiguous
-// in memory is kept row by row, its 16-byte groups at group ^ (row / 4 % 4), and
-// read with 128-bit reads.  An operand stored the other way round (W in the forward,
-// both in dW) is kept as it lies and read with the transposing 64-bit read:
-// the four rows that one 16-lane group reads lie in different banks, because
-// group g of row k is stored at g ^ f(k).  Tiles multiply as D^T = B^T A^T, so that
-// a lane ends up with four consecutive columns of one row.
-// The LoRA term joins in the epilogue: per run of rows that share a LoRA, V
-// (fp32, split into hi + lo 16-bit halves) times E_k on the matrix cores, added
-// to the accumulators in fp32; outputs are rounded once.
-#include "sgmv_layer_ops.h"
+// descriptor and get zeros (sgmv_tile.h has the layouts).  Tiles multiply as
+// D^T = B^T A^T, so that a lane ends up with four consecutive columns of one row.
+// The LoRA term joins in the epilogue: per run of rows that share a LoRA, V's
+// hi + lo 16-bit halves (together 16 or 22 bits of fp32's V) times E_k on the
+// matrix cores, onto the accumulators; outputs are rounded once.
+#include "sgmv_tile.h"
 
 namespace sgmv {
 namespace {
 
 constexpr int kXcds = 8;
 constexpr int kGroupRows = 8;  // row tiles that walk the columns together (they share W tiles in an XCD's L2)
-
-template <int N>
-__device__ inline void wait_loads_and_lds() {
-  // All but the N newest of this wave's loads have landed, and its LDS reads are
-  // done (the slot they read is refilled after the barrier that follows).
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(N) : "memory");
-}
 
 template <int MODE, int BM_, int BN_, int WM_, int WN_, int STAGES_, int WAVES_PER_SIMD_>
 struct DenseShape {
@@ -57,92 +45,18 @@ struct DenseShape {
   static_assert(TM * 16 * WM == BM && TNP * NB * 16 * WN == BN, "tile splits evenly over the waves");
 };
 
-// Column swizzle of a tile stored [k][cols]: f(k) of the kernel's header comment, in
-// 16-byte groups, for rows of at least 16 (or 8) groups.
-template <int COLS>
-__device__ inline int swizzle_k(int k) {
-  return (((k & 3) | ((k >> 1) & 4)) << 1) & (COLS / 8 - 1);
-}
-
-// One operand tile of R rows (or columns) x 32 contraction steps.
-template <int R, int LOADS, bool T>
-struct TileLoader {
-  static constexpr int PIECES = R / 16;  // of 1 KiB
-  uint32_t voff[LOADS];
-  uint32_t lds_off[LOADS];  // uniform
-  uint32_t g8;              // first contraction index (of 8) of this lane within the step (row-major operand)
-  __device__ inline void init(int wave, int lane, int ld) {
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      const int L = (wave * LOADS + j) % PIECES;
-      lds_off[j] = (uint32_t)L * 512;
-      if constexpr (T) {
-        constexpr int G = R / 8;  // 16-byte groups per k row
-        const int k = L * (64 / G) + lane / G;
-        const int g = (lane % G) ^ swizzle_k<R>(k);
-        voff[j] = (uint32_t)(k * ld + g * 8) * 2u;
-      } else {
-        const int r = L * 16 + (lane >> 2);
-        voff[j] = (uint32_t)(r * ld + ((lane & 3) ^ ((lane >> 4) & 3)) * 8) * 2u;
-      }
-    }
-    g8 = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;
-  }
-  // base: the operand; r0: first row (column) of the tile, rows: how many the
-  // matrix has; k0: first contraction index of the step, K: how many there are.
-  // live = false: every lane is out of range (nothing is fetched, the slot is
-  // filled with zeros), so that each step counts the same loads.
-  __device__ inline void issue(const uint16_t* base, int ld, int r0, int rows, int k0, int K, bool live,
-                               uint16_t* lds) const {
-    if constexpr (T) {
-      const int kv = K - k0 < kDenseK ? K - k0 : kDenseK;
-      const uint32_t bytes = (uint32_t)((kv - 1) * ld + (rows - r0)) * (2u * (uint32_t)live);
-      const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)k0 * ld + r0), 0,
-                                                        (int)bytes, kRawBuffer);
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + lds_off[j]), 16, (int)voff[j], 0, 0, 0);
-    } else {
-      const int rv = rows - r0 < R ? rows - r0 : R;
-      const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base + (int64_t)r0 * ld), 0,
-                                                        rv * ld * (2 * (int)live), kRawBuffer);
-      const uint32_t past = k0 + (int)g8 < K ? 0u : kOutOfRange;
-#pragma unroll
-      for (int j = 0; j < LOADS; ++j)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + lds_off[j]), 16, (int)(voff[j] | past), k0 * 2,
-                                                 0, 0);
-    }
-  }
-};
-
-// Operand of 16 rows (columns) x 32 contraction steps of an LDS tile; tile: its
-// first row / column inside the tile (a multiple of 16).
-template <int R, bool T>
-__device__ inline u32x4 read_operand(const uint16_t* lds, int tile, int lane) {
-  const int q = lane >> 4, i = lane & 15;
-  if constexpr (T) {
-    const int k = q * 8 + (i >> 2);
-    const int g = (tile / 8 + ((i & 3) >> 1)) ^ swizzle_k<R>(k);
-    const uint16_t* a = lds + k * R + g * 8 + (i & 1) * 4;
-    const u32x2 l = read_transposed(a), h = read_transposed(a + 4 * R);  // k + 4 has the same swizzle
-    return u32x4{l[0], l[1], h[0], h[1]};
-  } else {
-    return load_vec(lds + (tile + i) * kDenseK + ((q ^ (i >> 2)) << 3));
-  }
-}
-
-// Adds the LoRA term of projection `t` to the accumulators acc[0..TM)[J0..J0+TNP)
-// of a wave's rows [m0, m0 + 16 TM) and columns c0 + 16 j.
-template <class T, int MODE, int TM, int TN, int J0, int TNP>
-__device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x4 (&acc)[TM][TN], int m0, int c0) {
+// Adds the LoRA term of projection `t` to the accumulators acc[0..TM)[J0..J0+JN)
+// of a wave's rows [m0, m0 + 16 TM) and columns c0 + 16 j; s_first: the first segment that ends past m0.
+template <class T, int MODE, int TM, int TN, int J0, int JN>
+__device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x4 (&acc)[TM][TN], int m0, int c0,
+                                int s_first) {
   const int lane = threadIdx.x & 63;
   const int q = lane >> 4, ml = lane & 15;
   const SegMeta& sm = p.meta;
-  if (t.V == nullptr || sm.num_segs <= 0) return;
+  if (t.V16 == nullptr) return;
   const int mend = m0 + 16 * TM < p.M ? m0 + 16 * TM : p.M;
   const int R = p.rank;
-  const int steps = R > 32 ? 2 : 1;
-  for (int s0 = first_segment_past(sm, m0); s0 < sm.num_segs; s0 += 64) {
+  for (int s0 = s_first; s0 < sm.num_segs; s0 += 64) {
     // Metadata of 64 segments at a time, one per lane.
     const int sl = s0 + lane < sm.num_segs ? s0 + lane : sm.num_segs - 1;
     const int lo_l = sm.seg_indptr[sl], hi_l = sm.seg_indptr[sl + 1];
@@ -160,78 +74,50 @@ __device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x
       const uint32_t e_hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(e_l >> 32), u);
       const uint16_t* E = reinterpret_cast<const uint16_t*>(((uint64_t)e_hi << 32) | e_lo);
       if (r1 <= r0 || rk <= 0 || E == nullptr) continue;
-      // E_k operands of the wave's columns: lane holds E[32 s + 8 q + e][c0 + 16 j + ml].
-      u32x4 ef[2][TNP];
+      for (int k0 = 0; k0 < rk; k0 += 32) {
+        const int r = k0 + 8 * q;
+        const bool rok = r < rk;
+        // E_k operands of the wave's columns: lane holds E[k0 + 8 q + e][c0 + 16 j + ml].
+        u32x4 ef[JN];
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int j = 0; j < JN; ++j) {
+          const int c = c0 + 16 * j + ml;
+          const bool ok = rok && c < p.N;
+          if constexpr (MODE == kDenseDx) {
+            ef[j] = load_vec(E + (ok ? (int64_t)c * rk + r : 0));
+          } else {
 #pragma unroll
-        for (int j = 0; j < TNP; ++j) {
-          ef[s][j] = u32x4{0u, 0u, 0u, 0u};
-          const int c = c0 + 16 * j + ml, r = 32 * s + 8 * q;
-          if (s < steps && r < rk && c < p.N) {
-            if constexpr (MODE == kDenseDx) {
-              ef[s][j] = load_vec(E + (int64_t)c * rk + r);
-            } else {
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                const uint32_t a = ((global_u16_ptr)E)[(int64_t)(r + 2 * w) * p.N + c];
-                const uint32_t b = ((global_u16_ptr)E)[(int64_t)(r + 2 * w + 1) * p.N + c];
-                ef[s][j][w] = a | (b << 16);
-              }
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t a = ((global_u16_ptr)E)[ok ? (int64_t)(r + 2 * w) * p.N + c : 0];
+              const uint32_t b = ((global_u16_ptr)E)[ok ? (int64_t)(r + 2 * w + 1) * p.N + c : 0];
+              ef[j][w] = a | (b << 16);
             }
           }
+          if (!ok) ef[j] = u32x4{0u, 0u, 0u, 0u};
         }
+        const uint16_t* vcol = t.V16 + (rok ? r : 0);
 #pragma unroll
-      for (int mi = 0; mi < TM; ++mi) {
-        const int mb = m0 + 16 * mi;
-        if (mb + 16 <= r0 || mb >= r1) continue;
-        const int row = mb + ml;
-        const bool in = row >= r0 && row < r1;
-        float v[2][8];
-        float big = 0.f;
+        for (int mi = 0; mi < TM; ++mi) {
+          const int mb = m0 + 16 * mi;
+          if (mb + 16 <= r0 || mb >= r1) continue;
+          const int row = mb + ml;
+          const bool in = row >= r0 && row < r1;
+          const uint16_t* vp = vcol + (int64_t)(in ? row : r0) * (2 * R);
+          u32x4 vh = load_vec(vp), vl = load_vec(vp + R);
+          if (!rok) vh = vl = u32x4{0u, 0u, 0u, 0u};  // (0 times an infinite V would be NaN)
+          // The term's own sum first, then the rows of the run take it: what another
+          // LoRA's matrices hold must not reach them (fp16: scaled back up).
+          float up = 1.f;
+          if constexpr (T::kMaxFinite < 1e6f) up = t.row_scale[in ? row : r0];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const bool ok = in && s < steps && 32 * s + 8 * q < rk;
-          const float* vp = t.V + (ok ? (int64_t)row * R + 32 * s + 8 * q : 0);
-          const f32x4 a = *reinterpret_cast<const f32x4*>(vp), b = *reinterpret_cast<const f32x4*>(vp + 4);
+          for (int j = 0; j < JN; ++j) {
+            f32x4 d = {0.f, 0.f, 0.f, 0.f};
+            d = mfma<T>(ef[j], vl, d);
+            d = mfma<T>(ef[j], vh, d);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[s][e] = ok ? a[e] : 0.f;
-            v[s][4 + e] = ok ? b[e] : 0.f;
-            big = fmaxf(big, fmaxf(fabsf(v[s][e]), fabsf(v[s][4 + e])));
+            for (int i = 0; i < 4; ++i)
+              acc[mi][J0 + j][i] = in ? __builtin_fmaf(d[i], up, acc[mi][J0 + j][i]) : acc[mi][J0 + j][i];
           }
-        }
-        // fp16 halves hold V only below 65504: a row beyond 32768 goes through the
-        // matrix cores scaled down by a power of two (exact) and back up.
-        float up = 1.f;
-        if constexpr (T::kMaxFinite < 1e6f) {
-          big = fmaxf(big, shfl_xor(big, 16));
-          big = fmaxf(big, shfl_xor(big, 32));
-          if (big > 32768.f && big < 3.4e38f) {
-            const int e = ((int)(__float_as_uint(big) >> 23) & 255) - 127 - 14;  // 1 .. 113
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-            up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-              for (int e8 = 0; e8 < 8; ++e8) v[s][e8] *= down;
-          }
-        }
-        u32x4 vh[2], vl[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) split8<T>(v[s], vh[s], vl[s]);
-#pragma unroll
-        for (int j = 0; j < TNP; ++j) {
-          f32x4 d = {0.f, 0.f, 0.f, 0.f};
-          d = mfma<T>(ef[0][j], vl[0], d);
-          d = mfma<T>(ef[0][j], vh[0], d);
-          if (steps > 1) {
-            d = mfma<T>(ef[1][j], vl[1], d);
-            d = mfma<T>(ef[1][j], vh[1], d);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[mi][J0 + j][i] = in ? __builtin_fmaf(d[i], up, acc[mi][J0 + j][i]) : acc[mi][J0 + j][i];
         }
       }
     }
@@ -286,16 +172,23 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
   la.init(wave, lane, p.lda);
   lb.init(wave - sub * WB, lane, p.ldb);
 
-  auto issue = [&](int step, int slot) {
-    const bool live = step < last;
-    const int s = live ? step : last - 1;
+  // Steps first .. last - 1 of the contraction, in order; dX may go on from pair 0 to pair 1.
+  auto start = [&](int s) {
     const int pair = MODE == kDenseDx && s >= kt ? 1 : 0;
     const int k0 = (s - pair * kt) * kDenseK;
+    const int in_pair = (last - pair * kt < kt ? last - pair * kt : kt) * kDenseK;
+    const int K = in_pair < p.K ? in_pair : p.K;
     const int bi = MODE == kDenseDw ? proj : S::GATED ? sub : pair;
-    const uint16_t* A = MODE == kDenseDx && pair ? p.A[1] : p.A[0];
-    const uint16_t* B = bi ? p.B[1] : p.B[0];
-    la.issue(A, p.lda, m0, p.M, k0, p.K, live, lds[slot]);
-    lb.issue(B, p.ldb, n0, p.N, k0, p.K, live, lds[slot] + B0 + sub * S::C * kDenseK);
+    la.start(MODE == kDenseDx && pair ? p.A[1] : p.A[0], p.lda, m0, p.M, k0, K);
+    lb.start(bi ? p.B[1] : p.B[0], p.ldb, n0, p.N, k0, K);
+  };
+  int left_in_pair = kt - first;  // steps before the second pair starts (dX)
+  auto issue = [&](int slot) {
+    la.issue(lds[slot]);
+    lb.issue(lds[slot] + B0 + sub * S::C * kDenseK);
+    if constexpr (MODE == kDenseDx) {
+      if (--left_in_pair == 0 && last > kt) start(kt);
+    }
   };
 
   f32x4 acc[TM][TN];
@@ -326,8 +219,9 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
     constexpr int kPerStep = S::LA + S::LB;  // loads of one wave per step
     constexpr int HB = TM / 2;
     constexpr int TURN = STAGES % 2 ? 2 * STAGES : STAGES;  // steps per loop: slots and b[] at fixed places
+    start(first);
 #pragma unroll
-    for (int s = 0; s < STAGES; ++s) issue(first + s, s);
+    for (int s = 0; s < STAGES; ++s) issue(s);
     wait_loads_and_lds<kPerStep*(STAGES - 1)>();
     __builtin_amdgcn_s_barrier();
     read_b(0, b[0]);
@@ -344,7 +238,7 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
         read_b(next, b[(s + 1) % 2]);
-        issue(step + s + STAGES, slot);
+        issue(slot);
 #pragma unroll
         for (int i = HB; i < TM; ++i) {
           read_a(next, i - HB);
@@ -364,13 +258,14 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
   if (MODE != kDenseDw && p.term_in_tile && g == 0) {
     // Two column tiles of E_k's operands at a time (registers).
     constexpr int J = TNP < 2 ? TNP : 2;
+    const int seg = first_segment_past(p.meta, mw);
     if constexpr (S::GATED) {
-      add_term<T, MODE, TM, TN, 0, J>(p, p.term[0], acc, mw, cw);
-      add_term<T, MODE, TM, TN, TNP, J>(p, p.term[1], acc, mw, cw);
+      add_term<T, MODE, TM, TN, 0, J>(p, p.term[0], acc, mw, cw, seg);
+      add_term<T, MODE, TM, TN, TNP, J>(p, p.term[1], acc, mw, cw, seg);
     } else {
       for (int t = 0; t < (MODE == kDenseDx ? p.pairs : 1); ++t) {
-        add_term<T, MODE, TM, TN, 0, J>(p, t ? p.term[1] : p.term[0], acc, mw, cw);
-        if constexpr (TN > 2) add_term<T, MODE, TM, TN, 2, 2>(p, t ? p.term[1] : p.term[0], acc, mw, cw + 32);
+        add_term<T, MODE, TM, TN, 0, J>(p, t ? p.term[1] : p.term[0], acc, mw, cw, seg);
+        if constexpr (TN > 2) add_term<T, MODE, TM, TN, 2, 2>(p, t ? p.term[1] : p.term[0], acc, mw, cw + 32, seg);
       }
     }
   }
@@ -533,7 +428,7 @@ hipError_t launch_tile(const DenseParams& p, hipStream_t s) {
 template <class T, int MODE>
 hipError_t launch_mode(int cfg, const DenseParams& p, hipStream_t s) {
   switch (cfg) {
-    case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 5, 2>(p, s);
+    case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 4, 2>(p, s);
     case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 4, 2>(p, s);
     case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 5, 2>(p, s);
     case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 6, 2>(p, s);
@@ -548,7 +443,7 @@ hipError_t launch_t(int mode, int cfg, const DenseParams& p, hipStream_t s) {
     case kDenseGated: return launch_mode<T, kDenseGated>(cfg, p, s);
     case kDenseDx: return launch_mode<T, kDenseDx>(cfg, p, s);
     case kDenseDw:
-      return cfg == kTile256 ? launch_tile<T, kDenseDw, 256, 256, 2, 4, 5, 2>(p, s)
+      return cfg == kTile256 ? launch_tile<T, kDenseDw, 256, 256, 2, 4, 4, 2>(p, s)
                              : launch_tile<T, kDenseDw, 128, 128, 2, 2, 4, 2>(p, s);
   }
   return hipErrorInvalidValue;

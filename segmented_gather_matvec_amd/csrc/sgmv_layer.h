@@ -23,7 +23,9 @@ struct SegMeta {
 //   out[i, c] += sum_j V[i, j] * E_k[j, c]
 // forward: V = s_k X @ A_k, E_k = B_k; dX: V = s_k dY @ B_k^T, E_k = A_k^T.
 struct LowRankTerm {
-  const float* V;          // [n_rows][rank] fp32 (null: no term)
+  const float* V;          // [n_rows][rank] fp32, read by the epilogue kernel (null: no term)
+  const uint16_t* V16;     // [n_rows][2][rank] V's hi, then lo halves, read by the tiles (null: no term)
+  const float* row_scale;  // fp16: [n_rows] the power of two that V16's rows are scaled down by
   const uint64_t* ptrs;    // [num_loras] -> B_k [r_k, N], or A_k [N, r_k] for dX
   const int32_t* ranks;    // null, or rank of each LoRA
 };
@@ -70,11 +72,13 @@ struct ThinParams {
   const uint64_t* ptrs;
   const int32_t* ranks;
   const float* scales;
-  float* V;               // [n_rows][rank]
+  float* V;               // null, or [n_rows][rank] fp32
+  uint16_t* V16;          // null, or [n_rows][2][rank] hi and lo halves (see LowRankTerm)
+  float* row_scale;       // with V16 in fp16: [n_rows]
   float* planes;          // [ksplit][n_rows][rank] (ksplit > 1)
   int32_t K, rank, transposed;
   int32_t units, direct;  // units of <= kThinRows rows of one segment
-  int32_t ksplit, kc;     // K per split, a multiple of 128
+  int32_t ksplit, kc;     // K per split, a multiple of 32
   SegMeta meta;
 };
 // count products on grid y (at most 2); the plane sum follows when ksplit > 1.

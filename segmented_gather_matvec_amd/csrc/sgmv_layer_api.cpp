@@ -64,7 +64,8 @@ sgmv::SegMeta seg_meta(const sgmv_problem_t& p, bool lora, const int32_t* seg_in
 }
 
 // V_i = s_k Z_i @ A_k (up = false) or s_k Z_i @ B_k^T (up = true) of every projection.
-sgmv_status_t thin(const Call& c, bool up, const void* const* Z) {
+// What of each is wanted: fp32 (the LoRA gradients and the epilogue kernel read it), 16-bit halves (the tiles).
+sgmv_status_t thin(const Call& c, bool up, const void* const* Z, bool full, bool halves) {
   sgmv::ThinParams t[2]{};
   const ThinPlan& plan = up ? c.plan.up : c.plan.down;
   for (int i = 0; i < c.np; ++i) {
@@ -72,7 +73,9 @@ sgmv_status_t thin(const Call& c, bool up, const void* const* Z) {
     t[i].ptrs = up ? table(c.proj[i]->B_ptrs) : table(c.proj[i]->A_ptrs);
     t[i].ranks = c.proj[i]->ranks;
     t[i].scales = c.proj[i]->scales;
-    t[i].V = c.at(up ? c.plan.dv_off[i] : c.plan.v_off[i]);
+    t[i].V = full ? c.at(up ? c.plan.dv_off[i] : c.plan.v_off[i]) : nullptr;
+    t[i].V16 = halves ? reinterpret_cast<uint16_t*>(c.at(c.plan.half_off[i])) : nullptr;
+    t[i].row_scale = c.at(c.plan.row_scale_off[i]);
     t[i].planes = c.at(c.plan.thin_off[i]);
     t[i].K = up ? c.p.h_out : c.p.h_in;
     t[i].rank = c.p.rank;
@@ -110,6 +113,19 @@ sgmv::DenseParams dense_params(const Call& c, const DensePlan& d, int64_t M, int
   return q;
 }
 
+sgmv::LowRankTerm term(const Call& c, int i, size_t v_off, const void* ptrs) {
+  sgmv::LowRankTerm t{};
+  if (c.plan.out.term_in_tile) {
+    t.V16 = reinterpret_cast<const uint16_t*>(c.at(c.plan.half_off[i]));
+    t.row_scale = c.at(c.plan.row_scale_off[i]);
+  } else {
+    t.V = c.at(v_off);
+  }
+  t.ptrs = table(ptrs);
+  t.ranks = c.proj[i]->ranks;
+  return t;
+}
+
 sgmv_status_t run_dense(const Call& c, int mode, const DensePlan& d, const sgmv::DenseParams& q) {
   if (sgmv::launch_dense(c.p.dtype, mode, d.cfg, q, c.stream) != hipSuccess) return SGMV_ERR_HIP;
   if (q.to_planes && sgmv::launch_dense_epilogue(c.p.dtype, mode, q, c.stream) != hipSuccess) return SGMV_ERR_HIP;
@@ -119,7 +135,7 @@ sgmv_status_t run_dense(const Call& c, int mode, const DensePlan& d, const sgmv:
 sgmv_status_t forward(const Call& c, void* const* out) {
   if (c.plan.lora) {
     const void* Z[2] = {c.X, c.X};
-    const sgmv_status_t st = thin(c, false, Z);
+    const sgmv_status_t st = thin(c, false, Z, !c.plan.out.term_in_tile, c.plan.out.term_in_tile);
     if (st != SGMV_OK) return st;
   }
   const bool gated = layer_gated(c.op);
@@ -127,7 +143,7 @@ sgmv_status_t forward(const Call& c, void* const* out) {
   q.A[0] = half(c.X);
   for (int i = 0; i < c.np; ++i) {
     q.B[i] = half(c.W[i]);
-    if (c.plan.lora) q.term[i] = {c.at(c.plan.v_off[i]), table(c.proj[i]->B_ptrs), c.proj[i]->ranks};
+    if (c.plan.lora) q.term[i] = term(c, i, c.plan.v_off[i], c.proj[i]->B_ptrs);
   }
   for (int i = 0; i < (gated ? 3 : 1); ++i) q.out[i] = static_cast<uint16_t*>(out[i]);
   return run_dense(c, gated ? sgmv::kDenseGated : sgmv::kDenseForward, c.plan.out, q);
@@ -143,11 +159,12 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
   }
   if (c.plan.lora && want_b) {
     const void* Z[2] = {c.X, c.X};
-    const sgmv_status_t st = thin(c, false, Z);
+    const sgmv_status_t st = thin(c, false, Z, true, false);
     if (st != SGMV_OK) return st;
   }
   if (c.plan.lora && (want_a || dX)) {
-    const sgmv_status_t st = thin(c, true, dY);
+    const bool halves = dX && c.plan.out.term_in_tile;
+    const sgmv_status_t st = thin(c, true, dY, want_a || !halves, halves);
     if (st != SGMV_OK) return st;
   }
   if (dX && rows) {
@@ -156,7 +173,7 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
     for (int i = 0; i < c.np; ++i) {
       q.A[i] = half(dY[i]);
       q.B[i] = half(c.W[i]);
-      if (c.plan.lora) q.term[i] = {c.at(c.plan.dv_off[i]), table(c.proj[i]->A_ptrs), c.proj[i]->ranks};
+      if (c.plan.lora) q.term[i] = term(c, i, c.plan.dv_off[i], c.proj[i]->A_ptrs);
     }
     q.out[0] = static_cast<uint16_t*>(dX);
     const sgmv_status_t st = run_dense(c, sgmv::kDenseDx, c.plan.out, q);

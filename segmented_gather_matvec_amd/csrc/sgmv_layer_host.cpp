@@ -73,9 +73,10 @@ ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products) {
     t.units = (int)std::min<int64_t>((int64_t)p.num_segs * ceil_div(p.max_seg_len, sgmv::kThinRows),
                                      ceil_div(p.n_rows, sgmv::kThinRows) + p.num_segs);
   }
-  const int64_t want = ceil_div(512, std::max<int64_t>(1, (int64_t)t.units * products));
+  // About four workgroups per CU, each of at least 256 contraction steps.
+  const int64_t want = ceil_div(1024, std::max<int64_t>(1, (int64_t)t.units * products));
   const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(want, ceil_div(K, 256)));
-  t.kc = (int)round_up(ceil_div(K, ks), 128);
+  t.kc = (int)round_up(ceil_div(K, ks), sgmv::kDenseK);
   t.ksplit = (int)ceil_div(K, t.kc);
   t.plane_bytes = t.ksplit > 1 ? (size_t)t.ksplit * p.n_rows * p.rank * sizeof(float) : 0;
   return t;
@@ -116,6 +117,8 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
     for (int i = 0; i < l.projections; ++i) {
       l.v_off[i] = take(v);
       if (back) l.dv_off[i] = take(v);
+      l.half_off[i] = take(v);  // two 16-bit halves a value
+      l.row_scale_off[i] = take((size_t)n * sizeof(float));
       l.thin_off[i] = take(planes);
     }
   }

@@ -33,6 +33,7 @@ struct LayerPlan {
   int nsplit_a = 1, nsplit_b = 1;  // row splits of the gradients of A_k and B_k
   // Byte offsets into the workspace.
   size_t v_off[2] = {0, 0}, dv_off[2] = {0, 0}, thin_off[2] = {0, 0}, gate_off[2] = {0, 0};
+  size_t half_off[2] = {0, 0}, row_scale_off[2] = {0, 0};  // V16 and its row scales, of the product the tiles add
   size_t planes_off = 0;  // partial planes of the dense product, then of the LoRA gradients (never both live)
   size_t total = 0;
 };

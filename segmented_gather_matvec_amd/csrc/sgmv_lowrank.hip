@@ -7,25 +7,59 @@
 // dV = s_k dy@B_k^T:
 //     dx  += dV @ A_k^T,   dA_k = sum_i x_i^T dV_i,   dB_k = sum_i V_i^T dy_i.
 // All of them read a [rows, thousands] operand once and are bound by memory.
-#include "sgmv_layer_ops.h"
+#include "sgmv_tile.h"
 
 namespace sgmv {
 namespace {
 
 // ---------------------------------------------------------------- thin products
-// Workgroup (unit, split): up to 64 rows of one segment, kc of the contraction,
-// a quarter of it per wave; the waves' sums meet in LDS in wave order.  JT:
-// 16-column tiles of the rank.  Z operands load straight from memory (8
-// contiguous values per lane), and so do B_k's rows; A_k's rows hold the rank
-// index, so eight 16-bit loads gather a lane's eight contraction steps.
+// Eight ranks c .. c+7 of row `row` of V, as fp32 and / or as hi + lo halves.
+// The rank / 8 lanes of one row are neighbours and all come here.
+template <class T>
+__device__ inline void store_v(const ThinParams& p, int row, int c, float (&v)[8]) {
+  if (p.V != nullptr) {
+    float* dst = p.V + (int64_t)row * p.rank + c;
+    *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
+  }
+  if (p.V16 == nullptr) return;
+  // fp16 halves hold V only below 65504: a row with a value beyond 32768 is kept
+  // scaled down by a power of two (exact), which the reader puts back.
+  if constexpr (T::kMaxFinite < 1e6f) {
+    float big = 0.f, up = 1.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(v[e]));
+    for (int d = 1; d < p.rank / 8; d <<= 1) big = fmaxf(big, shfl_xor(big, d));
+    if (big > 32768.f && big < 3.4e38f) {
+      const int e = ((int)(__float_as_uint(big) >> 23) & 255) - 127 - 14;  // 1 .. 113
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+      up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[x] *= down;
+    }
+    if (c == 0) p.row_scale[row] = up;
+  }
+  u32x4 hi, lo;
+  split8<T>(v, hi, lo);
+  uint16_t* dst = p.V16 + (int64_t)row * 2 * p.rank + c;
+  store_vec(dst, hi);
+  store_vec(dst + p.rank, lo);
+}
+
+// Workgroup (unit, split): up to 64 rows of one segment (16 per wave) times the
+// LoRA's D_k over kc contraction steps; both operands stream through a ring of
+// LDS slots (sgmv_tile.h).  Bound by reading Z.
 template <class T, int JT, bool TRANSPOSED>
 __global__ __launch_bounds__(kThreads) void sgmv_thin_kernel(ThinParams p0, ThinParams p1) {
   const ThinParams& p = blockIdx.y ? p1 : p0;
-  constexpr int RT = kThinRows / 16;
-  __shared__ float red[kWaves][kThinRows][JT * 16];
+  constexpr int COLS = JT * 16, STAGES = 6, kPerStep = 2;
+  constexpr int B0 = kThinRows * kDenseK, SLOT = (kThinRows + COLS) * kDenseK;
+  constexpr int RST = COLS + 4;  // row stride of the result in LDS (floats)
+  static_assert(STAGES * SLOT * 2 >= kThinRows * RST * 4, "the result fits the ring");
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES * SLOT];
   const int t = threadIdx.x;
   const int lane = t & 63;
-  const int wave = t >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int q = lane >> 4, ml = lane & 15;
   const int u = (int)blockIdx.x / p.ksplit;
   const int g = (int)blockIdx.x - u * p.ksplit;
@@ -35,88 +69,84 @@ __global__ __launch_bounds__(kThreads) void sgmv_thin_kernel(ThinParams p0, Thin
   const uint16_t* D = reinterpret_cast<const uint16_t*>(p.ptrs[un.k]);
   const int rk = D != nullptr ? rank_of(p.ranks, p.rank, un.k) : 0;
   const float scale = p.scales != nullptr ? p.scales[un.k] : 1.f;
-  const int kw = p.kc / kWaves;  // a multiple of 32
-  const int k0 = g * p.kc + wave * kw;
-  const int k1 = p.K < k0 + kw ? p.K : k0 + kw;
-  const int rts = (un.L + 15) / 16;
+  const int k0 = g * p.kc;
+  const int k1 = p.K < k0 + p.kc ? p.K : k0 + p.kc;
+  const int steps = rk > 0 ? (k1 - k0 + kDenseK - 1) / kDenseK : 0;
 
-  f32x4 acc[RT][JT];
+  f32x4 acc[JT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int j = 0; j < JT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (steps > 0) {
+    TileLoader<kThinRows, 1, false> la;
+    TileLoader<COLS, 1, !TRANSPOSED> lb;  // fewer pieces than waves: some load the same piece twice
+    const int ldd = TRANSPOSED ? p.K : rk;
+    la.init(wave, lane, p.K);
+    lb.init(wave, lane, ldd);
+    la.start(p.Z + (int64_t)un.r0 * p.K, p.K, 0, un.L, k0, k1);
+    lb.start(D, ldd, 0, rk, k0, k1);
 #pragma unroll
-    for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  if (rk > 0) {
-    const uint16_t* zrow[RT];
-    bool zok[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int r = i * 16 + ml;
-      zok[i] = r < un.L;
-      zrow[i] = p.Z + (int64_t)(un.r0 + (r < un.L ? r : 0)) * p.K;
+    for (int s = 0; s < STAGES - 1; ++s) {
+      la.issue(lds + s * SLOT);
+      lb.issue(lds + s * SLOT + B0);
     }
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    for (int kk = k0; kk < k1; kk += 32) {
-      const int k = kk + q * 8;
-      const bool kok = k < k1;  // K is a multiple of 8: eight steps are in or out together
-      u32x4 d[JT];
+    int slot = 0;
+    for (int s = 0; s < steps; ++s) {
+      wait_loads_and_lds<kPerStep*(STAGES - 2)>();
+      __builtin_amdgcn_s_barrier();
+      uint16_t* refill = lds + (slot == 0 ? STAGES - 1 : slot - 1) * SLOT;  // read in the step before this one
+      la.issue(refill);
+      lb.issue(refill + B0);
+      const uint16_t* now = lds + slot * SLOT;
+      const u32x4 z = read_operand<kThinRows, false>(now, wave * 16, lane);
 #pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        const int r = j * 16 + ml;
-        const bool ok = kok && r < rk;
-        if constexpr (TRANSPOSED) {
-          d[j] = load_vec(D + (ok ? (int64_t)r * p.K + k : 0));
-        } else {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t a = ((global_u16_ptr)D)[ok ? (int64_t)(k + 2 * w) * rk + r : 0];
-            const uint32_t b = ((global_u16_ptr)D)[ok ? (int64_t)(k + 2 * w + 1) * rk + r : 0];
-            d[j][w] = a | (b << 16);
-          }
-        }
-        d[j] = ok ? d[j] : zero;
-      }
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        if (i >= rts) break;
-        const bool ok = kok && zok[i];
-        u32x4 z = load_vec(zrow[i] + (ok ? k : 0));
-        z = ok ? z : zero;
-#pragma unroll
-        for (int j = 0; j < JT; ++j) acc[i][j] = mfma<T>(z, d[j], acc[i][j]);
-      }
+      for (int j = 0; j < JT; ++j)
+        acc[j] = mfma<T>(read_operand<COLS, !TRANSPOSED>(now + B0, j * 16, lane), z, acc[j]);
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
-  }
-  // acc[i][j][e]: row 16 i + 4 q + e, rank 16 j + ml.
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    if (i >= rts) break;
-#pragma unroll
-    for (int j = 0; j < JT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave][i * 16 + q * 4 + e][j * 16 + ml] = acc[i][j][e];
+    wait_loads_and_lds<0>();
   }
   __syncthreads();
-  float* dst = p.ksplit > 1 ? p.planes + (int64_t)g * p.meta.n_rows * p.rank : p.V;
-  for (int x = t; x < un.L * p.rank; x += kThreads) {
-    const int r = x / p.rank, c = x - r * p.rank;
-    float v = 0.f;
+  // acc[j][e]: row 16 wave + ml, rank 16 j + 4 q + e.
+  float* res = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += red[w][r][c];
-    dst[(int64_t)(un.r0 + r) * p.rank + c] = v * scale;
+  for (int j = 0; j < JT; ++j) *reinterpret_cast<f32x4*>(&res[(wave * 16 + ml) * RST + j * 16 + q * 4]) = acc[j];
+  __syncthreads();
+  const int per_row = p.rank / 8;
+  for (int x = t; x < un.L * per_row; x += kThreads) {
+    const int r = x / per_row, c = (x - r * per_row) * 8;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c < rk ? res[r * RST + c + e] * scale : 0.f;
+    if (p.ksplit > 1) {
+      float* dst = p.planes + ((int64_t)g * p.meta.n_rows + un.r0 + r) * p.rank + c;
+      *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+      store_v<T>(p, un.r0 + r, c, v);
+    }
   }
 }
 
 // V = sum of the planes, in plane order (rows no segment covers hold anything;
 // nothing reads them).
+template <class T>
 __global__ __launch_bounds__(kThreads) void sgmv_thin_sum_kernel(ThinParams p0, ThinParams p1) {
   const ThinParams& p = blockIdx.y ? p1 : p0;
+  const int per_row = p.rank / 8;
   const int64_t n = (int64_t)p.meta.n_rows * p.rank;
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (i >= n) return;  // n is a multiple of 8
-  f32x4 s = {0.f, 0.f, 0.f, 0.f};
-  for (int g = 0; g < p.ksplit; ++g) s += *reinterpret_cast<const f32x4*>(p.planes + g * n + i);
-  *reinterpret_cast<f32x4*>(p.V + i) = s;
+  const int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (x * 8 >= n) return;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int g = 0; g < p.ksplit; ++g) {
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p.planes + g * n + x * 8);
+    const f32x4 b = *reinterpret_cast<const f32x4*>(p.planes + g * n + x * 8 + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] += a[e];
+      v[4 + e] += b[e];
+    }
+  }
+  store_v<T>(p, (int)(x / per_row), (int)(x % per_row) * 8, v);
 }
 
 // ---------------------------------------------------------------- gradients of A_k and B_k
@@ -380,8 +410,8 @@ hipError_t launch_thin_j(const ThinParams* p, int count, hipStream_t s) {
     hipLaunchKernelGGL((sgmv_thin_kernel<T, JT, false>), grid, dim3(kThreads), 0, s, a, b);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.ksplit <= 1) return e;
-  const int64_t quads = (int64_t)a.meta.n_rows * a.rank / 4;
-  hipLaunchKernelGGL(sgmv_thin_sum_kernel, dim3((unsigned)((quads + kThreads - 1) / kThreads), (unsigned)count),
+  const int64_t items = (int64_t)a.meta.n_rows * a.rank / 8;
+  hipLaunchKernelGGL((sgmv_thin_sum_kernel<T>), dim3((unsigned)((items + kThreads - 1) / kThreads), (unsigned)count),
                      dim3(kThreads), 0, s, a, b);
   return hipGetLastError();
 }
