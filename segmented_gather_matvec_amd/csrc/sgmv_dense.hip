@@ -15,7 +15,7 @@
 // The LoRA term joins in the epilogue: per run of rows that share a LoRA, V's
 // hi + lo 16-bit halves (together 16 or 22 bits of fp32's V) times E_k on the
 // matrix cores, onto the accumulators; outputs are rounded once.
-#include "sgmv_tile.h"
+#include "sgmv_thin.h"
 
 namespace sgmv {
 namespace {
@@ -40,6 +40,7 @@ struct DenseShape {
   static constexpr int LA = BM / 16 < NW ? 1 : BM / 16 / NW;
   static constexpr int LB = BN / 16 / NW;
   static constexpr int TNP = TN / NB;                 // 16-column tiles of one projection per wave
+  static constexpr int SLOT = (BM + BN) * kDenseK;    // halves of one ring slot
   static_assert((LA * 16 * NW) % BM == 0 && LB * 16 * NW == BN, "tile loads split evenly over the waves");
   static_assert(TNP == 1 || TNP == 2 || (TNP == 4 && !GATED), "the LoRA term joins two column tiles at a time");
   static_assert(TM * 16 * WM == BM && TNP * NB * 16 * WN == BN, "tile splits evenly over the waves");
@@ -131,10 +132,12 @@ __device__ inline u32x2 round4(const f32x4& v) {
 }
 
 template <class T, int MODE, class S>
-__global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kernel(DenseParams p) {
+__device__ inline void dense_body(const DenseParams& p, int block, uint16_t* ring) {
   constexpr int STAGES = S::STAGES, TM = S::TM, TN = S::TN, TNP = S::TNP;
-  constexpr int B0 = S::BM * kDenseK;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES][(S::BM + S::BN) * kDenseK];  // a slot: A, then B
+  constexpr int B0 = S::BM * kDenseK;  // a slot: A, then B
+  uint16_t* lds[STAGES];
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) lds[s] = ring + s * S::SLOT;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -147,8 +150,8 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
   const int tiles = p.tiles_m * p.tiles_n;
   const int total = tiles * p.ksplit;
   const int per_xcd = (total + kXcds - 1) / kXcds;
-  const int idx = ((int)blockIdx.x % kXcds) * per_xcd + (int)blockIdx.x / kXcds;
-  if (idx >= total || (int)blockIdx.x / kXcds >= per_xcd) return;
+  const int idx = (block % kXcds) * per_xcd + block / kXcds;
+  if (idx >= total || block / kXcds >= per_xcd) return;
   const int g = idx / tiles;
   const int t = idx - g * tiles;
   const int group = t / (kGroupRows * p.tiles_n);
@@ -306,6 +309,62 @@ __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kern
   }
 }
 
+template <class T, int MODE, class S>
+__global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kernel(DenseParams p) {
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[S::STAGES * S::SLOT];
+  dense_body<T, MODE, S>(p, (int)blockIdx.x, lds);
+}
+
+// One of two parameter blocks, field by field: a conditional copy of the struct
+// would go through the stack.
+__device__ inline ThinParams pick(const ThinParams& a, const ThinParams& b, bool first) {
+  ThinParams t;
+  t.Z = first ? a.Z : b.Z;
+  t.ptrs = first ? a.ptrs : b.ptrs;
+  t.ranks = first ? a.ranks : b.ranks;
+  t.scales = first ? a.scales : b.scales;
+  t.V = first ? a.V : b.V;
+  t.V16 = nullptr;  // V stays in planes, or is the one plane
+  t.row_scale = nullptr;
+  t.planes = first ? a.planes : b.planes;
+  t.row_k = first ? a.row_k : nullptr;  // the same for both
+  t.K = a.K;
+  t.rank = a.rank;
+  t.transposed = 0;
+  t.units = a.units;
+  t.direct = a.direct;
+  t.ksplit = a.ksplit;
+  t.kc = a.kc;
+  t.meta = a.meta;
+  return t;
+}
+
+// The first dense_grid workgroups are the dense product's, the others thin
+// products' (nothing waits for anything): while the dense ones stream W, the thin
+// ones fill the slots that are left.
+template <class T, int MODE, class S>
+__global__ __launch_bounds__(kThreads, S::WAVES_PER_SIMD) void sgmv_dense_thin_kernel(DenseParams p, ThinParams t0,
+                                                                                       ThinParams t1, int dense_grid,
+                                                                                       int thin_grid) {
+  constexpr int RING = S::STAGES * S::SLOT;
+  static_assert(S::NW == kWaves && RING >= ThinShape<4>::LDS, "one workgroup size, one LDS ring");
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[RING];
+  const int b = (int)blockIdx.x;
+  if (b < dense_grid) {
+    dense_body<T, MODE, S>(p, b, lds);
+    return;
+  }
+  const int x = b - dense_grid;
+  const ThinParams t = pick(t0, t1, x < thin_grid);
+  const int item = x < thin_grid ? x : x - thin_grid;
+  if (p.rank <= 16)
+    thin_body<T, 1, false>(t, item, lds);
+  else if (p.rank == 32)
+    thin_body<T, 2, false>(t, item, lds);
+  else
+    thin_body<T, 4, false>(t, item, lds);
+}
+
 // ---------------------------------------------------------------- epilogue of the partial planes
 // One wave per (row i, 512 columns): lane l owns columns c .. c+7.  Sums the
 // planes in plane order; when the tiles did not add the LoRA term, adds
@@ -336,43 +395,26 @@ __device__ inline void plane_sum(const DenseParams& p, int proj, int64_t o, floa
   }
 }
 
+// v: V[i] of this row (LDS); E: the LoRA's B_k (A_k for dX).
 template <class T, int MODE>
-__device__ inline void row_term(const DenseParams& p, const LowRankTerm& t, int i, int k, int c, float (&y)[8]) {
-  const uint16_t* E = reinterpret_cast<const uint16_t*>(t.ptrs[k]);
-  const int rk = rank_of(t.ranks, p.rank, k);
-  if (E == nullptr) return;
-  const float* v = t.V + (int64_t)i * p.rank;
+__device__ inline void row_term(const DenseParams& p, const float* v, const uint16_t* E, int rk, int c, float (&y)[8]) {
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if constexpr (MODE == kDenseDx) {
-    for (int j = 0; j < rk; j += 8) {  // A_k [N, r_k]: eight columns' ranks j .. j+7
-      u32x4 a[8];
+  for (int j = 0; j < rk; j += 8) {
+    u32x4 m[8];  // forward: B_k [r_k, N], ranks j .. j+7; dX: A_k [N, r_k], columns c .. c+7
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = load_stream(E + (int64_t)(c + e) * rk + j);
-      const f32x4 v0 = *reinterpret_cast<const f32x4*>(v + j), v1 = *reinterpret_cast<const f32x4*>(v + j + 4);
+    for (int w = 0; w < 8; ++w)
+      m[w] = load_stream(MODE == kDenseDx ? E + (int64_t)(c + w) * rk + j : E + (int64_t)(j + w) * p.N + c);
+    const f32x4 v0 = *reinterpret_cast<const f32x4*>(v + j), v1 = *reinterpret_cast<const f32x4*>(v + j + 4);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      float f[8];
+      unpack8<T>(m[w], f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        float f[8];
-        unpack8<T>(a[e], f);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          s[e] = __builtin_fmaf(v0[w], f[w], s[e]);
-          s[e] = __builtin_fmaf(v1[w], f[4 + w], s[e]);
-        }
-      }
-    }
-  } else {
-    for (int j = 0; j < rk; j += 8) {  // B_k [r_k, N]
-      u32x4 b[8];
-#pragma unroll
-      for (int w = 0; w < 8; ++w) b[w] = load_stream(E + (int64_t)(j + w) * p.N + c);
-      const f32x4 v0 = *reinterpret_cast<const f32x4*>(v + j), v1 = *reinterpret_cast<const f32x4*>(v + j + 4);
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        float f[8];
-        unpack8<T>(b[w], f);
-        const float vj = w < 4 ? v0[w & 3] : v1[w & 3];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(vj, f[e], s[e]);
+        if constexpr (MODE == kDenseDx)
+          s[w] = __builtin_fmaf(e < 4 ? v0[e & 3] : v1[e & 3], f[e], s[w]);
+        else
+          s[e] = __builtin_fmaf(w < 4 ? v0[w & 3] : v1[w & 3], f[e], s[e]);
       }
     }
   }
@@ -382,34 +424,68 @@ __device__ inline void row_term(const DenseParams& p, const LowRankTerm& t, int 
 
 template <class T, int MODE>
 __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) {
+  constexpr int NT = MODE == kDenseForward ? 1 : 2;  // LoRA terms
+  constexpr int kBatch = 8;
+  __shared__ __attribute__((aligned(16))) float lds_v[NT][64];
   const int lane = threadIdx.x;
   const int i = blockIdx.x;
   const int c = blockIdx.y * 512 + lane * 8;
   if (i >= p.M) return;
+  const bool terms = !p.term_in_tile && p.meta.num_segs > 0 && p.term[0].V != nullptr;
   int k = -1;
-  if (!p.term_in_tile && p.meta.num_segs > 0) {
-    const int s = first_segment_past(p.meta, i);
-    if (s < p.meta.num_segs && p.meta.seg_indptr[s] <= i) k = p.meta.lora_idx[s];
+  if (terms) {
+    if (p.row_k != nullptr) {
+      // Covered rows are those before the last segment's end.
+      const int end = p.meta.seg_indptr[p.meta.num_segs], known = p.row_k[i];
+      k = i < end ? known : -1;
+    } else {
+      const int s = first_segment_past(p.meta, i);
+      if (s < p.meta.num_segs && p.meta.seg_indptr[s] <= i) k = p.meta.lora_idx[s];
+    }
     if (k >= p.meta.num_loras) k = -1;
+    // V[i] = the sum of its planes, in plane order; lane j holds rank j.
+    const int64_t vs = (int64_t)p.meta.n_rows * p.rank;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (t > 0 && MODE == kDenseDx && p.pairs < 2) break;
+      const float* vp = p.term[t].V + (int64_t)i * p.rank + (lane < p.rank ? lane : 0);
+      float v = 0.f;
+      for (int g0 = 0; g0 < p.v_planes; g0 += kBatch) {
+        float x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) x[u] = vp[(g0 + u < p.v_planes ? g0 + u : p.v_planes - 1) * vs];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) v = g0 + u < p.v_planes ? v + x[u] : v;
+      }
+      lds_v[t][lane] = v;
+    }
   }
+  k = __builtin_amdgcn_readfirstlane(k);
+  const uint16_t* E[NT];
+  int rk[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const bool on = k >= 0 && !(t > 0 && MODE == kDenseDx && p.pairs < 2);
+    E[t] = on ? reinterpret_cast<const uint16_t*>(p.term[t].ptrs[k]) : nullptr;
+    rk[t] = on && E[t] != nullptr ? rank_of(p.term[t].ranks, p.rank, k) : 0;
+  }
+  __syncthreads();
   if (c >= p.N) return;
   const int64_t o = (int64_t)i * p.N + c;
   float y[8];
   plane_sum<T, MODE>(p, 0, o, y);
-  if (k >= 0 && p.term[0].V != nullptr) row_term<T, MODE>(p, p.term[0], i, k, c, y);
+  row_term<T, MODE>(p, lds_v[0], E[0], rk[0], c, y);
   if constexpr (MODE == kDenseGated) {
     float u[8], h[8];
     plane_sum<T, MODE>(p, 1, o, u);
-    if (k >= 0 && p.term[1].V != nullptr) row_term<T, MODE>(p, p.term[1], i, k, c, u);
+    row_term<T, MODE>(p, lds_v[1], E[1], rk[1], c, u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = act_value(p.act, y[e]) * u[e];
     if (p.out[0]) store_vec(p.out[0] + o, pack8<T>(y));
     if (p.out[1]) store_vec(p.out[1] + o, pack8<T>(u));
     store_vec(p.out[2] + o, pack8<T>(h));
   } else {
-    if constexpr (MODE == kDenseDx) {
-      if (k >= 0 && p.pairs > 1 && p.term[1].V != nullptr) row_term<T, MODE>(p, p.term[1], i, k, c, y);
-    }
+    if constexpr (MODE == kDenseDx) row_term<T, MODE>(p, lds_v[1], E[1], rk[1], c, y);
     store_vec(p.out[0] + o, pack8<T>(y));
   }
 }
@@ -425,13 +501,34 @@ hipError_t launch_tile(const DenseParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <class T, int MODE, int BM, int BN, int WM, int WN, int STAGES, int WPS>
+hipError_t launch_tile_thin(const DenseParams& p, const ThinParams* t, int count, hipStream_t s) {
+  using S = DenseShape<MODE, BM, BN, WM, WN, STAGES, WPS>;
+  const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.ksplit;
+  const int64_t dense = (total + kXcds - 1) / kXcds * kXcds, thin = (int64_t)t[0].units * t[0].ksplit;
+  if (dense <= 0 || thin <= 0 || dense + thin * count > 0x7fffffff) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((sgmv_dense_thin_kernel<T, MODE, S>), dim3((unsigned)(dense + thin * count)), dim3(kThreads), 0, s,
+                     p, t[0], t[count - 1], (int)dense, (int)thin);
+  return hipGetLastError();
+}
+
+template <class T, int MODE>
+hipError_t launch_mode_thin(int cfg, const DenseParams& p, const ThinParams* t, int count, hipStream_t s) {
+  switch (cfg) {
+    case kTile128: return launch_tile_thin<T, MODE, 128, 128, 2, 2, 4, 2>(p, t, count, s);
+    case kTile64: return launch_tile_thin<T, MODE, 64, 128, 1, 4, 6, 2>(p, t, count, s);
+    case kTile32: return launch_tile_thin<T, MODE, 32, 128, 1, 4, 7, 2>(p, t, count, s);
+  }
+  return hipErrorInvalidValue;
+}
+
 template <class T, int MODE>
 hipError_t launch_mode(int cfg, const DenseParams& p, hipStream_t s) {
   switch (cfg) {
     case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 4, 2>(p, s);
     case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 4, 2>(p, s);
-    case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 5, 2>(p, s);
-    case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 6, 2>(p, s);
+    case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 6, 2>(p, s);
+    case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 7, 2>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -466,6 +563,18 @@ hipError_t launch_epilogue_t(int mode, const DenseParams& p, hipStream_t s) {
 hipError_t launch_dense(int dtype, int mode, int cfg, const DenseParams& p, hipStream_t stream) {
   if (p.M <= 0 || p.N <= 0) return hipSuccess;
   return dtype == 1 ? launch_t<BF16>(mode, cfg, p, stream) : launch_t<F16>(mode, cfg, p, stream);
+}
+
+hipError_t launch_dense_thin(int dtype, int mode, int cfg, const DenseParams& p, const ThinParams* t, int count,
+                             hipStream_t stream) {
+  if (p.M <= 0 || p.N <= 0) return hipSuccess;
+  if (mode == kDenseGated)
+    return dtype == 1 ? launch_mode_thin<BF16, kDenseGated>(cfg, p, t, count, stream)
+                      : launch_mode_thin<F16, kDenseGated>(cfg, p, t, count, stream);
+  if (mode == kDenseForward)
+    return dtype == 1 ? launch_mode_thin<BF16, kDenseForward>(cfg, p, t, count, stream)
+                      : launch_mode_thin<F16, kDenseForward>(cfg, p, t, count, stream);
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_dense_epilogue(int dtype, int mode, const DenseParams& p, hipStream_t stream) {

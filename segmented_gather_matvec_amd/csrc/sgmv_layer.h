@@ -23,7 +23,7 @@ struct SegMeta {
 //   out[i, c] += sum_j V[i, j] * E_k[j, c]
 // forward: V = s_k X @ A_k, E_k = B_k; dX: V = s_k dY @ B_k^T, E_k = A_k^T.
 struct LowRankTerm {
-  const float* V;          // [n_rows][rank] fp32, read by the epilogue kernel (null: no term)
+  const float* V;          // [v_planes][n_rows][rank] fp32, read by the epilogue kernel (null: no term)
   const uint16_t* V16;     // [n_rows][2][rank] V's hi, then lo halves, read by the tiles (null: no term)
   const float* row_scale;  // fp16: [n_rows] the power of two that V16's rows are scaled down by
   const uint64_t* ptrs;    // [num_loras] -> B_k [r_k, N], or A_k [N, r_k] for dX
@@ -50,6 +50,8 @@ struct DenseParams {
   int32_t accumulate;    // dW: add to what is there
   int32_t to_planes;     // 1: fp32 partial planes instead of the outputs (ksplit > 1, or a term added by the epilogue kernel)
   int32_t term_in_tile;  // 1: split 0 of every tile adds the LoRA term
+  int32_t v_planes;      // partial planes of term[].V that the epilogue sums
+  const int32_t* row_k;  // [n_rows] LoRA of each covered row (see ThinParams); null: the epilogue searches
   int64_t plane_stride;  // floats between planes of one projection's output (M * N)
   const uint16_t* A[2];
   const uint16_t* B[2];
@@ -58,12 +60,6 @@ struct DenseParams {
   SegMeta meta;
   LowRankTerm term[2];
 };
-
-// cfg: DenseTile of sgmv_layer_shapes.h.
-hipError_t launch_dense(int dtype, int mode, int cfg, const DenseParams& p, hipStream_t stream);
-// Sums the partial planes, adds the LoRA term when term_in_tile is 0, applies
-// the activation (gated) and writes the outputs.
-hipError_t launch_dense_epilogue(int dtype, int mode, const DenseParams& p, hipStream_t stream);
 
 // Thin products of the LoRA term: V[i, :] = s_k Z[i, :] @ D_k for every covered
 // row, with D_k = A_k ([K, r_k]) or B_k^T (B_k [r_k, K], transposed = 1).
@@ -76,11 +72,22 @@ struct ThinParams {
   uint16_t* V16;          // null, or [n_rows][2][rank] hi and lo halves (see LowRankTerm)
   float* row_scale;       // with V16 in fp16: [n_rows]
   float* planes;          // [ksplit][n_rows][rank] (ksplit > 1)
+  int32_t* row_k;         // null, or [n_rows] the LoRA of each covered row, written
   int32_t K, rank, transposed;
   int32_t units, direct;  // units of <= kThinRows rows of one segment
   int32_t ksplit, kc;     // K per split, a multiple of 32
   SegMeta meta;
 };
+// cfg: DenseTile of sgmv_layer_shapes.h.
+hipError_t launch_dense(int dtype, int mode, int cfg, const DenseParams& p, hipStream_t stream);
+// The forward modes' product of at most 128-row tiles together with `count` thin products (of A_k) in one launch;
+// their V stays in partial planes, which the epilogue sums.
+hipError_t launch_dense_thin(int dtype, int mode, int cfg, const DenseParams& p, const ThinParams* t, int count,
+                             hipStream_t stream);
+// Sums the partial planes, adds the LoRA term when term_in_tile is 0, applies
+// the activation (gated) and writes the outputs.
+hipError_t launch_dense_epilogue(int dtype, int mode, const DenseParams& p, hipStream_t stream);
+
 // count products on grid y (at most 2); the plane sum follows when ksplit > 1.
 hipError_t launch_thin(int dtype, const ThinParams* p, int count, hipStream_t stream);
 
@@ -88,7 +95,8 @@ hipError_t launch_thin(int dtype, const ThinParams* p, int count, hipStream_t st
 // stored [C, r_k] (dA_k: Z = X, Q = s_k dY @ B_k^T) or [r_k, C] (dB_k: Z = dY, Q = s_k X @ A_k).
 struct LoraGradParams {
   const uint16_t* Z;      // [n_rows, C]
-  const float* Q;         // [n_rows][rank]
+  const uint16_t* Q;      // [n_rows][2][rank] hi and lo halves (see LowRankTerm)
+  const float* row_scale; // fp16: of Q's rows
   const uint64_t* out;    // [num_loras] -> gradient (0: not wanted)
   const int32_t* ranks;
   float* planes;          // [nsplit][num_loras][C][rank] or [nsplit][num_loras][rank][C] (nsplit > 1)

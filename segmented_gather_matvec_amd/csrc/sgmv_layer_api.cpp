@@ -64,18 +64,18 @@ sgmv::SegMeta seg_meta(const sgmv_problem_t& p, bool lora, const int32_t* seg_in
 }
 
 // V_i = s_k Z_i @ A_k (up = false) or s_k Z_i @ B_k^T (up = true) of every projection.
-// What of each is wanted: fp32 (the LoRA gradients and the epilogue kernel read it), 16-bit halves (the tiles).
-sgmv_status_t thin(const Call& c, bool up, const void* const* Z, bool full, bool halves) {
-  sgmv::ThinParams t[2]{};
+// What of each is wanted: fp32 (the epilogue kernel reads it), 16-bit halves (the tiles and the LoRA gradients).
+void thin_params(const Call& c, bool up, const void* const* Z, bool full, bool halves, sgmv::ThinParams* t) {
   const ThinPlan& plan = up ? c.plan.up : c.plan.down;
   for (int i = 0; i < c.np; ++i) {
+    t[i] = sgmv::ThinParams{};
     t[i].Z = half(Z[i]);
     t[i].ptrs = up ? table(c.proj[i]->B_ptrs) : table(c.proj[i]->A_ptrs);
     t[i].ranks = c.proj[i]->ranks;
     t[i].scales = c.proj[i]->scales;
-    t[i].V = full ? c.at(up ? c.plan.dv_off[i] : c.plan.v_off[i]) : nullptr;
-    t[i].V16 = halves ? reinterpret_cast<uint16_t*>(c.at(c.plan.half_off[i])) : nullptr;
-    t[i].row_scale = c.at(c.plan.row_scale_off[i]);
+    t[i].V = full ? c.at(c.plan.v_off[up][i]) : nullptr;
+    t[i].V16 = halves ? reinterpret_cast<uint16_t*>(c.at(c.plan.half_off[up][i])) : nullptr;
+    t[i].row_scale = c.at(c.plan.row_scale_off[up][i]);
     t[i].planes = c.at(c.plan.thin_off[i]);
     t[i].K = up ? c.p.h_out : c.p.h_in;
     t[i].rank = c.p.rank;
@@ -86,6 +86,11 @@ sgmv_status_t thin(const Call& c, bool up, const void* const* Z, bool full, bool
     t[i].kc = plan.kc;
     t[i].meta = c.meta;
   }
+}
+
+sgmv_status_t thin(const Call& c, bool up, const void* const* Z, bool full, bool halves) {
+  sgmv::ThinParams t[2];
+  thin_params(c, up, Z, full, halves, t);
   return sgmv::launch_thin(c.p.dtype, t, c.np, c.stream) == hipSuccess ? SGMV_OK : SGMV_ERR_HIP;
 }
 
@@ -108,18 +113,19 @@ sgmv::DenseParams dense_params(const Call& c, const DensePlan& d, int64_t M, int
   q.to_planes = d.to_planes;
   q.term_in_tile = d.term_in_tile;
   q.plane_stride = M * N;
+  q.v_planes = 1;
   q.planes = c.at(c.plan.planes_off);
   q.meta = c.meta;
   return q;
 }
 
-sgmv::LowRankTerm term(const Call& c, int i, size_t v_off, const void* ptrs) {
+sgmv::LowRankTerm term(const Call& c, int i, bool up, const void* ptrs) {
   sgmv::LowRankTerm t{};
   if (c.plan.out.term_in_tile) {
-    t.V16 = reinterpret_cast<const uint16_t*>(c.at(c.plan.half_off[i]));
-    t.row_scale = c.at(c.plan.row_scale_off[i]);
+    t.V16 = reinterpret_cast<const uint16_t*>(c.at(c.plan.half_off[up][i]));
+    t.row_scale = c.at(c.plan.row_scale_off[up][i]);
   } else {
-    t.V = c.at(v_off);
+    t.V = c.at(c.plan.v_off[up][i]);
   }
   t.ptrs = table(ptrs);
   t.ranks = c.proj[i]->ranks;
@@ -133,20 +139,33 @@ sgmv_status_t run_dense(const Call& c, int mode, const DensePlan& d, const sgmv:
 }
 
 sgmv_status_t forward(const Call& c, void* const* out) {
-  if (c.plan.lora) {
-    const void* Z[2] = {c.X, c.X};
+  const void* Z[2] = {c.X, c.X};
+  if (c.plan.lora && !c.plan.one_launch) {
     const sgmv_status_t st = thin(c, false, Z, !c.plan.out.term_in_tile, c.plan.out.term_in_tile);
     if (st != SGMV_OK) return st;
   }
   const bool gated = layer_gated(c.op);
+  const int mode = gated ? sgmv::kDenseGated : sgmv::kDenseForward;
   sgmv::DenseParams q = dense_params(c, c.plan.out, c.p.n_rows, c.p.h_out, c.p.h_in, c.p.h_in, c.p.h_out);
   q.A[0] = half(c.X);
   for (int i = 0; i < c.np; ++i) {
     q.B[i] = half(c.W[i]);
-    if (c.plan.lora) q.term[i] = term(c, i, c.plan.v_off[i], c.proj[i]->B_ptrs);
+    if (c.plan.lora) q.term[i] = term(c, i, false, c.proj[i]->B_ptrs);
   }
   for (int i = 0; i < (gated ? 3 : 1); ++i) q.out[i] = static_cast<uint16_t*>(out[i]);
-  return run_dense(c, gated ? sgmv::kDenseGated : sgmv::kDenseForward, c.plan.out, q);
+  if (!c.plan.one_launch) return run_dense(c, mode, c.plan.out, q);
+  sgmv::ThinParams t[2];
+  thin_params(c, false, Z, true, false, t);
+  int32_t* row_k = reinterpret_cast<int32_t*>(c.at(c.plan.row_k_off));
+  q.row_k = row_k;
+  q.v_planes = c.plan.down.ksplit;
+  for (int i = 0; i < c.np; ++i) {
+    t[i].row_k = row_k;
+    if (q.v_planes > 1) q.term[i].V = t[i].planes;
+  }
+  if (sgmv::launch_dense_thin(c.p.dtype, mode, c.plan.out.cfg, q, t, c.np, c.stream) != hipSuccess) return SGMV_ERR_HIP;
+  if (sgmv::launch_dense_epilogue(c.p.dtype, mode, q, c.stream) != hipSuccess) return SGMV_ERR_HIP;
+  return SGMV_OK;
 }
 
 sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgmv_projection_grad_t* const* grad,
@@ -159,12 +178,12 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
   }
   if (c.plan.lora && want_b) {
     const void* Z[2] = {c.X, c.X};
-    const sgmv_status_t st = thin(c, false, Z, true, false);
+    const sgmv_status_t st = thin(c, false, Z, false, true);
     if (st != SGMV_OK) return st;
   }
   if (c.plan.lora && (want_a || dX)) {
-    const bool halves = dX && c.plan.out.term_in_tile;
-    const sgmv_status_t st = thin(c, true, dY, want_a || !halves, halves);
+    const bool full = dX && !c.plan.out.term_in_tile;
+    const sgmv_status_t st = thin(c, true, dY, full, want_a || !full);
     if (st != SGMV_OK) return st;
   }
   if (dX && rows) {
@@ -173,7 +192,7 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
     for (int i = 0; i < c.np; ++i) {
       q.A[i] = half(dY[i]);
       q.B[i] = half(c.W[i]);
-      if (c.plan.lora) q.term[i] = term(c, i, c.plan.dv_off[i], c.proj[i]->A_ptrs);
+      if (c.plan.lora) q.term[i] = term(c, i, true, c.proj[i]->A_ptrs);
     }
     q.out[0] = static_cast<uint16_t*>(dX);
     const sgmv_status_t st = run_dense(c, sgmv::kDenseDx, c.plan.out, q);
@@ -204,7 +223,8 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
       if (!out) continue;
       sgmv::LoraGradParams& e = g[count];
       e.Z = half(b ? dY[i] : c.X);
-      e.Q = c.at(b ? c.plan.v_off[i] : c.plan.dv_off[i]);
+      e.Q = reinterpret_cast<const uint16_t*>(c.at(c.plan.half_off[!b][i]));
+      e.row_scale = c.at(c.plan.row_scale_off[!b][i]);
       e.out = table(out);
       e.ranks = c.proj[i]->ranks;
       e.planes = c.at(c.plan.planes_off) + (size_t)count * nsplit * c.p.num_loras * C * c.p.rank;

@@ -86,9 +86,11 @@ int plan_grad_split(const sgmv_problem_t& p, int64_t C, int products) {
   const int64_t wgs = (int64_t)p.num_loras * ceil_div(C, sgmv::kLoraGradCols) * products;
   const int64_t bytes = (int64_t)p.num_loras * C * p.rank * 4 * products;
   const int64_t fill = ceil_div(1024, std::max<int64_t>(1, wgs));
-  const int64_t steps = ceil_div(p.n_rows, 4 * sgmv::kLoraGradRows);  // at least four steps each
-  const int64_t longest = ceil_div(p.max_seg_len, 32 * sgmv::kLoraGradRows);  // one long segment alone
-  const int64_t n = std::min<int64_t>({std::max(fill, longest), steps, kGradPlaneBytes / std::max<int64_t>(1, bytes), 64});
+  const int64_t steps = ceil_div(p.n_rows, 4 * sgmv::kDenseK);  // at least four steps each
+  const int64_t longest = ceil_div(p.max_seg_len, 32 * sgmv::kDenseK);  // one long segment alone
+  // The planes are written and read once each: no more of them than Z has bytes.
+  const int64_t cheap = p.n_rows / std::max<int64_t>(1, 4 * (int64_t)p.num_loras * p.rank);
+  const int64_t n = std::min<int64_t>({std::max(fill, longest), steps, cheap, kGradPlaneBytes / std::max<int64_t>(1, bytes), 64});
   return (int)std::max<int64_t>(1, n);
 }
 
@@ -115,10 +117,11 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
       planes = std::max(planes, l.up.plane_bytes);
     }
     for (int i = 0; i < l.projections; ++i) {
-      l.v_off[i] = take(v);
-      if (back) l.dv_off[i] = take(v);
-      l.half_off[i] = take(v);  // two 16-bit halves a value
-      l.row_scale_off[i] = take((size_t)n * sizeof(float));
+      for (int d = 0; d < (back ? 2 : 1); ++d) {
+        l.v_off[d][i] = take(v);
+        l.half_off[d][i] = take(v);  // two 16-bit halves a value
+        l.row_scale_off[d][i] = take((size_t)n * sizeof(float));
+      }
       l.thin_off[i] = take(planes);
     }
   }
@@ -126,13 +129,16 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
     for (int i = 0; i < 2; ++i) l.gate_off[i] = take((size_t)n * p.h_out * 2);
   // The LoRA term joins in the tiles where segments are long enough for a
   // matrix instruction's 16 rows; else the epilogue launch adds it row by row.
-  const bool in_tile = l.lora && n >= (int64_t)kShortRun * p.num_segs;
+  const bool in_tile = l.lora && n > 128 && n >= (int64_t)kShortRun * p.num_segs;
   const int64_t M = n, N = back ? p.h_in : p.h_out;
   const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK);
   const int cols = op == SGMV_GATED_FORWARD ? 2 : 1;
   l.out = plan_dense(M, N, kt * (op == SGMV_GATED_BACKWARD ? 2 : 1), cols, true);
   l.out.term_in_tile = in_tile ? 1 : 0;
   l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile);
+  // (The largest tile's workgroups are too big to share a launch with.)
+  l.one_launch = l.lora && !back && l.out.to_planes && !in_tile && l.out.cfg != sgmv::kTile256;
+  if (l.one_launch) l.row_k_off = take((size_t)n * sizeof(int32_t));
   if (l.out.to_planes) l.out.plane_bytes = (size_t)l.out.ksplit * M * N * cols * sizeof(float);
   size_t area = l.out.plane_bytes;
   if (back) {

@@ -19,6 +19,5 @@ constexpr int dense_tile_cols(int t) { return t == kTile256 ? 256 : 128; }
 
 constexpr int kThinRows = 64;      // rows of one segment per thin-product workgroup
 constexpr int kLoraGradCols = 256; // columns of X or dY per LoRA-gradient workgroup
-constexpr int kLoraGradRows = 32;  // rows per step
 
 }  // namespace sgmv

@@ -7,124 +7,16 @@
 // dV = s_k dy@B_k^T:
 //     dx  += dV @ A_k^T,   dA_k = sum_i x_i^T dV_i,   dB_k = sum_i V_i^T dy_i.
 // All of them read a [rows, thousands] operand once and are bound by memory.
-#include "sgmv_tile.h"
+#include "sgmv_thin.h"
 
 namespace sgmv {
 namespace {
 
 // ---------------------------------------------------------------- thin products
-// Eight ranks c .. c+7 of row `row` of V, as fp32 and / or as hi + lo halves.
-// The rank / 8 lanes of one row are neighbours and all come here.
-template <class T>
-__device__ inline void store_v(const ThinParams& p, int row, int c, float (&v)[8]) {
-  if (p.V != nullptr) {
-    float* dst = p.V + (int64_t)row * p.rank + c;
-    *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
-    *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
-  }
-  if (p.V16 == nullptr) return;
-  // fp16 halves hold V only below 65504: a row with a value beyond 32768 is kept
-  // scaled down by a power of two (exact), which the reader puts back.
-  if constexpr (T::kMaxFinite < 1e6f) {
-    float big = 0.f, up = 1.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(v[e]));
-    for (int d = 1; d < p.rank / 8; d <<= 1) big = fmaxf(big, shfl_xor(big, d));
-    if (big > 32768.f && big < 3.4e38f) {
-      const int e = ((int)(__float_as_uint(big) >> 23) & 255) - 127 - 14;  // 1 .. 113
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] *= down;
-    }
-    if (c == 0) p.row_scale[row] = up;
-  }
-  u32x4 hi, lo;
-  split8<T>(v, hi, lo);
-  uint16_t* dst = p.V16 + (int64_t)row * 2 * p.rank + c;
-  store_vec(dst, hi);
-  store_vec(dst + p.rank, lo);
-}
-
-// Workgroup (unit, split): up to 64 rows of one segment (16 per wave) times the
-// LoRA's D_k over kc contraction steps; both operands stream through a ring of
-// LDS slots (sgmv_tile.h).  Bound by reading Z.
 template <class T, int JT, bool TRANSPOSED>
 __global__ __launch_bounds__(kThreads) void sgmv_thin_kernel(ThinParams p0, ThinParams p1) {
-  const ThinParams& p = blockIdx.y ? p1 : p0;
-  constexpr int COLS = JT * 16, STAGES = 6, kPerStep = 2;
-  constexpr int B0 = kThinRows * kDenseK, SLOT = (kThinRows + COLS) * kDenseK;
-  constexpr int RST = COLS + 4;  // row stride of the result in LDS (floats)
-  static_assert(STAGES * SLOT * 2 >= kThinRows * RST * 4, "the result fits the ring");
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES * SLOT];
-  const int t = threadIdx.x;
-  const int lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int q = lane >> 4, ml = lane & 15;
-  const int u = (int)blockIdx.x / p.ksplit;
-  const int g = (int)blockIdx.x - u * p.ksplit;
-  const Unit un = resolve_unit<kThinRows>(p.meta.seg_indptr, p.meta.lora_idx, p.meta.num_segs, p.meta.num_loras,
-                                          p.meta.n_rows, p.direct, u);
-  if (un.L <= 0) return;
-  const uint16_t* D = reinterpret_cast<const uint16_t*>(p.ptrs[un.k]);
-  const int rk = D != nullptr ? rank_of(p.ranks, p.rank, un.k) : 0;
-  const float scale = p.scales != nullptr ? p.scales[un.k] : 1.f;
-  const int k0 = g * p.kc;
-  const int k1 = p.K < k0 + p.kc ? p.K : k0 + p.kc;
-  const int steps = rk > 0 ? (k1 - k0 + kDenseK - 1) / kDenseK : 0;
-
-  f32x4 acc[JT];
-#pragma unroll
-  for (int j = 0; j < JT; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (steps > 0) {
-    TileLoader<kThinRows, 1, false> la;
-    TileLoader<COLS, 1, !TRANSPOSED> lb;  // fewer pieces than waves: some load the same piece twice
-    const int ldd = TRANSPOSED ? p.K : rk;
-    la.init(wave, lane, p.K);
-    lb.init(wave, lane, ldd);
-    la.start(p.Z + (int64_t)un.r0 * p.K, p.K, 0, un.L, k0, k1);
-    lb.start(D, ldd, 0, rk, k0, k1);
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-      la.issue(lds + s * SLOT);
-      lb.issue(lds + s * SLOT + B0);
-    }
-    int slot = 0;
-    for (int s = 0; s < steps; ++s) {
-      wait_loads_and_lds<kPerStep*(STAGES - 2)>();
-      __builtin_amdgcn_s_barrier();
-      uint16_t* refill = lds + (slot == 0 ? STAGES - 1 : slot - 1) * SLOT;  // read in the step before this one
-      la.issue(refill);
-      lb.issue(refill + B0);
-      const uint16_t* now = lds + slot * SLOT;
-      const u32x4 z = read_operand<kThinRows, false>(now, wave * 16, lane);
-#pragma unroll
-      for (int j = 0; j < JT; ++j)
-        acc[j] = mfma<T>(read_operand<COLS, !TRANSPOSED>(now + B0, j * 16, lane), z, acc[j]);
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
-    }
-    wait_loads_and_lds<0>();
-  }
-  __syncthreads();
-  // acc[j][e]: row 16 wave + ml, rank 16 j + 4 q + e.
-  float* res = reinterpret_cast<float*>(lds);
-#pragma unroll
-  for (int j = 0; j < JT; ++j) *reinterpret_cast<f32x4*>(&res[(wave * 16 + ml) * RST + j * 16 + q * 4]) = acc[j];
-  __syncthreads();
-  const int per_row = p.rank / 8;
-  for (int x = t; x < un.L * per_row; x += kThreads) {
-    const int r = x / per_row, c = (x - r * per_row) * 8;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c < rk ? res[r * RST + c + e] * scale : 0.f;
-    if (p.ksplit > 1) {
-      float* dst = p.planes + ((int64_t)g * p.meta.n_rows + un.r0 + r) * p.rank + c;
-      *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-      store_v<T>(p, un.r0 + r, c, v);
-    }
-  }
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[ThinShape<JT>::LDS];
+  thin_body<T, JT, TRANSPOSED>(blockIdx.y ? p1 : p0, (int)blockIdx.x, lds);
 }
 
 // V = sum of the planes, in plane order (rows no segment covers hold anything;
@@ -150,42 +42,49 @@ __global__ __launch_bounds__(kThreads) void sgmv_thin_sum_kernel(ThinParams p0, 
 }
 
 // ---------------------------------------------------------------- gradients of A_k and B_k
-// Workgroup (column tile, LoRA k, split z): 256 columns of Z, 64 per wave;
-// walks the rows of every segment of LoRA k in steps of 32, every nsplit-th
-// step its own.  The contraction index is the row, so Z's tile is kept as it
-// lies and read with the transposing read; Q (fp32) is split into hi + lo
-// halves, stored rank by rank.  fp16 halves need |Q| < 65504: the sums run at a
-// power-of-two scale that shrinks when a step's Q would not fit.
-template <class T, int JT>
+// Workgroup (column tile, LoRA k, split z): 256 columns of Z, 64 per wave; walks
+// the rows of every segment of LoRA k in steps of 32, every nsplit-th step its
+// own.  The contraction index is the row, so both operands (Z, and V16's rows
+// [hi | lo]) are kept as they lie and read with the transposing read; they
+// stream through a ring of LDS slots (sgmv_tile.h).  Bound by reading Z.
+// fp16 rows of V16 may be kept scaled down by a power of two each: then the sums run
+// in units of the largest scale so far.
+template <class T, int R>
 __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradParams p0, LoraGradParams p1) {
-  const int ctiles = (p0.C + kLoraGradCols - 1) / kLoraGradCols;
+  constexpr int ROWS = kDenseK, COLS = kLoraGradCols, QC = 2 * R, JT = R < 16 ? 1 : R / 16;
+  constexpr int STAGES = R == 64 ? 3 : 4;  // two workgroups per CU
+  constexpr bool F16T = T::kMaxFinite < 1e6f;
+  constexpr int LZ = COLS / 16 / kWaves, LQ = QC / 16 < kWaves ? 1 : QC / 16 / kWaves;
+  constexpr int B0 = COLS * ROWS, S0 = B0 + QC * ROWS, SLOT = S0 + (F16T ? 128 : 0);  // Z, V16, row scales
+  constexpr int kPerStep = LZ + LQ + (F16T ? 1 : 0);
+  const int ctiles = (p0.C + COLS - 1) / COLS;
   const int k = (int)blockIdx.x / ctiles;
   const LoraGradParams& p = blockIdx.y ? p1 : p0;
-  constexpr int ROWS = kLoraGradRows, COLS = kLoraGradCols, ZST = COLS + 16, QST = ROWS + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t lds_z[ROWS * ZST];
-  __shared__ __attribute__((aligned(16))) uint16_t lds_q[2][JT * 16 * QST];
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES * SLOT];
   __shared__ int lds_lo[kThreads], lds_hi[kThreads];
   __shared__ int lds_count[kWaves];
-  __shared__ float lds_max[kWaves];
   const int t = threadIdx.x;
   const int lane = t & 63;
-  const int wave = t >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int q = lane >> 4, ml = lane & 15;
   const int c0 = ((int)blockIdx.x - k * ctiles) * COLS;
   const int z = (int)blockIdx.z;
-  const int R = p.rank;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out[k]);
   const int rk = rank_of(p.ranks, R, k);
   if (out == nullptr || rk <= 0) return;
 
+  TileLoader<COLS, LZ, true> lz;
+  TileLoader<QC, LQ, true> lq;
+  lz.init(wave, lane, p.C);
+  lq.init(wave, lane, QC);
   f32x4 acc[4][JT];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float scale = 1.f;  // of the sums (fp16 only)
-  bool any = false;   // LoRA k has rows
-  int counter = 0;    // steps of 32 rows so far, over all of its segments
+  float unit = 1.f;  // of the sums (fp16 only)
+  bool any = false;  // LoRA k has rows
+  int counter = 0;   // steps of 32 rows so far, over all of its segments
 
   for (int s0 = 0; s0 < p.meta.num_segs; s0 += kThreads) {
     // The window's segments of LoRA k, in order.
@@ -212,109 +111,112 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradParams
       lds_hi[at] = hi;
     }
     __syncthreads();
+    count = __builtin_amdgcn_readfirstlane(count);
     any = any || count > 0;
-    for (int e = 0; e < count; ++e) {
-      const int lo_e = lds_lo[e], hi_e = lds_hi[e];
-      const int steps = (hi_e - lo_e + ROWS - 1) / ROWS;
-      // First step of this segment that is this split's.
-      int st = (z - counter % p.nsplit + p.nsplit) % p.nsplit;
-      counter += steps;
-      for (; st < steps; st += p.nsplit) {
-        const int r0 = lo_e + st * ROWS;
-        const int L = hi_e - r0 < ROWS ? hi_e - r0 : ROWS;
-        // Z: 32 rows x 32 vectors of 8 columns, 4 per thread; rows past the segment are zero.
-        u32x4 zv[4];
+    // This split's steps of the window, in order: step st of segment e, which has `steps`.
+    int e = -1, st = z - counter % p.nsplit, row = 0, end = 0, steps = 0, mine = 0;
+    if (st < 0) st += p.nsplit;
+    {
+      int all = 0;
+      for (int x = lane; x < count; x += 64) all += (lds_hi[x] - lds_lo[x] + ROWS - 1) / ROWS;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int r = (t >> 5) + 8 * x, c = c0 + (t & 31) * 8;
-          const bool ok = r < L && c < p.C;
-          zv[x] = load_vec(p.Z + (ok ? (int64_t)(r0 + r) * p.C + c : 0));
-          if (!ok) zv[x] = u32x4{0u, 0u, 0u, 0u};
+      for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
+      all = __builtin_amdgcn_readfirstlane(all);
+      mine = all > st ? (all - st + p.nsplit - 1) / p.nsplit : 0;
+      counter += all;
+    }
+    auto issue = [&](uint16_t* slot) {
+      while (st >= steps && e < count) {  // on to the segment that holds step st
+        st -= steps;
+        steps = 0;
+        if (++e < count) {
+          row = __builtin_amdgcn_readfirstlane(lds_lo[e]);
+          end = __builtin_amdgcn_readfirstlane(lds_hi[e]);
+          steps = (end - row + ROWS - 1) / ROWS;
         }
-        // Q: 32 rows x R values; thread t takes row t % 32, ranks (t / 32) * 2 JT ...
-        float qv[2 * JT];
-        float big = 0.f;
+      }
+      const int r0 = e < count ? row + st * ROWS : 0;
+      const int n = e < count ? (end - r0 < ROWS ? end - r0 : ROWS) : 0;
+      lz.issue_rows(p.Z, p.C, c0, p.C, r0, n, slot);
+      lq.issue_rows(p.Q, QC, 0, QC, r0, n, slot + B0);
+      if constexpr (F16T) {
+        const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p.row_scale + r0), 0, n * 4, kRawBuffer);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(slot + S0), 4, lane * 4, 0, 0, 0);
+      }
+      st += p.nsplit;
+    };
+    if (mine > 0) {
 #pragma unroll
-        for (int x = 0; x < 2 * JT; ++x) {
-          const int r = t & 31, j = (t >> 5) * 2 * JT + x;
-          const bool ok = r < L && j < rk;
-          const float v = p.Q[ok ? (int64_t)(r0 + r) * R + j : 0];
-          qv[x] = ok ? v : 0.f;
-          big = fmaxf(big, fabsf(qv[x]));
-        }
-        if constexpr (T::kMaxFinite < 1e6f) {
+      for (int x = 0; x < STAGES - 1; ++x) issue(lds + x * SLOT);
+      int slot = 0;
+      for (int x = 0; x < mine; ++x) {
+        wait_loads_and_lds<kPerStep*(STAGES - 2)>();
+        __builtin_amdgcn_s_barrier();
+        issue(lds + (slot == 0 ? STAGES - 1 : slot - 1) * SLOT);
+        const uint16_t* now = lds + slot * SLOT;
+        u32x4 zf[4], qf[QC / 16];
 #pragma unroll
-          for (int d = 1; d < 64; d <<= 1) big = fmaxf(big, shfl_xor(big, d));
-          if (lane == 0) lds_max[wave] = big;
-        }
-        __syncthreads();  // the last step's tiles are read, the maxima are in
-        if constexpr (T::kMaxFinite < 1e6f) {
-          big = 0.f;
+        for (int i = 0; i < 4; ++i) zf[i] = read_operand<COLS, true>(now, wave * 64 + i * 16, lane);
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) big = fmaxf(big, lds_max[w]);
-          if (big * scale > 32768.f && big < 3.4e38f) {
-            const int ex = ((int)(__float_as_uint(big) >> 23) & 255) - 127 - 14;
-            const float next = __uint_as_float((uint32_t)(127 - ex) << 23);
-            const float f = next / scale;
+        for (int j = 0; j < QC / 16; ++j) qf[j] = read_operand<QC, true>(now + B0, j * 16, lane);
+        if constexpr (F16T) {
+          // Rows 8 q .. 8 q + 7 are this lane's contraction steps.
+          const float* sp = reinterpret_cast<const float*>(now + S0) + q * 8;
+          const f32x4 u0 = *reinterpret_cast<const f32x4*>(sp), u1 = *reinterpret_cast<const f32x4*>(sp + 4);
+          float big = fmaxf(fmaxf(fmaxf(u0[0], u0[1]), fmaxf(u0[2], u0[3])), fmaxf(fmaxf(u1[0], u1[1]), fmaxf(u1[2], u1[3])));
+          big = fmaxf(big, shfl_xor(big, 16));
+          big = fmaxf(big, shfl_xor(big, 32));
+          if (big > 1.f || unit > 1.f) {  // uniform over the wave
+            if (big > unit) {
+              const float f = unit / big;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+              for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int j = 0; j < JT; ++j) acc[i][j] *= f;
-            scale = next;
-          }
+                for (int j = 0; j < JT; ++j) acc[i][j] *= f;
+              unit = big;
+            }
+            float f[8];
 #pragma unroll
-          for (int x = 0; x < 2 * JT; ++x) qv[x] *= scale;
-        }
+            for (int x8 = 0; x8 < 8; ++x8) f[x8] = (x8 < 4 ? u0[x8 & 3] : u1[x8 & 3]) / unit;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) store_vec(&lds_z[((t >> 5) + 8 * x) * ZST + (t & 31) * 8], zv[x]);
+            for (int j = 0; j < QC / 16; ++j) {
+              float v[8];
+              unpack8<T>(qf[j], v);
 #pragma unroll
-        for (int x = 0; x < 2 * JT; ++x) {
-          uint16_t h, l;
-          split_hi_lo<T>(qv[x], h, l);
-          const int a = ((t >> 5) * 2 * JT + x) * QST + (t & 31);
-          lds_q[0][a] = h;
-          lds_q[1][a] = l;
-        }
-        __syncthreads();
-        u32x4 qh[JT], ql[JT];
-#pragma unroll
-        for (int j = 0; j < JT; ++j) {
-          qh[j] = load_vec(&lds_q[0][(j * 16 + ml) * QST + q * 8]);
-          ql[j] = load_vec(&lds_q[1][(j * 16 + ml) * QST + q * 8]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint16_t* a = &lds_z[(q * 8 + (ml >> 2)) * ZST + wave * 64 + i * 16 + (ml & 3) * 4];
-          const u32x2 l2 = read_transposed(a), h2 = read_transposed(a + 4 * ZST);
-          const u32x4 zf = {l2[0], l2[1], h2[0], h2[1]};
-#pragma unroll
-          for (int j = 0; j < JT; ++j) {
-            // rank_major: lane holds 4 columns of one rank; else 4 ranks of one column
-            if (p.rank_major) {
-              acc[i][j] = mfma<T>(zf, ql[j], acc[i][j]);
-              acc[i][j] = mfma<T>(zf, qh[j], acc[i][j]);
-            } else {
-              acc[i][j] = mfma<T>(ql[j], zf, acc[i][j]);
-              acc[i][j] = mfma<T>(qh[j], zf, acc[i][j]);
+              for (int x8 = 0; x8 < 8; ++x8) v[x8] = f[x8] > 0.f ? v[x8] * f[x8] : v[x8];
+              qf[j] = pack8<T>(v);
             }
           }
         }
+        // rank_major: lane holds 4 columns of one rank; else 4 ranks of one column.
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = QC / 16 - 1; j >= 0; --j) {  // lo halves first
+            f32x4& a = acc[i][j % JT];
+            a = p.rank_major ? mfma<T>(zf[i], qf[j], a) : mfma<T>(qf[j], zf[i], a);
+          }
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
       }
+      wait_loads_and_lds<0>();
     }
-    __syncthreads();  // the list is read before the next window overwrites it
+    __syncthreads();  // the list and the slots are read before the next window overwrites them
   }
   // A LoRA without rows keeps what it has when gradients accumulate.
   if (p.accumulate && !any) return;
-  const float inv = 1.f / scale;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
       const int c = c0 + wave * 64 + i * 16 + (p.rank_major ? q * 4 : ml);
       const int r = j * 16 + (p.rank_major ? ml : q * 4);
-      if (c >= p.C || r >= rk) continue;
       f32x4 v = acc[i][j];
-      if constexpr (T::kMaxFinite < 1e6f) v *= inv;
+      if constexpr (R == 8) {  // ranks 8..15 are the lo halves' sums of ranks 0..7
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] += p.rank_major ? shfl_xor(v[x], 8) : shfl_xor(v[x], 32);
+      }
+      if (c >= p.C || r >= rk) continue;
+      if constexpr (F16T) v *= unit;
       if (p.nsplit > 1) {
         float* dst = p.planes + ((int64_t)z * p.meta.num_loras + k) * p.C * R +
                      (p.rank_major ? (int64_t)r * p.C + c : (int64_t)c * R + r);
@@ -436,10 +338,10 @@ hipError_t launch_lora_grad_t(const LoraGradParams* p, int count, hipStream_t s)
   if (tiles > 0x7fffffff || blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid((unsigned)tiles, (unsigned)count, (unsigned)a.nsplit);
   switch (a.rank) {
-    case 8:
-    case 16: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 1>), grid, dim3(kThreads), 0, s, a, b); break;
-    case 32: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 2>), grid, dim3(kThreads), 0, s, a, b); break;
-    case 64: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 4>), grid, dim3(kThreads), 0, s, a, b); break;
+    case 8: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 8>), grid, dim3(kThreads), 0, s, a, b); break;
+    case 16: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 16>), grid, dim3(kThreads), 0, s, a, b); break;
+    case 32: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 32>), grid, dim3(kThreads), 0, s, a, b); break;
+    case 64: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 64>), grid, dim3(kThreads), 0, s, a, b); break;
     default: return hipErrorInvalidValue;
   }
   hipError_t e = hipGetLastError();

@@ -69,6 +69,18 @@ struct TileLoader {
       full = (uint32_t)((rows - r0 < R ? rows - r0 : R) * ld - k0) * 2u;
     }
   }
+  // One step of an operand stored with the contraction index as row: `n` rows (0: none, the slot is
+  // filled with zeros) from row `row` on, from column r0 of `cols`.
+  __device__ inline void issue_rows(const uint16_t* operand, int ld, int r0, int cols, int row, int n,
+                                    uint16_t* lds) const {
+    static_assert(T, "row-wise steps");
+    const uint32_t bytes = n > 0 ? (uint32_t)((n - 1) * ld + (cols - r0)) * 2u : 0u;
+    const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(operand + (int64_t)row * ld + r0), 0,
+                                                      (int)bytes, kRawBuffer);
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + lds_off[j]), 16, (int)voff[j], 0, 0, 0);
+  }
   // Loads the next step into an LDS slot.  Past the last contraction index every
   // lane is out of range: nothing is fetched and the slot is filled with
   // zeros, so that each step counts the same loads.
