@@ -366,127 +366,166 @@ __global__ __launch_bounds__(kThreads, S::WAVES_PER_SIMD) void sgmv_dense_thin_k
 }
 
 // ---------------------------------------------------------------- epilogue of the partial planes
-// One wave per (row i, 512 columns): lane l owns columns c .. c+7.  Sums the
+// One wave per (row i, 256 columns): lane l owns columns c .. c+3.  Sums the
 // planes in plane order; when the tiles did not add the LoRA term, adds
 // V[i] @ E_k with vector FMA in fp32 (short segments: a row brings its own E_k).
-template <class T, int MODE>
-__device__ inline void plane_sum(const DenseParams& p, int proj, int64_t o, float (&y)[8]) {
-  constexpr int kBatch = 4;
+// Bound by the latency of its dependent loads: the first kPlanes planes, V's planes and
+// the row's LoRA are all asked for before any of them is waited for, then 16 ranks of E_k of both terms.
+// (Eight columns per lane and four planes at a time took 11.2 us for one gated row of 11008, against
+// 4.6 us for a dense row of 4096.)
+constexpr int kPlanes = 8;
+constexpr int kEpilogueCols = 256;
+typedef const __attribute__((address_space(1))) u32x2* global_u32x2_ptr;
+struct PlaneBatch {
+  f32x4 a[kPlanes];
+};
+__device__ inline void load_planes(const DenseParams& p, int proj, int64_t o, int g0, PlaneBatch& x) {
   const float* src = p.planes + (int64_t)proj * p.ksplit * p.plane_stride + o;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] = 0.f;
-  for (int g0 = 0; g0 < p.ksplit; g0 += kBatch) {
-    f32x4 a[kBatch], b[kBatch];
+  for (int u = 0; u < kPlanes; ++u)
+    x.a[u] = *reinterpret_cast<const f32x4*>(src + (int64_t)(g0 + u < p.ksplit ? g0 + u : p.ksplit - 1) * p.plane_stride);
+}
+// y = the sum of all planes; x holds the first kPlanes of them.
+__device__ inline void plane_sum(const DenseParams& p, int proj, int64_t o, PlaneBatch& x, f32x4& y) {
+  y = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int g0 = 0; g0 < p.ksplit; g0 += kPlanes) {
+    if (g0 > 0) load_planes(p, proj, o, g0, x);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int64_t g = g0 + u < p.ksplit ? g0 + u : p.ksplit - 1;
-      a[u] = *reinterpret_cast<const f32x4*>(src + g * p.plane_stride);
-      b[u] = *reinterpret_cast<const f32x4*>(src + g * p.plane_stride + 4);
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
+    for (int u = 0; u < kPlanes; ++u) {
       const bool live = g0 + u < p.ksplit;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] = live ? y[e] + a[u][e] : y[e];
-        y[4 + e] = live ? y[4 + e] + b[u][e] : y[4 + e];
-      }
+      for (int e = 0; e < 4; ++e) y[e] = live ? y[e] + x.a[u][e] : y[e];
     }
   }
 }
 
-// v: V[i] of this row (LDS); E: the LoRA's B_k (A_k for dX).
+// Ranks j0 .. j0+15 of E_k over the lane's four columns.  Forward, B_k [r_k, N]: m[w] is rank
+// j0 + w (half a vector each).  dX, A_k [N, r_k]: m[2 w], m[2 w + 1] are the ranks of column c + w.
+template <int MODE>
+__device__ inline void load_rows(const DenseParams& p, const uint16_t* E, int rk, int c, int j0, u32x2 (&m)[16]) {
+#pragma unroll
+  for (int w = 0; w < 16; ++w) {
+    const int r = MODE == kDenseDx ? j0 + (w & 3) * 4 : j0 + w;
+    const int64_t at = MODE == kDenseDx ? (int64_t)(c + w / 4) * rk + r : (int64_t)r * p.N + c;
+    m[w] = __builtin_nontemporal_load((global_u32x2_ptr)(E + (r < rk ? at : 0)));
+  }
+}
+// y += V[i] @ E_k; v: V[i] (LDS); m: ranks 0 .. 15 of E_k.
 template <class T, int MODE>
-__device__ inline void row_term(const DenseParams& p, const float* v, const uint16_t* E, int rk, int c, float (&y)[8]) {
-  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int j = 0; j < rk; j += 8) {
-    u32x4 m[8];  // forward: B_k [r_k, N], ranks j .. j+7; dX: A_k [N, r_k], columns c .. c+7
+__device__ inline void row_term(const DenseParams& p, const float* v, const uint16_t* E, int rk, int c, u32x2 (&m)[16],
+                                f32x4& y) {
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < rk; j0 += 16) {
+    if (j0 > 0) load_rows<MODE>(p, E, rk, c, j0, m);
 #pragma unroll
-    for (int w = 0; w < 8; ++w)
-      m[w] = load_stream(MODE == kDenseDx ? E + (int64_t)(c + w) * rk + j : E + (int64_t)(j + w) * p.N + c);
-    const f32x4 v0 = *reinterpret_cast<const f32x4*>(v + j), v1 = *reinterpret_cast<const f32x4*>(v + j + 4);
+    for (int w = 0; w < 16; ++w) {
+      const int r = MODE == kDenseDx ? j0 + (w & 3) * 4 : j0 + w;
+      if (r >= rk) continue;  // uniform
+      const float f[4] = {T::lo(m[w][0]), T::hi(m[w][0]), T::lo(m[w][1]), T::hi(m[w][1])};
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      float f[8];
-      unpack8<T>(m[w], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
+      for (int e = 0; e < 4; ++e) {
         if constexpr (MODE == kDenseDx)
-          s[w] = __builtin_fmaf(e < 4 ? v0[e & 3] : v1[e & 3], f[e], s[w]);
+          s[w / 4] = __builtin_fmaf(v[r + e], f[e], s[w / 4]);
         else
-          s[e] = __builtin_fmaf(w < 4 ? v0[w & 3] : v1[w & 3], f[e], s[e]);
+          s[e] = __builtin_fmaf(v[r], f[e], s[e]);
       }
     }
   }
 #pragma unroll
-  for (int e = 0; e < 8; ++e) y[e] += s[e];
+  for (int e = 0; e < 4; ++e) y[e] += s[e];
 }
 
 template <class T, int MODE>
 __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) {
   constexpr int NT = MODE == kDenseForward ? 1 : 2;  // LoRA terms
-  constexpr int kBatch = 8;
+  constexpr int NP = MODE == kDenseGated ? 2 : 1;    // projections' planes
+  constexpr int kBatch = 16;
   __shared__ __attribute__((aligned(16))) float lds_v[NT][64];
   const int lane = threadIdx.x;
   const int i = blockIdx.x;
-  const int c = blockIdx.y * 512 + lane * 8;
+  const int c = blockIdx.y * kEpilogueCols + lane * 4;
   if (i >= p.M) return;
   const bool terms = !p.term_in_tile && p.meta.num_segs > 0 && p.term[0].V != nullptr;
-  int k = -1;
+  int k = -1, end = 0;
+  if (terms && p.row_k != nullptr) {
+    // Covered rows are those before the last segment's end.
+    end = p.meta.seg_indptr[p.meta.num_segs];
+    k = p.row_k[i];
+  }
+  const int64_t vs = (int64_t)p.meta.n_rows * p.rank;
+  float vx[NT][kBatch];
+  const float* vp[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const bool on = terms && !(t > 0 && MODE == kDenseDx && p.pairs < 2);
+    vp[t] = on ? p.term[t].V + (int64_t)i * p.rank + (lane < p.rank ? lane : 0) : nullptr;
+    if (on) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) vx[t][u] = vp[t][(u < p.v_planes ? u : p.v_planes - 1) * vs];
+    }
+  }
+  const bool col = c < p.N;
+  const int64_t o = (int64_t)i * p.N + (col ? c : 0);
+  PlaneBatch x[NP];
+#pragma unroll
+  for (int n = 0; n < NP; ++n) load_planes(p, n, o, 0, x[n]);
+
   if (terms) {
     if (p.row_k != nullptr) {
-      // Covered rows are those before the last segment's end.
-      const int end = p.meta.seg_indptr[p.meta.num_segs], known = p.row_k[i];
-      k = i < end ? known : -1;
+      k = i < end ? k : -1;
     } else {
       const int s = first_segment_past(p.meta, i);
       if (s < p.meta.num_segs && p.meta.seg_indptr[s] <= i) k = p.meta.lora_idx[s];
     }
     if (k >= p.meta.num_loras) k = -1;
-    // V[i] = the sum of its planes, in plane order; lane j holds rank j.
-    const int64_t vs = (int64_t)p.meta.n_rows * p.rank;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (t > 0 && MODE == kDenseDx && p.pairs < 2) break;
-      const float* vp = p.term[t].V + (int64_t)i * p.rank + (lane < p.rank ? lane : 0);
-      float v = 0.f;
-      for (int g0 = 0; g0 < p.v_planes; g0 += kBatch) {
-        float x[kBatch];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) x[u] = vp[(g0 + u < p.v_planes ? g0 + u : p.v_planes - 1) * vs];
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) v = g0 + u < p.v_planes ? v + x[u] : v;
-      }
-      lds_v[t][lane] = v;
-    }
   }
   k = __builtin_amdgcn_readfirstlane(k);
   const uint16_t* E[NT];
   int rk[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const bool on = k >= 0 && !(t > 0 && MODE == kDenseDx && p.pairs < 2);
+    const bool on = k >= 0 && vp[t] != nullptr;
     E[t] = on ? reinterpret_cast<const uint16_t*>(p.term[t].ptrs[k]) : nullptr;
-    rk[t] = on && E[t] != nullptr ? rank_of(p.term[t].ranks, p.rank, k) : 0;
+    rk[t] = on ? rank_of(p.term[t].ranks, p.rank, k) : 0;
+  }
+  u32x2 m[NT][16];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (E[t] == nullptr) rk[t] = 0;
+    if (rk[t] > 0) load_rows<MODE>(p, E[t], rk[t], col ? c : 0, 0, m[t]);
+  }
+  // V[i] = the sum of its planes, in plane order; lane j holds rank j.
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (vp[t] == nullptr) continue;
+    float v = 0.f;
+    for (int g0 = 0; g0 < p.v_planes; g0 += kBatch) {
+      if (g0 > 0) {
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) vx[t][u] = vp[t][(g0 + u < p.v_planes ? g0 + u : p.v_planes - 1) * vs];
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) v = g0 + u < p.v_planes ? v + vx[t][u] : v;
+    }
+    lds_v[t][lane] = v;
   }
   __syncthreads();
-  if (c >= p.N) return;
-  const int64_t o = (int64_t)i * p.N + c;
-  float y[8];
-  plane_sum<T, MODE>(p, 0, o, y);
-  row_term<T, MODE>(p, lds_v[0], E[0], rk[0], c, y);
+  if (!col) return;
+  f32x4 y;
+  plane_sum(p, 0, o, x[0], y);
+  row_term<T, MODE>(p, lds_v[0], E[0], rk[0], c, m[0], y);
   if constexpr (MODE == kDenseGated) {
-    float u[8], h[8];
-    plane_sum<T, MODE>(p, 1, o, u);
-    row_term<T, MODE>(p, lds_v[1], E[1], rk[1], c, u);
+    f32x4 u, h;
+    plane_sum(p, 1, o, x[1], u);
+    row_term<T, MODE>(p, lds_v[1], E[1], rk[1], c, m[1], u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = act_value(p.act, y[e]) * u[e];
-    if (p.out[0]) store_vec(p.out[0] + o, pack8<T>(y));
-    if (p.out[1]) store_vec(p.out[1] + o, pack8<T>(u));
-    store_vec(p.out[2] + o, pack8<T>(h));
+    for (int e = 0; e < 4; ++e) h[e] = act_value(p.act, y[e]) * u[e];
+    if (p.out[0]) *reinterpret_cast<u32x2*>(p.out[0] + o) = round4<T>(y);
+    if (p.out[1]) *reinterpret_cast<u32x2*>(p.out[1] + o) = round4<T>(u);
+    *reinterpret_cast<u32x2*>(p.out[2] + o) = round4<T>(h);
   } else {
-    if constexpr (MODE == kDenseDx) row_term<T, MODE>(p, lds_v[1], E[1], rk[1], c, y);
-    store_vec(p.out[0] + o, pack8<T>(y));
+    if constexpr (MODE == kDenseDx) row_term<T, MODE>(p, lds_v[1], E[1], rk[1], c, m[1], y);
+    *reinterpret_cast<u32x2*>(p.out[0] + o) = round4<T>(y);
   }
 }
 
@@ -516,8 +555,8 @@ template <class T, int MODE>
 hipError_t launch_mode_thin(int cfg, const DenseParams& p, const ThinParams* t, int count, hipStream_t s) {
   switch (cfg) {
     case kTile128: return launch_tile_thin<T, MODE, 128, 128, 2, 2, 4, 2>(p, t, count, s);
-    case kTile64: return launch_tile_thin<T, MODE, 64, 128, 1, 4, 6, 2>(p, t, count, s);
-    case kTile32: return launch_tile_thin<T, MODE, 32, 128, 1, 4, 7, 2>(p, t, count, s);
+    case kTile64: return launch_tile_thin<T, MODE, 64, 256, 1, 4, 4, 2>(p, t, count, s);
+    case kTile32: return launch_tile_thin<T, MODE, 32, 256, 1, 4, 4, 2>(p, t, count, s);
   }
   return hipErrorInvalidValue;
 }
@@ -527,8 +566,8 @@ hipError_t launch_mode(int cfg, const DenseParams& p, hipStream_t s) {
   switch (cfg) {
     case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 4, 2>(p, s);
     case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 4, 2>(p, s);
-    case kTile64: return launch_tile<T, MODE, 64, 128, 1, 4, 6, 2>(p, s);
-    case kTile32: return launch_tile<T, MODE, 32, 128, 1, 4, 7, 2>(p, s);
+    case kTile64: return launch_tile<T, MODE, 64, 256, 1, 4, 4, 2>(p, s);
+    case kTile32: return launch_tile<T, MODE, 32, 256, 1, 4, 4, 2>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -548,7 +587,7 @@ hipError_t launch_t(int mode, int cfg, const DenseParams& p, hipStream_t s) {
 
 template <class T>
 hipError_t launch_epilogue_t(int mode, const DenseParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)p.M, (unsigned)((p.N + 511) / 512));
+  const dim3 grid((unsigned)p.M, (unsigned)((p.N + kEpilogueCols - 1) / kEpilogueCols));
   switch (mode) {
     case kDenseForward: hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, kDenseForward>), grid, dim3(64), 0, s, p); break;
     case kDenseGated: hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, kDenseGated>), grid, dim3(64), 0, s, p); break;

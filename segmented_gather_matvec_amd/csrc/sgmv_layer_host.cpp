@@ -15,23 +15,18 @@ constexpr int kShortRun = 16;  // rows per segment from which the tiles' matrix 
 // Workgroups of a tile shape that run at once on one CU (LDS).
 int resident(int cfg) { return cfg == sgmv::kTile256 ? 1 : 2; }
 
-// Microseconds of one contraction step of every workgroup resident on a CU,
-// and the bytes per microsecond that partial planes move at: the model that
-// picks between tile shapes and splits (only their ratios matter).
-double step_us(int cfg) {
-  switch (cfg) {
-    case sgmv::kTile256: return 0.55;
-    case sgmv::kTile128: return 0.37;
-    case sgmv::kTile64: return 0.25;
-    default: return 0.2;
-  }
-}
-constexpr double kPlaneBytesPerUs = 4.0e6;
+// The model that picks between tile shapes and splits; only ratios matter.
+// Large tiles are bound by the matrix cores: microseconds of one contraction
+// step of all workgroups resident on a CU.  The two small ones are bound by streaming B.
+constexpr double kStep256Us = 0.5, kStep128Us = 0.33;
+constexpr double kStreamBytesPerUs = 5.2e6;  // B of the small tiles, with every slot of the device taken
+constexpr double kPlaneBytesPerUs = 3.0e6;   // partial planes, written and read again
 
 DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, bool may_split) {
   // columns_per_n: 2 for a gated tile (gate and up columns side by side).
   DensePlan best;
   double best_cost = -1;
+  steps = std::max<int64_t>(steps, 1);
   for (int cfg = sgmv::kTile256; cfg <= sgmv::kTile32; ++cfg) {
     const int bm = sgmv::dense_tile_rows(cfg);
     // A tile with more than half of its rows empty only where none is smaller.
@@ -44,11 +39,18 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
     const int64_t slots = kCus * resident(cfg);
     const int64_t most = may_split ? std::max<int64_t>(1, std::min<int64_t>(16, steps / 8)) : 1;
     for (int64_t ks = 1; ks <= most; ++ks) {
-      const int64_t per = ceil_div(std::max<int64_t>(steps, 1), ks);
-      const int64_t used = ceil_div(std::max<int64_t>(steps, 1), per);
-      if (used != ks) continue;
-      const int64_t rounds = ceil_div(tm * tn * ks, slots);
-      double cost = (double)rounds * ((double)per * step_us(cfg) + 4.0);
+      const int64_t per = ceil_div(steps, ks);
+      if (ceil_div(steps, per) != ks) continue;
+      const int64_t wgs = tm * tn * ks, rounds = ceil_div(wgs, slots);
+      double cost;
+      if (cfg <= sgmv::kTile128) {
+        cost = (double)rounds * ((double)per * (cfg == sgmv::kTile256 ? kStep256Us : kStep128Us) + 4.0);
+      } else {
+        // Gated 4096 -> 11008, one row: 344, 430 and 516 workgroups on 512 slots took 37.8, 34.9 and 39.1 us.
+        const double fill = (double)wgs / (double)(rounds * slots);
+        cost = (double)steps * sgmv::kDenseK * (double)N * columns_per_n * 2 / kStreamBytesPerUs *
+               (fill < 0.5 ? 0.6 / fill : 1.35 - 0.35 * fill);
+      }
       if (ks > 1) cost += 3.0 + 2.0 * (double)ks * (double)M * (double)N * columns_per_n * 4 / kPlaneBytesPerUs;
       if (best_cost < 0 || cost < best_cost) {
         best_cost = cost;

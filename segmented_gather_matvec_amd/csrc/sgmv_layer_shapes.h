@@ -11,11 +11,11 @@ constexpr int kDenseK = 32;  // contraction length of one tile step
 enum DenseTile : int {
   kTile256 = 0,  // 256 x 256, 8 waves
   kTile128 = 1,  // 128 x 128, 4 waves
-  kTile64 = 2,   // 64 x 128, 4 waves
-  kTile32 = 3    // 32 x 128, 4 waves
+  kTile64 = 2,   // 64 x 256, 4 waves
+  kTile32 = 3    // 32 x 256, 4 waves
 };
 constexpr int dense_tile_rows(int t) { return t == kTile256 ? 256 : t == kTile128 ? 128 : t == kTile64 ? 64 : 32; }
-constexpr int dense_tile_cols(int t) { return t == kTile256 ? 256 : 128; }
+constexpr int dense_tile_cols(int t) { return t == kTile128 ? 128 : 256; }
 
 constexpr int kThinRows = 64;      // rows of one segment per thin-product workgroup
 constexpr int kLoraGradCols = 256; // columns of X or dY per LoRA-gradient workgroup
