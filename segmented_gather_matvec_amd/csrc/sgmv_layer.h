@@ -88,7 +88,7 @@ hipError_t launch_dense_thin(int dtype, int mode, int cfg, const DenseParams& p,
 // the activation (gated) and writes the outputs.
 hipError_t launch_dense_epilogue(int dtype, int mode, const DenseParams& p, hipStream_t stream);
 
-// count products on grid y (at most 2); the plane sum follows when ksplit > 1.
+// count products (at most 4) in one launch; the plane sum follows when a ksplit > 1.
 hipError_t launch_thin(int dtype, const ThinParams* p, int count, hipStream_t stream);
 
 // Gradients of the LoRA matrices, out[c, j] = sum_{rows i of LoRA k} Z[i, c] * Q[i, j]
@@ -105,6 +105,7 @@ struct LoraGradParams {
   int32_t accumulate;
   SegMeta meta;
 };
+// count gradients (at most 4) in one launch; the plane sum follows when an nsplit > 1.
 hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipStream_t stream);
 
 // dG = dH * U * act'(G), dU = dH * act(G), rounded once to the 16-bit format.

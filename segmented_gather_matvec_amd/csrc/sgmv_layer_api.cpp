@@ -76,7 +76,7 @@ void thin_params(const Call& c, bool up, const void* const* Z, bool full, bool h
     t[i].V = full ? c.at(c.plan.v_off[up][i]) : nullptr;
     t[i].V16 = halves ? reinterpret_cast<uint16_t*>(c.at(c.plan.half_off[up][i])) : nullptr;
     t[i].row_scale = c.at(c.plan.row_scale_off[up][i]);
-    t[i].planes = c.at(c.plan.thin_off[i]);
+    t[i].planes = c.at(c.plan.thin_off[up][i]);
     t[i].K = up ? c.p.h_out : c.p.h_in;
     t[i].rank = c.p.rank;
     t[i].transposed = up ? 1 : 0;
@@ -176,15 +176,20 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
     want_a = want_a || grad[i]->dA_ptrs;
     want_b = want_b || grad[i]->dB_ptrs;
   }
-  if (c.plan.lora && want_b) {
-    const void* Z[2] = {c.X, c.X};
-    const sgmv_status_t st = thin(c, false, Z, false, true);
-    if (st != SGMV_OK) return st;
-  }
-  if (c.plan.lora && (want_a || dX)) {
-    const bool full = dX && !c.plan.out.term_in_tile;
-    const sgmv_status_t st = thin(c, true, dY, full, want_a || !full);
-    if (st != SGMV_OK) return st;
+  if (c.plan.lora) {  // V for dB, dV for dX and dA, in one launch
+    sgmv::ThinParams t[4];
+    int count = 0;
+    if (want_a || dX) {
+      const bool full = dX && !c.plan.out.term_in_tile;
+      thin_params(c, true, dY, full, want_a || !full, t);
+      count = c.np;
+    }
+    if (want_b) {
+      const void* Z[2] = {c.X, c.X};
+      thin_params(c, false, Z, false, true, t + count);
+      count += c.np;
+    }
+    if (sgmv::launch_thin(c.p.dtype, t, count, c.stream) != hipSuccess) return SGMV_ERR_HIP;
   }
   if (dX && rows) {
     sgmv::DenseParams q = dense_params(c, c.plan.out, c.p.n_rows, c.p.h_in, c.p.h_out, c.p.h_out, c.p.h_out);
@@ -213,31 +218,32 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
     if (st != SGMV_OK) return st;
   }
   if (!c.plan.lora && accumulate) return SGMV_OK;  // no rows: nothing to add
-  for (int b = 0; b < 2; ++b) {
-    sgmv::LoraGradParams g[2]{};
-    int count = 0;
+  sgmv::LoraGradParams g[4]{};
+  int count = 0;
+  float* planes = c.at(c.plan.planes_off);
+  for (int b = 1; b >= 0; --b) {
     const int64_t C = b ? c.p.h_out : c.p.h_in;
     const int nsplit = b ? c.plan.nsplit_b : c.plan.nsplit_a;
     for (int i = 0; i < c.np; ++i) {
       const void* out = b ? static_cast<const void*>(grad[i]->dB_ptrs) : static_cast<const void*>(grad[i]->dA_ptrs);
       if (!out) continue;
-      sgmv::LoraGradParams& e = g[count];
+      sgmv::LoraGradParams& e = g[count++];
       e.Z = half(b ? dY[i] : c.X);
       e.Q = reinterpret_cast<const uint16_t*>(c.at(c.plan.half_off[!b][i]));
       e.row_scale = c.at(c.plan.row_scale_off[!b][i]);
       e.out = table(out);
       e.ranks = c.proj[i]->ranks;
-      e.planes = c.at(c.plan.planes_off) + (size_t)count * nsplit * c.p.num_loras * C * c.p.rank;
+      e.planes = planes;
+      if (nsplit > 1) planes += (size_t)nsplit * c.p.num_loras * C * c.p.rank;
       e.C = (int32_t)C;
       e.rank = c.p.rank;
       e.rank_major = b;
       e.nsplit = nsplit;
       e.accumulate = accumulate;
       e.meta = c.meta;
-      ++count;
     }
-    if (count > 0 && sgmv::launch_lora_grad(c.p.dtype, g, count, c.stream) != hipSuccess) return SGMV_ERR_HIP;
   }
+  if (count > 0 && sgmv::launch_lora_grad(c.p.dtype, g, count, c.stream) != hipSuccess) return SGMV_ERR_HIP;
   return SGMV_OK;
 }
 

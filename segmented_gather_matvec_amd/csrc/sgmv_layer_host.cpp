@@ -113,18 +113,14 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   if (l.lora) {
     const size_t v = (size_t)n * p.rank * sizeof(float);
     l.down = plan_thin(p, p.h_in, l.projections);
-    size_t planes = l.down.plane_bytes;
-    if (back) {
-      l.up = plan_thin(p, p.h_out, l.projections);
-      planes = std::max(planes, l.up.plane_bytes);
-    }
+    if (back) l.up = plan_thin(p, p.h_out, l.projections);
     for (int i = 0; i < l.projections; ++i) {
       for (int d = 0; d < (back ? 2 : 1); ++d) {
         l.v_off[d][i] = take(v);
         l.half_off[d][i] = take(v);  // two 16-bit halves a value
         l.row_scale_off[d][i] = take((size_t)n * sizeof(float));
+        l.thin_off[d][i] = take(d ? l.up.plane_bytes : l.down.plane_bytes);
       }
-      l.thin_off[i] = take(planes);
     }
   }
   if (op == SGMV_GATED_BACKWARD)
@@ -151,7 +147,7 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
       const auto bytes = [&](int ns, int64_t C) {
         return ns > 1 ? (size_t)ns * p.num_loras * C * p.rank * sizeof(float) * l.projections : (size_t)0;
       };
-      area = std::max({area, bytes(l.nsplit_a, p.h_in), bytes(l.nsplit_b, p.h_out)});
+      area = std::max(area, bytes(l.nsplit_a, p.h_in) + bytes(l.nsplit_b, p.h_out));
     }
   }
   l.planes_off = take(area);

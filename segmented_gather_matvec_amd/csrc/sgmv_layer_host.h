@@ -33,9 +33,9 @@ struct LayerPlan {
   ThinPlan up;         // dV = s_k dY @ B_k^T    (K = h_out)
   int nsplit_a = 1, nsplit_b = 1;  // row splits of the gradients of A_k and B_k
   // Byte offsets into the workspace.
-  // [0][i]: V of projection i, [1][i]: dV; as fp32, as 16-bit halves, and the halves' row scales.
-  size_t v_off[2][2] = {}, half_off[2][2] = {}, row_scale_off[2][2] = {};
-  size_t thin_off[2] = {0, 0}, gate_off[2] = {0, 0}, row_k_off = 0;
+  // [0][i]: V of projection i, [1][i]: dV; as fp32, as 16-bit halves, the halves' row scales, partial planes.
+  size_t v_off[2][2] = {}, half_off[2][2] = {}, row_scale_off[2][2] = {}, thin_off[2][2] = {};
+  size_t gate_off[2] = {0, 0}, row_k_off = 0;
   size_t planes_off = 0;  // partial planes of the dense product, then of the LoRA gradients (never both live)
   size_t total = 0;
 };

@@ -7,35 +7,58 @@
 // dV = s_k dy@B_k^T:
 //     dx  += dV @ A_k^T,   dA_k = sum_i x_i^T dV_i,   dB_k = sum_i V_i^T dy_i.
 // All of them read a [rows, thousands] operand once and are bound by memory.
+#include <algorithm>
+
 #include "sgmv_thin.h"
 
 namespace sgmv {
 namespace {
 
 // ---------------------------------------------------------------- thin products
-template <class T, int JT, bool TRANSPOSED>
-__global__ __launch_bounds__(kThreads) void sgmv_thin_kernel(ThinParams p0, ThinParams p1) {
+// Up to four products in one launch (grid y).
+struct ThinBatch {
+  ThinParams p[4];
+};
+
+template <class T, int JT>
+__global__ __launch_bounds__(kThreads) void sgmv_thin_kernel(ThinBatch batch) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[ThinShape<JT>::LDS];
-  thin_body<T, JT, TRANSPOSED>(blockIdx.y ? p1 : p0, (int)blockIdx.x, lds);
+  const ThinParams& p = batch.p[blockIdx.y];
+  if ((int)blockIdx.x >= p.units * p.ksplit) return;
+  if (p.transposed)
+    thin_body<T, JT, true>(p, (int)blockIdx.x, lds);
+  else
+    thin_body<T, JT, false>(p, (int)blockIdx.x, lds);
 }
 
 // V = sum of the planes, in plane order (rows no segment covers hold anything;
 // nothing reads them).
 template <class T>
-__global__ __launch_bounds__(kThreads) void sgmv_thin_sum_kernel(ThinParams p0, ThinParams p1) {
-  const ThinParams& p = blockIdx.y ? p1 : p0;
+__global__ __launch_bounds__(kThreads) void sgmv_thin_sum_kernel(ThinBatch batch) {
+  const ThinParams& p = batch.p[blockIdx.y];
+  if (p.ksplit <= 1) return;  // written by the product itself
+  constexpr int kBatch = 8;   // planes in flight
   const int per_row = p.rank / 8;
   const int64_t n = (int64_t)p.meta.n_rows * p.rank;
   const int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (x * 8 >= n) return;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int g = 0; g < p.ksplit; ++g) {
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p.planes + g * n + x * 8);
-    const f32x4 b = *reinterpret_cast<const f32x4*>(p.planes + g * n + x * 8 + 4);
+  for (int g0 = 0; g0 < p.ksplit; g0 += kBatch) {
+    f32x4 a[kBatch], b[kBatch];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      v[e] += a[e];
-      v[4 + e] += b[e];
+    for (int u = 0; u < kBatch; ++u) {
+      const float* src = p.planes + (g0 + u < p.ksplit ? g0 + u : p.ksplit - 1) * n + x * 8;
+      a[u] = *reinterpret_cast<const f32x4*>(src);
+      b[u] = *reinterpret_cast<const f32x4*>(src + 4);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const bool live = g0 + u < p.ksplit;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = live ? v[e] + a[u][e] : v[e];
+        v[4 + e] = live ? v[4 + e] + b[u][e] : v[4 + e];
+      }
     }
   }
   store_v<T>(p, (int)(x / per_row), (int)(x % per_row) * 8, v);
@@ -49,17 +72,23 @@ __global__ __launch_bounds__(kThreads) void sgmv_thin_sum_kernel(ThinParams p0, 
 // stream through a ring of LDS slots (sgmv_tile.h).  Bound by reading Z.
 // fp16 rows of V16 may be kept scaled down by a power of two each: then the sums run
 // in units of the largest scale so far.
+// Up to four gradients in one launch (grid y).
+struct LoraGradBatch {
+  LoraGradParams p[4];
+};
+
 template <class T, int R>
-__global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradParams p0, LoraGradParams p1) {
+__global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch batch) {
   constexpr int ROWS = kDenseK, COLS = kLoraGradCols, QC = 2 * R, JT = R < 16 ? 1 : R / 16;
   constexpr int STAGES = R == 64 ? 3 : 4;  // two workgroups per CU
   constexpr bool F16T = T::kMaxFinite < 1e6f;
   constexpr int LZ = COLS / 16 / kWaves, LQ = QC / 16 < kWaves ? 1 : QC / 16 / kWaves;
   constexpr int B0 = COLS * ROWS, S0 = B0 + QC * ROWS, SLOT = S0 + (F16T ? 128 : 0);  // Z, V16, row scales
   constexpr int kPerStep = LZ + LQ + (F16T ? 1 : 0);
-  const int ctiles = (p0.C + COLS - 1) / COLS;
+  const LoraGradParams& p = batch.p[blockIdx.y];
+  const int ctiles = (p.C + COLS - 1) / COLS;
   const int k = (int)blockIdx.x / ctiles;
-  const LoraGradParams& p = blockIdx.y ? p1 : p0;
+  if (k >= p.meta.num_loras || (int)blockIdx.z >= p.nsplit) return;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES * SLOT];
   __shared__ int lds_lo[kThreads], lds_hi[kThreads];
   __shared__ int lds_count[kWaves];
@@ -239,10 +268,11 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradParams
 
 // Sums the splits' planes of one LoRA's gradient (split order), four values per thread.
 template <class T>
-__global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradParams p0, LoraGradParams p1) {
-  const int64_t blocks = ((int64_t)p0.C * p0.rank / 4 + kThreads - 1) / kThreads;  // of one LoRA
+__global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBatch batch) {
+  const LoraGradParams& p = batch.p[blockIdx.y];
+  const int64_t blocks = ((int64_t)p.C * p.rank / 4 + kThreads - 1) / kThreads;  // of one LoRA
   const int k = (int)(blockIdx.x / blocks);
-  const LoraGradParams& p = blockIdx.y ? p1 : p0;
+  if (k >= p.meta.num_loras || p.nsplit <= 1) return;
   const int R = p.rank;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out[k]);
   const int rk = rank_of(p.ranks, R, k);
@@ -301,53 +331,58 @@ __global__ __launch_bounds__(kThreads) void sgmv_gate_backward_kernel(int act, c
   }
 }
 
-template <class T, int JT>
-hipError_t launch_thin_j(const ThinParams* p, int count, hipStream_t s) {
-  const ThinParams& a = p[0];
-  const ThinParams& b = p[count - 1];
-  const dim3 grid((unsigned)((int64_t)a.units * a.ksplit), (unsigned)count);
-  if (a.transposed)
-    hipLaunchKernelGGL((sgmv_thin_kernel<T, JT, true>), grid, dim3(kThreads), 0, s, a, b);
-  else
-    hipLaunchKernelGGL((sgmv_thin_kernel<T, JT, false>), grid, dim3(kThreads), 0, s, a, b);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.ksplit <= 1) return e;
-  const int64_t items = (int64_t)a.meta.n_rows * a.rank / 8;
+template <class T>
+hipError_t launch_thin_t(const ThinParams* p, int count, hipStream_t s) {
+  ThinBatch batch{};
+  int64_t grid = 0;
+  int planes = 1;
+  for (int i = 0; i < count; ++i) {
+    batch.p[i] = p[i];
+    grid = std::max(grid, (int64_t)p[i].units * p[i].ksplit);
+    planes = std::max(planes, p[i].ksplit);
+  }
+  if (grid > 0x7fffffff) return hipErrorInvalidValue;
+  const dim3 g((unsigned)grid, (unsigned)count);
+  switch (p[0].rank) {
+    case 8:
+    case 16: hipLaunchKernelGGL((sgmv_thin_kernel<T, 1>), g, dim3(kThreads), 0, s, batch); break;
+    case 32: hipLaunchKernelGGL((sgmv_thin_kernel<T, 2>), g, dim3(kThreads), 0, s, batch); break;
+    case 64: hipLaunchKernelGGL((sgmv_thin_kernel<T, 4>), g, dim3(kThreads), 0, s, batch); break;
+    default: return hipErrorInvalidValue;
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || planes <= 1) return e;
+  const int64_t items = (int64_t)p[0].meta.n_rows * p[0].rank / 8;
   hipLaunchKernelGGL((sgmv_thin_sum_kernel<T>), dim3((unsigned)((items + kThreads - 1) / kThreads), (unsigned)count),
-                     dim3(kThreads), 0, s, a, b);
+                     dim3(kThreads), 0, s, batch);
   return hipGetLastError();
 }
 
 template <class T>
-hipError_t launch_thin_t(const ThinParams* p, int count, hipStream_t s) {
-  switch (p[0].rank) {
-    case 8:
-    case 16: return launch_thin_j<T, 1>(p, count, s);
-    case 32: return launch_thin_j<T, 2>(p, count, s);
-    case 64: return launch_thin_j<T, 4>(p, count, s);
-  }
-  return hipErrorInvalidValue;
-}
-
-template <class T>
 hipError_t launch_lora_grad_t(const LoraGradParams* p, int count, hipStream_t s) {
-  const LoraGradParams& a = p[0];
-  const LoraGradParams& b = p[count - 1];
-  const int64_t tiles = (int64_t)((a.C + kLoraGradCols - 1) / kLoraGradCols) * a.meta.num_loras;
-  const int64_t blocks = ((int64_t)a.C * a.rank / 4 + kThreads - 1) / kThreads * a.meta.num_loras;
+  LoraGradBatch batch{};
+  int64_t tiles = 0, blocks = 0;
+  int nsplit = 1;
+  for (int i = 0; i < count; ++i) {
+    batch.p[i] = p[i];
+    const int64_t loras = p[i].meta.num_loras;
+    tiles = std::max(tiles, (p[i].C + kLoraGradCols - 1) / kLoraGradCols * loras);
+    if (p[i].nsplit > 1) blocks = std::max(blocks, ((int64_t)p[i].C * p[i].rank / 4 + kThreads - 1) / kThreads * loras);
+    nsplit = std::max(nsplit, p[i].nsplit);
+  }
   if (tiles > 0x7fffffff || blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)tiles, (unsigned)count, (unsigned)a.nsplit);
-  switch (a.rank) {
-    case 8: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 8>), grid, dim3(kThreads), 0, s, a, b); break;
-    case 16: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 16>), grid, dim3(kThreads), 0, s, a, b); break;
-    case 32: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 32>), grid, dim3(kThreads), 0, s, a, b); break;
-    case 64: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 64>), grid, dim3(kThreads), 0, s, a, b); break;
+  const dim3 grid((unsigned)tiles, (unsigned)count, (unsigned)nsplit);
+  switch (p[0].rank) {
+    case 8: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 8>), grid, dim3(kThreads), 0, s, batch); break;
+    case 16: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 16>), grid, dim3(kThreads), 0, s, batch); break;
+    case 32: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 32>), grid, dim3(kThreads), 0, s, batch); break;
+    case 64: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 64>), grid, dim3(kThreads), 0, s, batch); break;
     default: return hipErrorInvalidValue;
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || a.nsplit <= 1) return e;
-  hipLaunchKernelGGL((sgmv_lora_grad_sum_kernel<T>), dim3((unsigned)blocks, (unsigned)count), dim3(kThreads), 0, s, a,
-                     b);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || blocks == 0) return e;
+  hipLaunchKernelGGL((sgmv_lora_grad_sum_kernel<T>), dim3((unsigned)blocks, (unsigned)count), dim3(kThreads), 0, s,
+                     batch);
   return hipGetLastError();
 }
 
@@ -355,11 +390,13 @@ hipError_t launch_lora_grad_t(const LoraGradParams* p, int count, hipStream_t s)
 
 hipError_t launch_thin(int dtype, const ThinParams* p, int count, hipStream_t stream) {
   if (count < 1 || p[0].units <= 0) return hipSuccess;
+  if (count > 4) return hipErrorInvalidValue;
   return dtype == 1 ? launch_thin_t<BF16>(p, count, stream) : launch_thin_t<F16>(p, count, stream);
 }
 
 hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipStream_t stream) {
   if (count < 1 || p[0].meta.num_loras <= 0) return hipSuccess;
+  if (count > 4) return hipErrorInvalidValue;
   return dtype == 1 ? launch_lora_grad_t<BF16>(p, count, stream) : launch_lora_grad_t<F16>(p, count, stream);
 }
 
