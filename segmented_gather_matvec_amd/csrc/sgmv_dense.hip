@@ -12,9 +12,9 @@
 // slot per step; lanes past the matrix ask for an offset beyond the buffer
 // descriptor and get zeros (sgmv_tile.h has the layouts).  Tiles multiply as
 // D^T = B^T A^T, so that a lane ends up with four consecutive columns of one row.
-// The LoRA term joins in the epilogue: per run of rows that share a LoRA, V's
+// The LoRA term joins before the output: per run of rows that share a LoRA, V's
 // hi + lo 16-bit halves (together 16 or 22 bits of fp32's V) times E_k on the
-// matrix cores, onto the accumulators; outputs are rounded once.
+// matrix cores, added to the accumulators in fp32; outputs are rounded once.
 #include "sgmv_thin.h"
 
 namespace sgmv {
@@ -42,86 +42,152 @@ struct DenseShape {
   static constexpr int TNP = TN / NB;                 // 16-column tiles of one projection per wave
   static constexpr int SLOT = (BM + BN) * kDenseK;    // halves of one ring slot
   static_assert((LA * 16 * NW) % BM == 0 && LB * 16 * NW == BN, "tile loads split evenly over the waves");
-  static_assert(TNP == 1 || TNP == 2 || (TNP == 4 && !GATED), "the LoRA term joins two column tiles at a time");
   static_assert(TM * 16 * WM == BM && TNP * NB * 16 * WN == BN, "tile splits evenly over the waves");
 };
 
-// Adds the LoRA term of projection `t` to the accumulators acc[0..TM)[J0..J0+JN)
-// of a wave's rows [m0, m0 + 16 TM) and columns c0 + 16 j; s_first: the first segment that ends past m0.
-template <class T, int MODE, int TM, int TN, int J0, int JN>
-__device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x4 (&acc)[TM][TN], int m0, int c0,
-                                int s_first) {
-  const int lane = threadIdx.x & 63;
-  const int q = lane >> 4, ml = lane & 15;
+// Loads a step of E_k (columns n0 .. n0 + C of the forward's B_k [r_k, N], or rows of dX's A_k [N, r_k]) as a B operand tile:
+// ranks k0 .. k0+31, or, at ranks up to 16, all of them twice, for V's hi and lo halves.
+template <int C, int LOADS, bool T>
+__device__ inline void issue_e(const uint16_t* E, int rk, int R, int k0, int N, int n0, uint16_t* lds, int wave, int lane) {
+  const int cols = N - n0 < C ? N - n0 : C;
+  const uint32_t bytes = T ? (uint32_t)((rk - 1) * N + (N - n0)) * 2u : (uint32_t)(cols * rk) * 2u;
+  const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(E + (T ? (int64_t)n0 : (int64_t)n0 * rk)), 0,
+                                                    (int)bytes, kRawBuffer);
+#pragma unroll
+  for (int j = 0; j < LOADS; ++j) {
+    const int L = (wave * LOADS + j) % (C / 16);
+    uint32_t off;
+    if constexpr (T) {
+      constexpr int G = C / 8;
+      const int k = L * (64 / G) + lane / G;
+      const int r = R <= 16 ? k & (R - 1) : k0 + k;
+      off = r < rk && (R > 16 || k < 2 * R) ? (uint32_t)(r * N + ((lane % G) ^ swizzle_k<C>(k)) * 8) * 2u : kOutOfRange;
+    } else {
+      const int k = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;
+      const int r = R <= 16 ? k & (R - 1) : k0 + k;
+      off = r < rk && (R > 16 || k < 2 * R) ? (uint32_t)((L * 16 + (lane >> 2)) * rk + r) * 2u : kOutOfRange;
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + L * 512), 16, (int)off, 0, 0, 0);
+  }
+}
+
+// Adds the LoRA term t to the accumulators' columns J0 .. J0+TNP of the workgroup's tile, run by
+// run of rows that share a LoRA.  V's halves of the tile's rows and E_k of up to four
+// runs go through the ring's slots (the product is done with them), behind one barrier.
+template <class T, int MODE, class S, int J0>
+__device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x4 (&acc)[S::TM][S::TN], uint16_t* ring,
+                                int m0, int n0, int wave, int lane) {
+  constexpr int TM = S::TM, TNP = S::TNP, C = S::C, B0 = S::BM * kDenseK, SLOTS = 4;
+  constexpr int LE = C / 16 < S::NW ? 1 : C / 16 / S::NW;
+  static_assert(S::STAGES >= SLOTS, "ring slots");
   const SegMeta& sm = p.meta;
-  if (t.V16 == nullptr) return;
-  const int mend = m0 + 16 * TM < p.M ? m0 + 16 * TM : p.M;
+  const int ml = lane & 15;
+  const int wm = wave / S::WN, wn = wave % S::WN;
   const int R = p.rank;
-  for (int s0 = s_first; s0 < sm.num_segs; s0 += 64) {
+  const int chunks = R > 32 ? 2 : 1;              // of 32 ranks: B slots of a run
+  const int steps = R <= 16 ? 1 : 2 * chunks;     // hi then lo (together at ranks up to 16): A slots
+  const int depth = SLOTS / chunks;               // runs at once
+  const int mend = m0 + S::BM < p.M ? m0 + S::BM : p.M;
+  bool first = true;
+  for (int s0 = first_segment_past(sm, m0); s0 < sm.num_segs; s0 += 64) {
     // Metadata of 64 segments at a time, one per lane.
     const int sl = s0 + lane < sm.num_segs ? s0 + lane : sm.num_segs - 1;
     const int lo_l = sm.seg_indptr[sl], hi_l = sm.seg_indptr[sl + 1];
     int k_l = sm.lora_idx[sl];
     if (k_l < 0 || k_l >= sm.num_loras) k_l = -1;
     const uint64_t e_l = k_l >= 0 ? t.ptrs[k_l] : 0ull;
-    const int r_l = k_l >= 0 ? rank_of(t.ranks, R, k_l) : 0;
+    const int r_l = k_l >= 0 && e_l != 0ull ? rank_of(t.ranks, R, k_l) : 0;
     const int ns = sm.num_segs - s0 < 64 ? sm.num_segs - s0 : 64;
-    for (int u = 0; u < ns; ++u) {
-      const int lo = __builtin_amdgcn_readlane(lo_l, u), hi_s = __builtin_amdgcn_readlane(hi_l, u);
-      if (lo >= mend) return;
-      const int r0 = lo > m0 ? lo : m0, r1 = hi_s < mend ? hi_s : mend;
-      const int rk = __builtin_amdgcn_readlane(r_l, u);
-      const uint32_t e_lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e_l, u);
-      const uint32_t e_hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(e_l >> 32), u);
-      const uint16_t* E = reinterpret_cast<const uint16_t*>(((uint64_t)e_hi << 32) | e_lo);
-      if (r1 <= r0 || rk <= 0 || E == nullptr) continue;
-      for (int k0 = 0; k0 < rk; k0 += 32) {
-        const int r = k0 + 8 * q;
-        const bool rok = r < rk;
-        // E_k operands of the wave's columns: lane holds E[k0 + 8 q + e][c0 + 16 j + ml].
-        u32x4 ef[JN];
+    int u = 0;
+    while (u < ns) {
+      // The next `depth` runs with rows in this tile: E_k into their B slots.
+      int r0[SLOTS], r1[SLOTS], found = 0;
+      __builtin_amdgcn_s_barrier();  // the slots are free
 #pragma unroll
-        for (int j = 0; j < JN; ++j) {
-          const int c = c0 + 16 * j + ml;
-          const bool ok = rok && c < p.N;
-          if constexpr (MODE == kDenseDx) {
-            ef[j] = load_vec(E + (ok ? (int64_t)c * rk + r : 0));
-          } else {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t a = ((global_u16_ptr)E)[ok ? (int64_t)(r + 2 * w) * p.N + c : 0];
-              const uint32_t b = ((global_u16_ptr)E)[ok ? (int64_t)(r + 2 * w + 1) * p.N + c : 0];
-              ef[j][w] = a | (b << 16);
-            }
+      for (int d = 0; d < SLOTS; ++d) {
+        r0[d] = r1[d] = 0;
+        if (d >= depth) continue;
+        for (; u < ns && r1[d] <= r0[d]; ++u) {
+          const int lo = __builtin_amdgcn_readlane(lo_l, u), hi = __builtin_amdgcn_readlane(hi_l, u);
+          const int rk = __builtin_amdgcn_readlane(r_l, u);
+          if (lo >= mend) {
+            u = ns;  // no later segment has rows here
+            break;
           }
-          if (!ok) ef[j] = u32x4{0u, 0u, 0u, 0u};
+          if (rk <= 0) continue;
+          r0[d] = lo > m0 ? lo : m0;
+          r1[d] = hi < mend ? hi : mend;
+          if (r1[d] <= r0[d]) continue;
+          const uint32_t e_lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)e_l, u);
+          const uint32_t e_hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(e_l >> 32), u);
+          const uint16_t* E = reinterpret_cast<const uint16_t*>(((uint64_t)e_hi << 32) | e_lo);
+          for (int c = 0; c < chunks; ++c)
+            issue_e<C, LE, S::B_T>(E, rk, R, c * 32, p.N, n0, ring + (d * chunks + c) * S::SLOT + B0, wave, lane);
+          found = d + 1;
         }
-        const uint16_t* vcol = t.V16 + (rok ? r : 0);
+      }
+      if (found == 0) break;
+      if (first) {
+        TileLoader<S::BM, S::LA, false> lv;
+        lv.init(wave, lane, 2 * R);
+        for (int a = 0; a < steps; ++a) {
+          const int col = a / chunks * R + a % chunks * 32;
+          lv.start(t.V16, 2 * R, m0, p.M, col, col + (2 * R < 32 ? 2 * R : 32));
+          lv.issue(ring + a * S::SLOT);
+        }
+        first = false;
+      }
+      wait_loads_and_lds<0>();
+      __builtin_amdgcn_s_barrier();
 #pragma unroll
-        for (int mi = 0; mi < TM; ++mi) {
-          const int mb = m0 + 16 * mi;
-          if (mb + 16 <= r0 || mb >= r1) continue;
-          const int row = mb + ml;
-          const bool in = row >= r0 && row < r1;
-          const uint16_t* vp = vcol + (int64_t)(in ? row : r0) * (2 * R);
-          u32x4 vh = load_vec(vp), vl = load_vec(vp + R);
-          if (!rok) vh = vl = u32x4{0u, 0u, 0u, 0u};  // (0 times an infinite V would be NaN)
-          // The term's own sum first, then the rows of the run take it: what another
-          // LoRA's matrices hold must not reach them (fp16: scaled back up).
-          float up = 1.f;
-          if constexpr (T::kMaxFinite < 1e6f) up = t.row_scale[in ? row : r0];
+      for (int d = 0; d < SLOTS; ++d) {
+        if (d >= found || r1[d] <= r0[d]) continue;
+        constexpr int JN = TNP < 2 ? TNP : 2;  // column tiles at a time (registers)
 #pragma unroll
-          for (int j = 0; j < JN; ++j) {
-            f32x4 d = {0.f, 0.f, 0.f, 0.f};
-            d = mfma<T>(ef[j], vl, d);
-            d = mfma<T>(ef[j], vh, d);
+        for (int j0 = 0; j0 < TNP; j0 += JN) {
+          u32x4 ef[2][JN];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[mi][J0 + j][i] = in ? __builtin_fmaf(d[i], up, acc[mi][J0 + j][i]) : acc[mi][J0 + j][i];
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+              ef[c][j] = read_operand<C, S::B_T>(ring + (d * chunks + (c < chunks ? c : 0)) * S::SLOT + B0,
+                                                 (wn * TNP + j0 + j) * 16, lane);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) {
+            const int mb = m0 + (wm * TM + i) * 16;
+            if (mb + 16 <= r0[d] || mb >= r1[d]) continue;
+            f32x4 sum[JN];
+#pragma unroll
+            for (int j = 0; j < JN; ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int a = 3; a >= 0; --a) {  // lo halves first
+              if (a >= steps) continue;
+              const u32x4 vf = read_operand<S::BM, false>(ring + a * S::SLOT, (wm * TM + i) * 16, lane);
+              if (chunks > 1 && (a & 1)) {
+#pragma unroll
+                for (int j = 0; j < JN; ++j) sum[j] = mfma<T>(ef[1][j], vf, sum[j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < JN; ++j) sum[j] = mfma<T>(ef[0][j], vf, sum[j]);
+              }
+            }
+            // The rows of the run take their sum: what another LoRA's matrices hold must not
+            // reach them (fp16: scaled back up).
+            const int row = mb + ml;
+            const bool in = row >= r0[d] && row < r1[d];
+            const float up = T::kMaxFinite < 1e6f ? t.row_scale[in ? row : r0[d]] : 1.f;
+#pragma unroll
+            for (int j = 0; j < JN; ++j)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                acc[i][J0 + j0 + j][e] =
+                    in ? __builtin_fmaf(sum[j][e], up, acc[i][J0 + j0 + j][e]) : acc[i][J0 + j0 + j][e];
           }
         }
       }
+      wait_loads_and_lds<0>();
     }
+    if (__builtin_amdgcn_readlane(lo_l, ns - 1) >= mend) return;
   }
 }
 
@@ -259,16 +325,14 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
   const int mw = m0 + wm * TM * 16;
   const int cw = n0 + wn * TNP * 16;
   if (MODE != kDenseDw && p.term_in_tile && g == 0) {
-    // Two column tiles of E_k's operands at a time (registers).
-    constexpr int J = TNP < 2 ? TNP : 2;
-    const int seg = first_segment_past(p.meta, mw);
     if constexpr (S::GATED) {
-      add_term<T, MODE, TM, TN, 0, J>(p, p.term[0], acc, mw, cw, seg);
-      add_term<T, MODE, TM, TN, TNP, J>(p, p.term[1], acc, mw, cw, seg);
+      if (p.term[0].V16 != nullptr) add_term<T, MODE, S, 0>(p, p.term[0], acc, ring, m0, n0, wave, lane);
+      if (p.term[1].V16 != nullptr) add_term<T, MODE, S, TNP>(p, p.term[1], acc, ring, m0, n0, wave, lane);
     } else {
       for (int t = 0; t < (MODE == kDenseDx ? p.pairs : 1); ++t) {
-        add_term<T, MODE, TM, TN, 0, J>(p, t ? p.term[1] : p.term[0], acc, mw, cw, seg);
-        if constexpr (TN > 2) add_term<T, MODE, TM, TN, 2, 2>(p, t ? p.term[1] : p.term[0], acc, mw, cw + 32, seg);
+        const LowRankTerm term{nullptr, t ? p.term[1].V16 : p.term[0].V16, t ? p.term[1].row_scale : p.term[0].row_scale,
+                               t ? p.term[1].ptrs : p.term[0].ptrs, t ? p.term[1].ranks : p.term[0].ranks};
+        if (term.V16 != nullptr) add_term<T, MODE, S, 0>(p, term, acc, ring, m0, n0, wave, lane);
       }
     }
   }
@@ -529,6 +593,37 @@ __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) 
   }
 }
 
+// The epilogue where no LoRA term is left to add: eight values per thread.
+template <class T, int MODE>
+__global__ __launch_bounds__(kThreads) void sgmv_dense_sum_kernel(DenseParams p) {
+  constexpr int NP = MODE == kDenseGated ? 2 : 1;
+  const int64_t o = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+  if (o >= (int64_t)p.M * p.N) return;
+  float y[NP][8];
+#pragma unroll
+  for (int n = 0; n < NP; ++n) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      PlaneBatch x;
+      f32x4 v;
+      load_planes(p, n, o + 4 * h, 0, x);
+      plane_sum(p, n, o + 4 * h, x, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[n][4 * h + e] = v[e];
+    }
+  }
+  if constexpr (MODE == kDenseGated) {
+    float h[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[e] = act_value(p.act, y[0][e]) * y[1][e];
+    if (p.out[0]) store_vec(p.out[0] + o, pack8<T>(y[0]));
+    if (p.out[1]) store_vec(p.out[1] + o, pack8<T>(y[1]));
+    store_vec(p.out[2] + o, pack8<T>(h));
+  } else {
+    store_vec(p.out[0] + o, pack8<T>(y[0]));
+  }
+}
+
 template <class T, int MODE, int BM, int BN, int WM, int WN, int STAGES, int WPS>
 hipError_t launch_tile(const DenseParams& p, hipStream_t s) {
   using S = DenseShape<MODE, BM, BN, WM, WN, STAGES, WPS>;
@@ -585,16 +680,27 @@ hipError_t launch_t(int mode, int cfg, const DenseParams& p, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
-template <class T>
-hipError_t launch_epilogue_t(int mode, const DenseParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)p.M, (unsigned)((p.N + kEpilogueCols - 1) / kEpilogueCols));
-  switch (mode) {
-    case kDenseForward: hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, kDenseForward>), grid, dim3(64), 0, s, p); break;
-    case kDenseGated: hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, kDenseGated>), grid, dim3(64), 0, s, p); break;
-    case kDenseDx: hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, kDenseDx>), grid, dim3(64), 0, s, p); break;
-    default: return hipErrorInvalidValue;
+template <class T, int MODE>
+hipError_t launch_epilogue_mode(const DenseParams& p, hipStream_t s) {
+  if (p.term_in_tile || p.meta.num_segs <= 0 || p.term[0].V == nullptr) {
+    const int64_t blocks = ((int64_t)p.M * p.N / 8 + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((sgmv_dense_sum_kernel<T, MODE>), dim3((unsigned)blocks), dim3(kThreads), 0, s, p);
+  } else {
+    const dim3 grid((unsigned)p.M, (unsigned)((p.N + kEpilogueCols - 1) / kEpilogueCols));
+    hipLaunchKernelGGL((sgmv_dense_epilogue_kernel<T, MODE>), grid, dim3(64), 0, s, p);
   }
   return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_epilogue_t(int mode, const DenseParams& p, hipStream_t s) {
+  switch (mode) {
+    case kDenseForward: return launch_epilogue_mode<T, kDenseForward>(p, s);
+    case kDenseGated: return launch_epilogue_mode<T, kDenseGated>(p, s);
+    case kDenseDx: return launch_epilogue_mode<T, kDenseDx>(p, s);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
