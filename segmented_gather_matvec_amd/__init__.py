@@ -459,6 +459,11 @@ def _need_shape(t, name, shape):
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
+def _need_len(t, name, least):
+    if t is not None and t.numel() < least:
+        raise ValueError(f"{name} must hold {least} entries, got {t.numel()}")
+
+
 def _layer_inputs(problem, X, weights, seg_indptr, lora_idx, ws, others=()):
     """Checks what every layer call takes; ``others``: (tensor or None, name, width) in the problem's format."""
     import torch
@@ -469,6 +474,7 @@ def _layer_inputs(problem, X, weights, seg_indptr, lora_idx, ws, others=()):
     for t, name, width in others:
         _need(t, name, dt); _need_shape(t, name, (n, width))
     _need(seg_indptr, "seg_indptr", torch.int32); _need(lora_idx, "lora_idx", torch.int32)
+    _need_len(seg_indptr, "seg_indptr", problem.num_segs + 1); _need_len(lora_idx, "lora_idx", problem.num_segs)
     _need(ws, "ws")
 
 
@@ -478,6 +484,8 @@ def _layer_projection(problem, pj, name):
     _need(A_ptrs, f"{name} A_ptrs", torch.int64); _need(B_ptrs, f"{name} B_ptrs", torch.int64)
     _need(Y, f"{name} Y", _torch_dtype(problem)); _need_shape(Y, f"{name} Y", (problem.n_rows, problem.h_out))
     _need(ranks, f"{name} ranks", torch.int32); _need(scales, f"{name} scales", torch.float32)
+    for t, what in ((A_ptrs, "A_ptrs"), (B_ptrs, "B_ptrs"), (ranks, "ranks"), (scales, "scales")):
+        _need_len(t, f"{name} {what}", problem.num_loras)
     return sgmv_projection_t(_ptr(A_ptrs), _ptr(B_ptrs), _ptr(Y), _ptr(ranks), _ptr(scales))
 
 
@@ -486,6 +494,7 @@ def _layer_grad(problem, grad, name):
     dW, dA_ptrs, dB_ptrs = (tuple(grad) + (None,) * 3)[:3] if grad is not None else (None,) * 3
     _need(dW, f"{name} dW", _torch_dtype(problem)); _need_shape(dW, f"{name} dW", (problem.h_in, problem.h_out))
     _need(dA_ptrs, f"{name} dA_ptrs", torch.int64); _need(dB_ptrs, f"{name} dB_ptrs", torch.int64)
+    _need_len(dA_ptrs, f"{name} dA_ptrs", problem.num_loras); _need_len(dB_ptrs, f"{name} dB_ptrs", problem.num_loras)
     return sgmv_projection_grad_t(_ptr(dW), _ptr(dA_ptrs), _ptr(dB_ptrs))
 
 

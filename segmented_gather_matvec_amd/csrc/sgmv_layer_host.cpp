@@ -84,10 +84,12 @@ ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products) {
   return t;
 }
 
+// Row splits of one LoRA's gradient over columns C; all products' tiles share a launch.
 int plan_grad_split(const sgmv_problem_t& p, int64_t C, int products) {
-  const int64_t wgs = (int64_t)p.num_loras * ceil_div(C, sgmv::kLoraGradCols) * products;
+  const int64_t wgs = (int64_t)p.num_loras * products *
+                      (ceil_div(p.h_in, sgmv::kLoraGradCols) + ceil_div(p.h_out, sgmv::kLoraGradCols));
   const int64_t bytes = (int64_t)p.num_loras * C * p.rank * 4 * products;
-  const int64_t fill = ceil_div(1024, std::max<int64_t>(1, wgs));
+  const int64_t fill = ceil_div(768, std::max<int64_t>(1, wgs));
   const int64_t steps = ceil_div(p.n_rows, 4 * sgmv::kDenseK);  // at least four steps each
   const int64_t longest = ceil_div(p.max_seg_len, 32 * sgmv::kDenseK);  // one long segment alone
   // The planes are written and read once each: no more of them than Z has bytes.

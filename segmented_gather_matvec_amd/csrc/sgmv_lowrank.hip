@@ -78,20 +78,25 @@ struct LoraGradBatch {
 };
 
 template <class T, int R>
-__global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch batch) {
-  constexpr int ROWS = kDenseK, COLS = kLoraGradCols, QC = 2 * R, JT = R < 16 ? 1 : R / 16;
-  constexpr int STAGES = R == 64 ? 3 : 4;  // two workgroups per CU
-  constexpr bool F16T = T::kMaxFinite < 1e6f;
+struct LoraGradShape {
+  static constexpr bool F16T = T::kMaxFinite < 1e6f;
+  static constexpr int ROWS = kDenseK, COLS = kLoraGradCols, QC = 2 * R, JT = R < 16 ? 1 : R / 16;
+  static constexpr int STAGES = R == 64 ? 3 : 4;  // two workgroups per CU
+  static constexpr int B0 = COLS * ROWS, S0 = B0 + QC * ROWS, SLOT = S0 + (F16T ? 128 : 0);  // Z, V16, row scales
+};
+
+// RANK_MAJOR: a lane ends up with 4 columns of one rank; else with 4 ranks of one column.
+template <class T, int R, bool RANK_MAJOR>
+__device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, int* lds_lo, int* lds_hi, int* lds_count) {
+  using S = LoraGradShape<T, R>;
+  constexpr bool F16T = S::F16T;
+  constexpr int ROWS = S::ROWS, COLS = S::COLS, QC = S::QC, JT = S::JT, STAGES = S::STAGES;
+  constexpr int B0 = S::B0, S0 = S::S0, SLOT = S::SLOT;
   constexpr int LZ = COLS / 16 / kWaves, LQ = QC / 16 < kWaves ? 1 : QC / 16 / kWaves;
-  constexpr int B0 = COLS * ROWS, S0 = B0 + QC * ROWS, SLOT = S0 + (F16T ? 128 : 0);  // Z, V16, row scales
   constexpr int kPerStep = LZ + LQ + (F16T ? 1 : 0);
-  const LoraGradParams& p = batch.p[blockIdx.y];
   const int ctiles = (p.C + COLS - 1) / COLS;
   const int k = (int)blockIdx.x / ctiles;
   if (k >= p.meta.num_loras || (int)blockIdx.z >= p.nsplit) return;
-  __shared__ __attribute__((aligned(1024))) uint16_t lds[STAGES * SLOT];
-  __shared__ int lds_lo[kThreads], lds_hi[kThreads];
-  __shared__ int lds_count[kWaves];
   const int t = threadIdx.x;
   const int lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -118,13 +123,11 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch 
   for (int s0 = 0; s0 < p.meta.num_segs; s0 += kThreads) {
     // The window's segments of LoRA k, in order.
     const int s = s0 + t;
-    int lo = 0, hi = 0;
-    if (s < p.meta.num_segs && p.meta.lora_idx[s] == k) {
-      lo = p.meta.seg_indptr[s];
-      hi = p.meta.seg_indptr[s + 1];
-      hi = hi < p.meta.n_rows ? hi : p.meta.n_rows;
-    }
-    const bool hit = lo >= 0 && hi > lo;
+    const int sc = s < p.meta.num_segs ? s : p.meta.num_segs - 1;
+    const int id = p.meta.lora_idx[sc], lo = p.meta.seg_indptr[sc];
+    int hi = p.meta.seg_indptr[sc + 1];
+    hi = hi < p.meta.n_rows ? hi : p.meta.n_rows;
+    const bool hit = s < p.meta.num_segs && id == k && lo >= 0 && hi > lo;
     const unsigned long long m = __ballot(hit);
     __syncthreads();
     if (lane == 0) lds_count[wave] = __popcll(m);
@@ -217,14 +220,11 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch 
             }
           }
         }
-        // rank_major: lane holds 4 columns of one rank; else 4 ranks of one column.
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = QC / 16 - 1; j >= 0; --j)  // lo halves first
 #pragma unroll
-          for (int j = QC / 16 - 1; j >= 0; --j) {  // lo halves first
-            f32x4& a = acc[i][j % JT];
-            a = p.rank_major ? mfma<T>(zf[i], qf[j], a) : mfma<T>(qf[j], zf[i], a);
-          }
+          for (int i = 0; i < 4; ++i)
+            acc[i][j % JT] = RANK_MAJOR ? mfma<T>(zf[i], qf[j], acc[i][j % JT]) : mfma<T>(qf[j], zf[i], acc[i][j % JT]);
         slot = slot + 1 == STAGES ? 0 : slot + 1;
       }
       wait_loads_and_lds<0>();
@@ -237,21 +237,21 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch 
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < JT; ++j) {
-      const int c = c0 + wave * 64 + i * 16 + (p.rank_major ? q * 4 : ml);
-      const int r = j * 16 + (p.rank_major ? ml : q * 4);
+      const int c = c0 + wave * 64 + i * 16 + (RANK_MAJOR ? q * 4 : ml);
+      const int r = j * 16 + (RANK_MAJOR ? ml : q * 4);
       f32x4 v = acc[i][j];
       if constexpr (R == 8) {  // ranks 8..15 are the lo halves' sums of ranks 0..7
 #pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] += p.rank_major ? shfl_xor(v[x], 8) : shfl_xor(v[x], 32);
+        for (int x = 0; x < 4; ++x) v[x] += RANK_MAJOR ? shfl_xor(v[x], 8) : shfl_xor(v[x], 32);
       }
       if (c >= p.C || r >= rk) continue;
       if constexpr (F16T) v *= unit;
       if (p.nsplit > 1) {
         float* dst = p.planes + ((int64_t)z * p.meta.num_loras + k) * p.C * R +
-                     (p.rank_major ? (int64_t)r * p.C + c : (int64_t)c * R + r);
+                     (RANK_MAJOR ? (int64_t)r * p.C + c : (int64_t)c * R + r);
         *reinterpret_cast<f32x4*>(dst) = v;
       } else {
-        uint16_t* dst = out + (p.rank_major ? (int64_t)r * p.C + c : (int64_t)c * rk + r);
+        uint16_t* dst = out + (RANK_MAJOR ? (int64_t)r * p.C + c : (int64_t)c * rk + r);
         if (p.accumulate) {
           const u32x2 old = *reinterpret_cast<const u32x2*>(dst);
           v[0] += T::lo(old[0]);
@@ -264,6 +264,19 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch 
                   (uint32_t)T::round(v[2]) | ((uint32_t)T::round(v[3]) << 16)};
       }
     }
+}
+
+template <class T, int R>
+__global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch batch) {
+  using S = LoraGradShape<T, R>;
+  __shared__ __attribute__((aligned(1024))) uint16_t lds[S::STAGES * S::SLOT];
+  __shared__ int lds_lo[kThreads], lds_hi[kThreads];
+  __shared__ int lds_count[kWaves];
+  const LoraGradParams& p = batch.p[blockIdx.y];
+  if (p.rank_major)
+    lora_grad_body<T, R, true>(p, lds, lds_lo, lds_hi, lds_count);
+  else
+    lora_grad_body<T, R, false>(p, lds, lds_lo, lds_hi, lds_count);
 }
 
 // Sums the splits' planes of one LoRA's gradient (split order), four values per thread.

@@ -44,7 +44,7 @@ __device__ inline void store_v(const ThinParams& p, int row, int c, float (&v)[8
 // LDS slots (sgmv_tile.h).  Bound by reading Z.
 template <int JT>
 struct ThinShape {
-  static constexpr int COLS = JT * 16, STAGES = 4;
+  static constexpr int COLS = JT * 16, STAGES = JT == 4 ? 3 : 4;  // three or four workgroups per CU
   // A slot: two steps of 32 (the halves of Z's 128-byte lines are asked for together), each Z then D.
   static constexpr int B0 = kThinRows * kDenseK, HALF = (kThinRows + COLS) * kDenseK, SLOT = 2 * HALF;
   static constexpr int RST = COLS + 4;  // row stride of the result in LDS (floats)

@@ -421,3 +421,73 @@ def test_same_call_twice_is_bitwise_equal():
         assert torch.equal(a[0], b[0])
         for x, y in zip(a[1], b[1]):
             assert torch.equal(x[0], y[0]) and all(torch.equal(s, t) for s, t in zip(x[1] + x[2], y[1] + y[2]))
+
+
+@pytest.mark.parametrize("n,h_in,h_out", [(60, 136, 264), (420, 264, 520)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_broken_lora_stays_with_its_own_rows(n, h_in, h_out, bad):
+    """NaN or infinity in one LoRA's matrices reaches that LoRA's rows only, where the tiles add the term and where
+    the epilogue does, and dX likewise."""
+    c = lr.Layer(81, "bf16", n, h_in, h_out, 16, 3, "none", 2, None, False)
+    c.seg, c.ids = [0, n // 3 + 1, n // 2 + 3, n], [0, 2, 1]
+    before = run_gated(c, "bf16", 0), run_gated_back(c, "bf16", 0, train_w=False)[0], run_dense(c, "bf16")
+    for p in c.proj:
+        p["A"][2][5] = bad
+        p["B"][2][3, 7] = bad
+    after = run_gated(c, "bf16", 0), run_gated_back(c, "bf16", 0, train_w=False)[0], run_dense(c, "bf16")
+    mine = slice(c.seg[1], c.seg[2])
+    others = [i for i in range(n) if not c.seg[1] <= i < c.seg[2]]
+    for a, b in list(zip(before[0], after[0])) + [(before[1], after[1]), (before[2], after[2])]:
+        assert torch.equal(a[others], b[others])
+        assert not torch.isfinite(b[mine]).all()
+
+
+@pytest.mark.parametrize("wide", ["in", "out"])
+def test_offsets_beyond_32_bits(wide):
+    """X (or dY) of more than 2^31 elements, zero but for the last rows: outputs of those rows and the gradients,
+    which only they reach, against 64 bits on those rows alone."""
+    big, tail = 4104, 700
+    n = 2 ** 31 // big + 2000
+    h_in, h_out = (big, 24) if wide == "in" else (24, big)
+    c = lr.Layer(91, "bf16", tail, h_in, h_out, 8, 2, "none", 1, None, False)
+    small = lr.Layer(91, "bf16", tail, h_in, h_out, 8, 2, "none", 1, None, False)
+    c.n = n
+    for name, width in (("X", h_in), ("dY", h_out)):
+        full = torch.zeros(n, width, dtype=c.dtype, device="cuda")
+        full[-tail:] = getattr(small, name)
+        setattr(c, name, full)
+    c.seg, c.ids = [0, n - 300, n], [0, 1]
+    small.seg, small.ids = [0, tail - 300, tail], [0, 1]
+    Y = run_dense(c, "bf16")
+    lr.check(Y[-tail:], *lr.project(small, small.proj[0]), c.dtype, "Y")
+    assert (Y[:-tail] == 0).all()
+    del Y
+    dX, grads = run_dense_back(c, "bf16")
+    d = small.dY.double()
+    small.n = n  # the bounds count every row that is summed
+    ref = lr.backward(small, small.proj[0], d, torch.zeros_like(d))
+    lr.check(dX[-tail:], *ref[0], c.dtype, "dX")
+    check_grads(c, grads, [ref])
+
+
+def test_binding_refuses_wrong_shapes():
+    c, dtype = case("mixed_r32", 1)
+    call = Call(c, sg.SGMV_DENSE_FORWARD, dtype)
+    Y = call.nan(c.n, c.h_out)
+    good = dict(X=c.X, W=c.proj[0]["W"], proj=call.projection(0, Y), seg=call.seg, ids=call.ids, ws=call.ws)
+
+    def run(**kw):
+        a = {**good, **kw}
+        sg.sgmv_dense_lora_apply(call.problem, a["X"], a["W"], a["proj"], a["seg"], a["ids"], a["ws"])
+
+    run()
+    A, B, Yp, ranks, scales = good["proj"]
+    for kw in (dict(X=c.X[:-1]), dict(W=c.proj[0]["W"].t()), dict(W=c.proj[0]["W"].float()), dict(X=c.X.cpu()),
+               dict(proj=(A[:-1], B, Yp, ranks, scales)), dict(proj=(A, B[:1], Yp, ranks, scales)),
+               dict(proj=(A, B, Yp[:, :8], ranks, scales)), dict(proj=(A, B, Yp, ranks, scales[:-1])),
+               dict(proj=(A, B, Yp, call.ids[:1], scales)), dict(seg=call.seg[:-1]), dict(ids=call.ids[:-1]),
+               dict(seg=call.seg.long())):
+        with pytest.raises(ValueError):
+            run(**kw)
+    with pytest.raises(sg.SgmvError):
+        run(ws=call.ws[:-16])
