@@ -229,7 +229,8 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
 
   // Steps of the contraction: all of pair 0, then all of pair 1.
   const int kt = (p.K + kDenseK - 1) / kDenseK;
-  const int steps_all = kt * (MODE == kDenseDx ? p.pairs : 1);
+  constexpr bool PAIRS = MODE == kDenseDx || MODE == kDenseDw;
+  const int steps_all = kt * (PAIRS ? p.pairs : 1);
   const int first = g * p.ktiles_per_split;
   const int last = first + p.ktiles_per_split < steps_all ? first + p.ktiles_per_split : steps_all;
 
@@ -241,21 +242,22 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
   la.init(wave, lane, p.lda);
   lb.init(wave - sub * WB, lane, p.ldb);
 
-  // Steps first .. last - 1 of the contraction, in order; dX may go on from pair 0 to pair 1.
+  // Steps first .. last - 1 of the contraction, in order; dX and dW may go on from pair 0 to pair 1.
   auto start = [&](int s) {
-    const int pair = MODE == kDenseDx && s >= kt ? 1 : 0;
+    const int pair = PAIRS && s >= kt ? 1 : 0;
     const int k0 = (s - pair * kt) * kDenseK;
     const int in_pair = (last - pair * kt < kt ? last - pair * kt : kt) * kDenseK;
     const int K = in_pair < p.K ? in_pair : p.K;
     const int bi = MODE == kDenseDw ? proj : S::GATED ? sub : pair;
     la.start(MODE == kDenseDx && pair ? p.A[1] : p.A[0], p.lda, m0, p.M, k0, K);
-    lb.start(bi ? p.B[1] : p.B[0], p.ldb, n0, p.N, k0, K);
+    const int64_t behind = MODE == kDenseDw && pair ? (int64_t)p.K * p.ldb : 0;
+    lb.start((bi ? p.B[1] : p.B[0]) + behind, p.ldb, n0, p.N, k0, K);
   };
-  int left_in_pair = kt - first;  // steps before the second pair starts (dX)
+  int left_in_pair = kt - first;  // steps before the second pair starts
   auto issue = [&](int slot) {
     la.issue(lds[slot]);
     lb.issue(lds[slot] + B0 + sub * S::C * kDenseK);
-    if constexpr (MODE == kDenseDx) {
+    if constexpr (PAIRS) {
       if (--left_in_pair == 0 && last > kt) start(kt);
     }
   };
@@ -391,6 +393,8 @@ __device__ inline ThinParams pick(const ThinParams& a, const ThinParams& b, bool
   t.V16 = nullptr;  // V stays in planes, or is the one plane
   t.row_scale = nullptr;
   t.planes = first ? a.planes : b.planes;
+  t.to_planes = a.to_planes;
+  t.sum_planes = 0;
   t.row_k = first ? a.row_k : nullptr;  // the same for both
   t.K = a.K;
   t.rank = a.rank;

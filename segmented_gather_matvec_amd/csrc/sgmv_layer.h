@@ -40,7 +40,7 @@ enum DenseMode : int {
 struct DenseParams {
   int32_t M, N, K;       // output rows and columns, contraction length (of one operand pair)
   int32_t lda, ldb;      // row strides (elements) of the operands as stored
-  int32_t pairs;         // dX: operand pairs summed (1 or 2)
+  int32_t pairs;         // operand pairs summed (1 or 2); dW: the second is X with the K rows behind B's first K
   int32_t projections;   // dW: projections (grid y)
   int32_t tiles_m, tiles_n;
   int32_t ksplit;        // workgroups sharing one output tile
@@ -71,7 +71,9 @@ struct ThinParams {
   float* V;               // null, or [n_rows][rank] fp32
   uint16_t* V16;          // null, or [n_rows][2][rank] hi and lo halves (see LowRankTerm)
   float* row_scale;       // with V16 in fp16: [n_rows]
-  float* planes;          // [ksplit][n_rows][rank] (ksplit > 1)
+  float* planes;          // [ksplit][n_rows][rank], written when to_planes
+  int32_t to_planes;      // 1: partial planes (ksplit > 1, or a sum over several products)
+  int32_t sum_planes;     // planes from `planes` on that make V (0: another product's sum has them)
   int32_t* row_k;         // null, or [n_rows] the LoRA of each covered row, written
   int32_t K, rank, transposed;
   int32_t units, direct;  // units of <= kThinRows rows of one segment
@@ -88,13 +90,15 @@ hipError_t launch_dense_thin(int dtype, int mode, int cfg, const DenseParams& p,
 // the activation (gated) and writes the outputs.
 hipError_t launch_dense_epilogue(int dtype, int mode, const DenseParams& p, hipStream_t stream);
 
-// count products (at most 4) in one launch; the plane sum follows when a ksplit > 1.
+// count products (at most kMaxThin) in one launch; the plane sums follow.
+constexpr int kMaxThin = 6;
 hipError_t launch_thin(int dtype, const ThinParams* p, int count, hipStream_t stream);
 
 // Gradients of the LoRA matrices, out[c, j] = sum_{rows i of LoRA k} Z[i, c] * Q[i, j]
 // stored [C, r_k] (dA_k: Z = X, Q = s_k dY @ B_k^T) or [r_k, C] (dB_k: Z = dY, Q = s_k X @ A_k).
 struct LoraGradParams {
-  const uint16_t* Z;      // [n_rows, C]
+  const uint16_t* Z;      // [n_rows, C], or [2 n_rows, C]: hi halves, then lo (passes = 2)
+  int32_t passes;
   const uint16_t* Q;      // [n_rows][2][rank] hi and lo halves (see LowRankTerm)
   const float* row_scale; // fp16: of Q's rows
   const uint64_t* out;    // [num_loras] -> gradient (0: not wanted)
@@ -108,8 +112,9 @@ struct LoraGradParams {
 // count gradients (at most 4) in one launch; the plane sum follows when an nsplit > 1.
 hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipStream_t stream);
 
-// dG = dH * U * act'(G), dU = dH * act(G), rounded once to the 16-bit format.
-hipError_t launch_gate_backward(int dtype, int act, const uint16_t* G, const uint16_t* U, const uint16_t* dH,
-                                uint16_t* dG, uint16_t* dU, int64_t n, hipStream_t stream);
+// dG = dH * U * act'(G), dU = dH * act(G) (n values each), rounded once to the 16-bit format, or (halves) as hi
+// halves followed by lo halves.
+hipError_t launch_gate_backward(int dtype, int act, bool halves, const uint16_t* G, const uint16_t* U,
+                                const uint16_t* dH, uint16_t* dG, uint16_t* dU, int64_t n, hipStream_t stream);
 
 }  // namespace sgmv

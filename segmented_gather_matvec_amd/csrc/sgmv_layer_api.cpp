@@ -77,6 +77,8 @@ void thin_params(const Call& c, bool up, const void* const* Z, bool full, bool h
     t[i].V16 = halves ? reinterpret_cast<uint16_t*>(c.at(c.plan.half_off[up][i])) : nullptr;
     t[i].row_scale = c.at(c.plan.row_scale_off[up][i]);
     t[i].planes = c.at(c.plan.thin_off[up][i]);
+    t[i].to_planes = plan.planes > 0;
+    t[i].sum_planes = plan.planes;
     t[i].K = up ? c.p.h_out : c.p.h_in;
     t[i].rank = c.p.rank;
     t[i].transposed = up ? 1 : 0;
@@ -85,6 +87,16 @@ void thin_params(const Call& c, bool up, const void* const* Z, bool full, bool h
     t[i].ksplit = plan.ksplit;
     t[i].kc = plan.kc;
     t[i].meta = c.meta;
+  }
+}
+
+// The lo halves' part of dV, in the planes behind the hi halves' (which t holds).
+void thin_lo(const Call& c, const sgmv::ThinParams* t, sgmv::ThinParams* lo) {
+  for (int i = 0; i < c.np; ++i) {
+    lo[i] = t[i];
+    lo[i].Z += (size_t)c.p.n_rows * c.p.h_out;
+    lo[i].planes += (size_t)c.plan.up.ksplit * c.p.n_rows * c.p.rank;
+    lo[i].sum_planes = 0;
   }
 }
 
@@ -132,10 +144,15 @@ sgmv::LowRankTerm term(const Call& c, int i, bool up, const void* ptrs) {
   return t;
 }
 
-sgmv_status_t run_dense(const Call& c, int mode, const DensePlan& d, const sgmv::DenseParams& q) {
+// fold = 2: the product's second half of rows adds onto the first (a plane of 2 n rows is two planes of n).
+sgmv_status_t run_dense(const Call& c, int mode, const DensePlan& d, const sgmv::DenseParams& q, int fold = 1) {
   if (sgmv::launch_dense(c.p.dtype, mode, d.cfg, q, c.stream) != hipSuccess) return SGMV_ERR_HIP;
-  if (q.to_planes && sgmv::launch_dense_epilogue(c.p.dtype, mode, q, c.stream) != hipSuccess) return SGMV_ERR_HIP;
-  return SGMV_OK;
+  if (!q.to_planes) return SGMV_OK;
+  sgmv::DenseParams e = q;
+  e.M /= fold;
+  e.ksplit *= fold;
+  e.plane_stride /= fold;
+  return sgmv::launch_dense_epilogue(c.p.dtype, mode, e, c.stream) == hipSuccess ? SGMV_OK : SGMV_ERR_HIP;
 }
 
 sgmv_status_t forward(const Call& c, void* const* out) {
@@ -177,12 +194,16 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
     want_b = want_b || grad[i]->dB_ptrs;
   }
   if (c.plan.lora) {  // V for dB, dV for dX and dA, in one launch
-    sgmv::ThinParams t[4];
+    sgmv::ThinParams t[sgmv::kMaxThin];
     int count = 0;
     if (want_a || dX) {
       const bool full = dX && !c.plan.out.term_in_tile;
       thin_params(c, true, dY, full, want_a || !full, t);
       count = c.np;
+      if (c.plan.halves > 1) {
+        thin_lo(c, t, t + count);
+        count += c.np;
+      }
     }
     if (want_b) {
       const void* Z[2] = {c.X, c.X};
@@ -192,7 +213,8 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
     if (sgmv::launch_thin(c.p.dtype, t, count, c.stream) != hipSuccess) return SGMV_ERR_HIP;
   }
   if (dX && rows) {
-    sgmv::DenseParams q = dense_params(c, c.plan.out, c.p.n_rows, c.p.h_in, c.p.h_out, c.p.h_out, c.p.h_out);
+    sgmv::DenseParams q = dense_params(c, c.plan.out, (int64_t)c.p.n_rows * c.plan.halves, c.p.h_in, c.p.h_out, c.p.h_out,
+                                       c.p.h_out);
     q.pairs = c.np;
     for (int i = 0; i < c.np; ++i) {
       q.A[i] = half(dY[i]);
@@ -200,12 +222,14 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
       if (c.plan.lora) q.term[i] = term(c, i, true, c.proj[i]->A_ptrs);
     }
     q.out[0] = static_cast<uint16_t*>(dX);
-    const sgmv_status_t st = run_dense(c, sgmv::kDenseDx, c.plan.out, q);
+    const sgmv_status_t st = run_dense(c, sgmv::kDenseDx, c.plan.out, q, c.plan.halves);
     if (st != SGMV_OK) return st;
   }
   // dW of the projections that want it, one launch when both do.
   sgmv::DenseParams w = dense_params(c, c.plan.dw, c.p.h_in, c.p.h_out, c.p.n_rows, c.p.h_in, c.p.h_out);
   w.projections = 0;
+  w.pairs = c.plan.halves;
+  w.ktiles_per_split *= c.plan.halves;
   w.A[0] = half(c.X);
   w.accumulate = accumulate;
   for (int i = 0; i < c.np; ++i) {
@@ -229,6 +253,7 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
       if (!out) continue;
       sgmv::LoraGradParams& e = g[count++];
       e.Z = half(b ? dY[i] : c.X);
+      e.passes = b ? c.plan.halves : 1;
       e.Q = reinterpret_cast<const uint16_t*>(c.at(c.plan.half_off[!b][i]));
       e.row_scale = c.at(c.plan.row_scale_off[!b][i]);
       e.out = table(out);
@@ -349,7 +374,7 @@ sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* p, const void* X, c
                static_cast<char*>(ws), static_cast<hipStream_t>(stream), act};
   uint16_t* d[2] = {reinterpret_cast<uint16_t*>(c.at(plan.gate_off[0])), reinterpret_cast<uint16_t*>(c.at(plan.gate_off[1]))};
   if (p->n_rows > 0 &&
-      sgmv::launch_gate_backward(p->dtype, act, half(gate->Y), half(up->Y), half(dH), d[0], d[1],
+      sgmv::launch_gate_backward(p->dtype, act, plan.halves > 1, half(gate->Y), half(up->Y), half(dH), d[0], d[1],
                                  (int64_t)p->n_rows * p->h_out, c.stream) != hipSuccess)
     return SGMV_ERR_HIP;
   const void* dY[2] = {d[0], d[1]};

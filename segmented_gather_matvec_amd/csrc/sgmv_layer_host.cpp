@@ -10,6 +10,10 @@ namespace {
 
 constexpr int64_t kCus = 256;                          // compute units of an MI355X
 constexpr int64_t kGradPlaneBytes = (int64_t)256 << 20;  // most the splits of a LoRA gradient may take
+// Rows up to which the gated backward carries dG and dU unrounded (hi + lo halves): its products are
+// bound by reading W there, and a few large values' rounding would show in dX and dA (up to 1.7 times the
+// error of an output's own rounding; 1.4 times where it averages out over many rows).
+constexpr int kHalvesRows = 64;
 constexpr int kShortRun = 16;  // rows per segment from which the tiles' matrix cores add the LoRA term
 
 // Workgroups of a tile shape that run at once on one CU (LDS).
@@ -65,7 +69,8 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
   return best;
 }
 
-ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products) {
+// products: that share the launch; summed: whose planes make one V.
+ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products, int summed) {
   ThinPlan t;
   if (p.max_seg_len <= sgmv::kThinRows) {
     t.units = p.num_segs;
@@ -80,7 +85,8 @@ ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products) {
   const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(want, ceil_div(K, 256)));
   t.kc = (int)round_up(ceil_div(K, ks), sgmv::kDenseK);
   t.ksplit = (int)ceil_div(K, t.kc);
-  t.plane_bytes = t.ksplit > 1 ? (size_t)t.ksplit * p.n_rows * p.rank * sizeof(float) : 0;
+  t.planes = t.ksplit * summed > 1 ? t.ksplit * summed : 0;
+  t.plane_bytes = (size_t)t.planes * p.n_rows * p.rank * sizeof(float);
   return t;
 }
 
@@ -104,6 +110,7 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   LayerPlan l;
   l.projections = layer_gated(op) ? 2 : 1;
   l.lora = !nothing_to_do(p);
+  l.halves = op == SGMV_GATED_BACKWARD && p.n_rows <= kHalvesRows ? 2 : 1;
   const int64_t n = p.n_rows;
   const bool back = layer_backward(op);
   size_t at = 0;
@@ -114,8 +121,8 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   };
   if (l.lora) {
     const size_t v = (size_t)n * p.rank * sizeof(float);
-    l.down = plan_thin(p, p.h_in, l.projections);
-    if (back) l.up = plan_thin(p, p.h_out, l.projections);
+    l.down = plan_thin(p, p.h_in, l.projections, 1);
+    if (back) l.up = plan_thin(p, p.h_out, l.projections * l.halves, l.halves);
     for (int i = 0; i < l.projections; ++i) {
       for (int d = 0; d < (back ? 2 : 1); ++d) {
         l.v_off[d][i] = take(v);
@@ -126,16 +133,16 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
     }
   }
   if (op == SGMV_GATED_BACKWARD)
-    for (int i = 0; i < 2; ++i) l.gate_off[i] = take((size_t)n * p.h_out * 2);
+    for (int i = 0; i < 2; ++i) l.gate_off[i] = take((size_t)n * l.halves * p.h_out * 2);
   // The LoRA term joins in the tiles where segments are long enough for a
   // matrix instruction's 16 rows; else the epilogue launch adds it row by row.
   const bool in_tile = l.lora && n > 128 && n >= (int64_t)kShortRun * p.num_segs;
-  const int64_t M = n, N = back ? p.h_in : p.h_out;
+  const int64_t M = n * l.halves, N = back ? p.h_in : p.h_out;
   const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK);
   const int cols = op == SGMV_GATED_FORWARD ? 2 : 1;
   l.out = plan_dense(M, N, kt * (op == SGMV_GATED_BACKWARD ? 2 : 1), cols, true);
   l.out.term_in_tile = in_tile ? 1 : 0;
-  l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile);
+  l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile) || l.halves > 1;
   // (The largest tile's workgroups are too big to share a launch with.)
   l.one_launch = l.lora && !back && l.out.to_planes && !in_tile && l.out.cfg != sgmv::kTile256;
   if (l.one_launch) l.row_k_off = take((size_t)n * sizeof(int32_t));

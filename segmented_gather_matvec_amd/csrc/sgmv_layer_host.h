@@ -20,13 +20,15 @@ struct DensePlan {
 
 struct ThinPlan {
   int units = 0, direct = 1, ksplit = 1, kc = 128;
-  size_t plane_bytes = 0;  // of one product
+  int planes = 0;          // partial planes of one V (0: written at once)
+  size_t plane_bytes = 0;  // of them
 };
 
 struct LayerPlan {
   bool lora = false;
   int projections = 1;
   DensePlan out;       // forward, or dX
+  int halves = 1;      // 2: the gated backward keeps dG and dU as hi and lo halves, 2 n rows (few rows)
   bool one_launch = false;  // the thin products run in the dense product's launch, the epilogue sums their planes
   DensePlan dw;        // dW
   ThinPlan down;       // V = s_k X @ A_k        (K = h_in)

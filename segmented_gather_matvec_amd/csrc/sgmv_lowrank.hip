@@ -15,9 +15,9 @@ namespace sgmv {
 namespace {
 
 // ---------------------------------------------------------------- thin products
-// Up to four products in one launch (grid y).
+// The products of one launch (grid y).
 struct ThinBatch {
-  ThinParams p[4];
+  ThinParams p[kMaxThin];
 };
 
 template <class T, int JT>
@@ -36,24 +36,24 @@ __global__ __launch_bounds__(kThreads) void sgmv_thin_kernel(ThinBatch batch) {
 template <class T>
 __global__ __launch_bounds__(kThreads) void sgmv_thin_sum_kernel(ThinBatch batch) {
   const ThinParams& p = batch.p[blockIdx.y];
-  if (p.ksplit <= 1) return;  // written by the product itself
+  if (p.sum_planes < 1) return;  // written by the product itself, or part of another's sum
   constexpr int kBatch = 8;   // planes in flight
   const int per_row = p.rank / 8;
   const int64_t n = (int64_t)p.meta.n_rows * p.rank;
   const int64_t x = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   if (x * 8 >= n) return;
   float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int g0 = 0; g0 < p.ksplit; g0 += kBatch) {
+  for (int g0 = 0; g0 < p.sum_planes; g0 += kBatch) {
     f32x4 a[kBatch], b[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const float* src = p.planes + (g0 + u < p.ksplit ? g0 + u : p.ksplit - 1) * n + x * 8;
+      const float* src = p.planes + (g0 + u < p.sum_planes ? g0 + u : p.sum_planes - 1) * n + x * 8;
       a[u] = *reinterpret_cast<const f32x4*>(src);
       b[u] = *reinterpret_cast<const f32x4*>(src + 4);
     }
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const bool live = g0 + u < p.ksplit;
+      const bool live = g0 + u < p.sum_planes;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[e] = live ? v[e] + a[u][e] : v[e];
@@ -146,90 +146,94 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
     count = __builtin_amdgcn_readfirstlane(count);
     any = any || count > 0;
     // This split's steps of the window, in order: step st of segment e, which has `steps`.
-    int e = -1, st = z - counter % p.nsplit, row = 0, end = 0, steps = 0, mine = 0;
-    if (st < 0) st += p.nsplit;
+    int st_first = z - counter % p.nsplit, mine = 0;
+    if (st_first < 0) st_first += p.nsplit;
     {
       int all = 0;
       for (int x = lane; x < count; x += 64) all += (lds_hi[x] - lds_lo[x] + ROWS - 1) / ROWS;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) all += __shfl_xor(all, d, 64);
       all = __builtin_amdgcn_readfirstlane(all);
-      mine = all > st ? (all - st + p.nsplit - 1) / p.nsplit : 0;
+      mine = all > st_first ? (all - st_first + p.nsplit - 1) / p.nsplit : 0;
       counter += all;
     }
-    auto issue = [&](uint16_t* slot) {
-      while (st >= steps && e < count) {  // on to the segment that holds step st
-        st -= steps;
-        steps = 0;
-        if (++e < count) {
-          row = __builtin_amdgcn_readfirstlane(lds_lo[e]);
-          end = __builtin_amdgcn_readfirstlane(lds_hi[e]);
-          steps = (end - row + ROWS - 1) / ROWS;
-        }
-      }
-      const int r0 = e < count ? row + st * ROWS : 0;
-      const int n = e < count ? (end - r0 < ROWS ? end - r0 : ROWS) : 0;
-      lz.issue_rows(p.Z, p.C, c0, p.C, r0, n, slot);
-      lq.issue_rows(p.Q, QC, 0, QC, r0, n, slot + B0);
-      if constexpr (F16T) {
-        const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p.row_scale + r0), 0, n * 4, kRawBuffer);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(slot + S0), 4, lane * 4, 0, 0, 0);
-      }
-      st += p.nsplit;
-    };
-    if (mine > 0) {
-#pragma unroll
-      for (int x = 0; x < STAGES - 1; ++x) issue(lds + x * SLOT);
-      int slot = 0;
-      for (int x = 0; x < mine; ++x) {
-        wait_loads_and_lds<kPerStep*(STAGES - 2)>();
-        __builtin_amdgcn_s_barrier();
-        issue(lds + (slot == 0 ? STAGES - 1 : slot - 1) * SLOT);
-        const uint16_t* now = lds + slot * SLOT;
-        u32x4 zf[4], qf[QC / 16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) zf[i] = read_operand<COLS, true>(now, wave * 64 + i * 16, lane);
-#pragma unroll
-        for (int j = 0; j < QC / 16; ++j) qf[j] = read_operand<QC, true>(now + B0, j * 16, lane);
-        if constexpr (F16T) {
-          // Rows 8 q .. 8 q + 7 are this lane's contraction steps.
-          const float* sp = reinterpret_cast<const float*>(now + S0) + q * 8;
-          const f32x4 u0 = *reinterpret_cast<const f32x4*>(sp), u1 = *reinterpret_cast<const f32x4*>(sp + 4);
-          float big = fmaxf(fmaxf(fmaxf(u0[0], u0[1]), fmaxf(u0[2], u0[3])), fmaxf(fmaxf(u1[0], u1[1]), fmaxf(u1[2], u1[3])));
-          big = fmaxf(big, shfl_xor(big, 16));
-          big = fmaxf(big, shfl_xor(big, 32));
-          if (big > 1.f || unit > 1.f) {  // uniform over the wave
-            if (big > unit) {
-              const float f = unit / big;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < JT; ++j) acc[i][j] *= f;
-              unit = big;
-            }
-            float f[8];
-#pragma unroll
-            for (int x8 = 0; x8 < 8; ++x8) f[x8] = (x8 < 4 ? u0[x8 & 3] : u1[x8 & 3]) / unit;
-#pragma unroll
-            for (int j = 0; j < QC / 16; ++j) {
-              float v[8];
-              unpack8<T>(qf[j], v);
-#pragma unroll
-              for (int x8 = 0; x8 < 8; ++x8) v[x8] = f[x8] > 0.f ? v[x8] * f[x8] : v[x8];
-              qf[j] = pack8<T>(v);
-            }
+    for (int pass = 0; pass < p.passes; ++pass) {
+      const uint16_t* Z = p.Z + (int64_t)pass * p.meta.n_rows * p.C;
+      int e = -1, st = st_first, row = 0, end = 0, steps = 0;
+      auto issue = [&](uint16_t* slot) {
+        while (st >= steps && e < count) {  // on to the segment that holds step st
+          st -= steps;
+          steps = 0;
+          if (++e < count) {
+            row = __builtin_amdgcn_readfirstlane(lds_lo[e]);
+            end = __builtin_amdgcn_readfirstlane(lds_hi[e]);
+            steps = (end - row + ROWS - 1) / ROWS;
           }
         }
+        const int r0 = e < count ? row + st * ROWS : 0;
+        const int n = e < count ? (end - r0 < ROWS ? end - r0 : ROWS) : 0;
+        lz.issue_rows(Z, p.C, c0, p.C, r0, n, slot);
+        lq.issue_rows(p.Q, QC, 0, QC, r0, n, slot + B0);
+        if constexpr (F16T) {
+          const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p.row_scale + r0), 0, n * 4, kRawBuffer);
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(slot + S0), 4, lane * 4, 0, 0, 0);
+        }
+        st += p.nsplit;
+      };
+      if (mine > 0) {
 #pragma unroll
-        for (int j = QC / 16 - 1; j >= 0; --j)  // lo halves first
+        for (int x = 0; x < STAGES - 1; ++x) issue(lds + x * SLOT);
+        int slot = 0;
+        for (int x = 0; x < mine; ++x) {
+          wait_loads_and_lds<kPerStep*(STAGES - 2)>();
+          __builtin_amdgcn_s_barrier();
+          issue(lds + (slot == 0 ? STAGES - 1 : slot - 1) * SLOT);
+          const uint16_t* now = lds + slot * SLOT;
+          u32x4 zf[4], qf[QC / 16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            acc[i][j % JT] = RANK_MAJOR ? mfma<T>(zf[i], qf[j], acc[i][j % JT]) : mfma<T>(qf[j], zf[i], acc[i][j % JT]);
-        slot = slot + 1 == STAGES ? 0 : slot + 1;
+          for (int i = 0; i < 4; ++i) zf[i] = read_operand<COLS, true>(now, wave * 64 + i * 16, lane);
+#pragma unroll
+          for (int j = 0; j < QC / 16; ++j) qf[j] = read_operand<QC, true>(now + B0, j * 16, lane);
+          if constexpr (F16T) {
+            // Rows 8 q .. 8 q + 7 are this lane's contraction steps.
+            const float* sp = reinterpret_cast<const float*>(now + S0) + q * 8;
+            const f32x4 u0 = *reinterpret_cast<const f32x4*>(sp), u1 = *reinterpret_cast<const f32x4*>(sp + 4);
+            float big = fmaxf(fmaxf(fmaxf(u0[0], u0[1]), fmaxf(u0[2], u0[3])), fmaxf(fmaxf(u1[0], u1[1]), fmaxf(u1[2], u1[3])));
+            big = fmaxf(big, shfl_xor(big, 16));
+            big = fmaxf(big, shfl_xor(big, 32));
+            if (big > 1.f || unit > 1.f) {  // uniform over the wave
+              if (big > unit) {
+                const float f = unit / big;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                  for (int j = 0; j < JT; ++j) acc[i][j] *= f;
+                unit = big;
+              }
+              float f[8];
+#pragma unroll
+              for (int x8 = 0; x8 < 8; ++x8) f[x8] = (x8 < 4 ? u0[x8 & 3] : u1[x8 & 3]) / unit;
+#pragma unroll
+              for (int j = 0; j < QC / 16; ++j) {
+                float v[8];
+                unpack8<T>(qf[j], v);
+#pragma unroll
+                for (int x8 = 0; x8 < 8; ++x8) v[x8] = f[x8] > 0.f ? v[x8] * f[x8] : v[x8];
+                qf[j] = pack8<T>(v);
+              }
+            }
+          }
+#pragma unroll
+          for (int j = QC / 16 - 1; j >= 0; --j)  // lo halves first
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[i][j % JT] = RANK_MAJOR ? mfma<T>(zf[i], qf[j], acc[i][j % JT]) : mfma<T>(qf[j], zf[i], acc[i][j % JT]);
+          slot = slot + 1 == STAGES ? 0 : slot + 1;
+        }
+        wait_loads_and_lds<0>();
       }
-      wait_loads_and_lds<0>();
+      __syncthreads();  // the list and the slots are read before the next pass or window overwrites them
     }
-    __syncthreads();  // the list and the slots are read before the next window overwrites them
   }
   // A LoRA without rows keeps what it has when gradients accumulate.
   if (p.accumulate && !any) return;
@@ -322,8 +326,10 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBa
 // ---------------------------------------------------------------- gated block, elementwise backward
 // Eight values per thread; bound by memory (three reads, two writes).  dG and
 // dU are the matrix cores' operands of everything that follows, so they are
-// rounded to the 16-bit format here, once.
-template <class T>
+// rounded to the 16-bit format here, once.  HALVES (few rows): kept as hi halves and,
+// n values behind them, lo halves, which go through the same products as further rows: those
+// are bound by reading W then, and the error of a handful of large values does not average out.
+template <class T, bool HALVES>
 __global__ __launch_bounds__(kThreads) void sgmv_gate_backward_kernel(int act, const uint16_t* G, const uint16_t* U,
                                                                       const uint16_t* dH, uint16_t* dG, uint16_t* dU,
                                                                       int64_t n8) {
@@ -339,8 +345,18 @@ __global__ __launch_bounds__(kThreads) void sgmv_gate_backward_kernel(int act, c
       a[e] = h[e] * u[e] * slope;
       b[e] = h[e] * value;
     }
-    store_vec(dG + i * 8, pack8<T>(a));
-    store_vec(dU + i * 8, pack8<T>(b));
+    if constexpr (HALVES) {
+      u32x4 hi, lo;
+      split8<T>(a, hi, lo);
+      store_vec(dG + i * 8, hi);
+      store_vec(dG + (n8 + i) * 8, lo);
+      split8<T>(b, hi, lo);
+      store_vec(dU + i * 8, hi);
+      store_vec(dU + (n8 + i) * 8, lo);
+    } else {
+      store_vec(dG + i * 8, pack8<T>(a));
+      store_vec(dU + i * 8, pack8<T>(b));
+    }
   }
 }
 
@@ -348,11 +364,11 @@ template <class T>
 hipError_t launch_thin_t(const ThinParams* p, int count, hipStream_t s) {
   ThinBatch batch{};
   int64_t grid = 0;
-  int planes = 1;
+  bool sums = false;
   for (int i = 0; i < count; ++i) {
     batch.p[i] = p[i];
     grid = std::max(grid, (int64_t)p[i].units * p[i].ksplit);
-    planes = std::max(planes, p[i].ksplit);
+    sums = sums || p[i].sum_planes > 0;
   }
   if (grid > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 g((unsigned)grid, (unsigned)count);
@@ -364,7 +380,7 @@ hipError_t launch_thin_t(const ThinParams* p, int count, hipStream_t s) {
     default: return hipErrorInvalidValue;
   }
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || planes <= 1) return e;
+  if (e != hipSuccess || !sums) return e;
   const int64_t items = (int64_t)p[0].meta.n_rows * p[0].rank / 8;
   hipLaunchKernelGGL((sgmv_thin_sum_kernel<T>), dim3((unsigned)((items + kThreads - 1) / kThreads), (unsigned)count),
                      dim3(kThreads), 0, s, batch);
@@ -403,7 +419,7 @@ hipError_t launch_lora_grad_t(const LoraGradParams* p, int count, hipStream_t s)
 
 hipError_t launch_thin(int dtype, const ThinParams* p, int count, hipStream_t stream) {
   if (count < 1 || p[0].units <= 0) return hipSuccess;
-  if (count > 4) return hipErrorInvalidValue;
+  if (count > kMaxThin) return hipErrorInvalidValue;
   return dtype == 1 ? launch_thin_t<BF16>(p, count, stream) : launch_thin_t<F16>(p, count, stream);
 }
 
@@ -413,15 +429,19 @@ hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipSt
   return dtype == 1 ? launch_lora_grad_t<BF16>(p, count, stream) : launch_lora_grad_t<F16>(p, count, stream);
 }
 
-hipError_t launch_gate_backward(int dtype, int act, const uint16_t* G, const uint16_t* U, const uint16_t* dH,
-                                uint16_t* dG, uint16_t* dU, int64_t n, hipStream_t stream) {
+hipError_t launch_gate_backward(int dtype, int act, bool halves, const uint16_t* G, const uint16_t* U,
+                                const uint16_t* dH, uint16_t* dG, uint16_t* dU, int64_t n, hipStream_t stream) {
   const int64_t n8 = n / 8;
   if (n8 <= 0) return hipSuccess;
-  const unsigned grid = (unsigned)(n8 < (int64_t)kThreads * 8192 ? (n8 + kThreads - 1) / kThreads : 8192);
-  if (dtype == 1)
-    hipLaunchKernelGGL((sgmv_gate_backward_kernel<BF16>), dim3(grid), dim3(kThreads), 0, stream, act, G, U, dH, dG, dU, n8);
+  const dim3 grid((unsigned)(n8 < (int64_t)kThreads * 8192 ? (n8 + kThreads - 1) / kThreads : 8192)), block(kThreads);
+  if (dtype == 1 && halves)
+    hipLaunchKernelGGL((sgmv_gate_backward_kernel<BF16, true>), grid, block, 0, stream, act, G, U, dH, dG, dU, n8);
+  else if (dtype == 1)
+    hipLaunchKernelGGL((sgmv_gate_backward_kernel<BF16, false>), grid, block, 0, stream, act, G, U, dH, dG, dU, n8);
+  else if (halves)
+    hipLaunchKernelGGL((sgmv_gate_backward_kernel<F16, true>), grid, block, 0, stream, act, G, U, dH, dG, dU, n8);
   else
-    hipLaunchKernelGGL((sgmv_gate_backward_kernel<F16>), dim3(grid), dim3(kThreads), 0, stream, act, G, U, dH, dG, dU, n8);
+    hipLaunchKernelGGL((sgmv_gate_backward_kernel<F16, false>), grid, block, 0, stream, act, G, U, dH, dG, dU, n8);
   return hipGetLastError();
 }
 

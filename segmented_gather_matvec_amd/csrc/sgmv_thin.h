@@ -124,7 +124,7 @@ __device__ inline void thin_body(const ThinParams& p, int block, uint16_t* lds) 
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c < rk ? res[r * RST + c + e] * scale : 0.f;
-    if (p.ksplit > 1) {
+    if (p.to_planes) {
       float* dst = p.planes + ((int64_t)g * p.meta.n_rows + un.r0 + r) * p.rank + c;
       *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
       *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};

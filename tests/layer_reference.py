@@ -8,7 +8,7 @@ Bounds, per element, with h = eps / 2 of the 16-bit format (half a step: 2^-8 bf
   place per addition covers matrix cores that truncate);
 * V = s x@A and dV = s dy@B^T enter matrix products as hi + lo halves: h^2 of each value, plus, in
   fp16, half of the smallest denormal (2^-25) where lo underflows (relative to a row or tile scaled by 2^-e: below h^2 there);
-* dG, dU of the gated backward are rounded once: h of each;
+* dG, dU of the gated backward are rounded once: h of each; up to 64 rows they are two halves: h^2;
 * the activation in fp32: 2^-20 of the terms it is made of (exp and the divisions are good to a few
   units in the last place each).
 Errors of intermediate values propagate through the absolute values of what multiplies them.
@@ -162,6 +162,8 @@ def gate_backward(c, kind):
     a, slope = act(kind, g)
     floor = 2.0 ** -25 if c.dtype == torch.float16 else 0.0
     dg, du = dh * u * slope, dh * a
+    if c.n <= 64:
+        h = h * h
     eg = h * dg.abs() + 2.0 ** -20 * (dh * u).abs() * 1.13 * (1 + g.abs()) + floor
     eu = h * du.abs() + 2.0 ** -20 * (dh * g).abs() + floor
     return (dg, eg), (du, eu)

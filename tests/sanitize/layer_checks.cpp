@@ -51,8 +51,9 @@ static void check_problem(const sgmv_problem_t& p, int op) {
   const int64_t n = p.n_rows;
   if (n > 0) {
     const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK) * (op == SGMV_GATED_BACKWARD ? 2 : 1);
-    check_dense(l.out, n, back ? p.h_in : p.h_out, kt, op == SGMV_GATED_FORWARD ? 2 : 1);
+    check_dense(l.out, n * l.halves, back ? p.h_in : p.h_out, kt, op == SGMV_GATED_FORWARD ? 2 : 1);
     CHECK(l.out.ksplit == 1 || l.out.to_planes);
+    CHECK(l.halves == 1 || (op == SGMV_GATED_BACKWARD && l.out.to_planes && !l.out.term_in_tile));
     CHECK(!l.lora || l.out.term_in_tile || l.out.to_planes);  // the term is added somewhere
     seen_one_launch += l.one_launch;
     seen_in_tile += l.out.term_in_tile;
@@ -78,13 +79,15 @@ static void check_problem(const sgmv_problem_t& p, int op) {
         add(l.v_off[d][i], v);
         add(l.half_off[d][i], v);
         add(l.row_scale_off[d][i], (size_t)n * 4);
-        add(l.thin_off[d][i], t.ksplit > 1 ? (size_t)t.ksplit * v : 0);
+        const int sum = t.ksplit * (d ? l.halves : 1);
+        CHECK(t.planes == (sum > 1 ? sum : 0));
+        add(l.thin_off[d][i], (size_t)t.planes * v);
       }
     if (l.one_launch) add(l.row_k_off, (size_t)n * 4);
   }
   if (op == SGMV_GATED_BACKWARD)
-    for (int i = 0; i < 2; ++i) add(l.gate_off[i], (size_t)n * p.h_out * 2);
-  const size_t out = l.out.to_planes ? (size_t)l.out.ksplit * n * (back ? p.h_in : p.h_out) * 4 * (gated && !back ? 2 : 1) : 0;
+    for (int i = 0; i < 2; ++i) add(l.gate_off[i], (size_t)n * l.halves * p.h_out * 2);
+  const size_t out = l.out.to_planes ? (size_t)l.out.ksplit * n * l.halves * (back ? p.h_in : p.h_out) * 4 * (gated && !back ? 2 : 1) : 0;
   size_t grads = 0;
   if (back && l.lora) {
     if (l.nsplit_a > 1) grads += (size_t)l.nsplit_a * p.num_loras * p.h_in * p.rank * 4 * l.projections;
