@@ -21,10 +21,12 @@ int resident(int cfg) { return cfg == sgmv::kTile256 ? 1 : 2; }
 
 // The model that picks between tile shapes and splits; only ratios matter.
 // Large tiles are bound by the matrix cores: microseconds of one contraction
-// step of all workgroups resident on a CU.  The two small ones are bound by streaming B.
-constexpr double kStep256Us = 0.5, kStep128Us = 0.33;
+// step of one workgroup alone on its CU (measured: 8192 x 4096 -> 11008 in 6 rounds of 128 steps 616 us; 512 x 4096
+// -> 4096 in 128 x 128 tiles, two splits, one workgroup a CU, 24 us, and 26 us with four splits, two a CU).
+// The two small ones are bound by streaming B.
+constexpr double kStep256Us = 0.8, kStep128Us = 0.35;
 constexpr double kStreamBytesPerUs = 5.2e6;  // B of the small tiles, with every slot of the device taken
-constexpr double kPlaneBytesPerUs = 3.0e6;   // partial planes, written and read again
+constexpr double kPlaneBytesPerUs = 4.0e6;   // partial planes, written and read again
 
 DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, bool may_split) {
   // columns_per_n: 2 for a gated tile (gate and up columns side by side).
@@ -48,7 +50,7 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
       const int64_t wgs = tm * tn * ks, rounds = ceil_div(wgs, slots);
       double cost;
       if (cfg <= sgmv::kTile128) {
-        cost = (double)rounds * ((double)per * (cfg == sgmv::kTile256 ? kStep256Us : kStep128Us) + 4.0);
+        cost = (double)ceil_div(wgs, kCus) * ((double)per * (cfg == sgmv::kTile256 ? kStep256Us : kStep128Us)) + 4.0;
       } else {
         // Gated 4096 -> 11008, one row: 344, 430 and 516 workgroups on 512 slots took 37.8, 34.9 and 39.1 us.
         const double fill = (double)wgs / (double)(rounds * slots);
@@ -90,16 +92,18 @@ ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products, int summed)
   return t;
 }
 
-// Row splits of one LoRA's gradient over columns C; all products' tiles share a launch.
+// Row splits of one LoRA's gradient over columns C.  All products' tiles share a launch; LoRAs without
+// rows leave it at once and have no planes.
 int plan_grad_split(const sgmv_problem_t& p, int64_t C, int products) {
-  const int64_t wgs = (int64_t)p.num_loras * products *
+  const int64_t used = std::min(p.num_loras, p.num_segs);
+  const int64_t wgs = used * products *
                       (ceil_div(p.h_in, sgmv::kLoraGradCols) + ceil_div(p.h_out, sgmv::kLoraGradCols));
-  const int64_t bytes = (int64_t)p.num_loras * C * p.rank * 4 * products;
   const int64_t fill = ceil_div(768, std::max<int64_t>(1, wgs));
-  const int64_t steps = ceil_div(p.n_rows, 4 * sgmv::kDenseK);  // at least four steps each
   const int64_t longest = ceil_div(p.max_seg_len, 32 * sgmv::kDenseK);  // one long segment alone
+  const int64_t steps = ceil_div(p.n_rows, 4 * sgmv::kDenseK);          // at least four steps each
   // The planes are written and read once each: no more of them than Z has bytes.
-  const int64_t cheap = p.n_rows / std::max<int64_t>(1, 4 * (int64_t)p.num_loras * p.rank);
+  const int64_t cheap = p.n_rows / std::max<int64_t>(1, 4 * used * p.rank);
+  const int64_t bytes = (int64_t)p.num_loras * C * p.rank * 4 * products;
   const int64_t n = std::min<int64_t>({std::max(fill, longest), steps, cheap, kGradPlaneBytes / std::max<int64_t>(1, bytes), 64});
   return (int)std::max<int64_t>(1, n);
 }

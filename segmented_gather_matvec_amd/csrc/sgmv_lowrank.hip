@@ -235,8 +235,9 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
       __syncthreads();  // the list and the slots are read before the next pass or window overwrites them
     }
   }
-  // A LoRA without rows keeps what it has when gradients accumulate.
-  if (p.accumulate && !any) return;
+  // A LoRA without rows: zeros, written by split 0, or what it has when gradients accumulate.
+  if (!any && (p.accumulate || z > 0)) return;
+  const bool planes = p.nsplit > 1 && any;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -250,7 +251,7 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
       }
       if (c >= p.C || r >= rk) continue;
       if constexpr (F16T) v *= unit;
-      if (p.nsplit > 1) {
+      if (planes) {
         float* dst = p.planes + ((int64_t)z * p.meta.num_loras + k) * p.C * R +
                      (RANK_MAJOR ? (int64_t)r * p.C + c : (int64_t)c * R + r);
         *reinterpret_cast<f32x4*>(dst) = v;
@@ -294,15 +295,14 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBa
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out[k]);
   const int rk = rank_of(p.ranks, R, k);
   if (out == nullptr || rk <= 0) return;
-  if (p.accumulate) {  // a LoRA without rows keeps what it has
-    bool any = false;
-    for (int s0 = 0; s0 < p.meta.num_segs && !any; s0 += kThreads) {
-      const int s = s0 + (int)threadIdx.x;
-      const bool hit = s < p.meta.num_segs && p.meta.lora_idx[s] == k && p.meta.seg_indptr[s + 1] > p.meta.seg_indptr[s];
-      any = __syncthreads_or(hit);
-    }
-    if (!any) return;
+  bool any = false;  // a LoRA without rows has no planes
+  for (int s0 = 0; s0 < p.meta.num_segs && !any; s0 += kThreads) {
+    const int s = s0 + (int)threadIdx.x, sc = s < p.meta.num_segs ? s : p.meta.num_segs - 1;
+    const int lo = p.meta.seg_indptr[sc], end = p.meta.seg_indptr[sc + 1];
+    const int hi = end < p.meta.n_rows ? end : p.meta.n_rows;
+    any = __syncthreads_or(s < p.meta.num_segs && p.meta.lora_idx[sc] == k && lo >= 0 && hi > lo);
   }
+  if (!any) return;
   const int64_t n = (int64_t)p.C * rk;
   const int64_t o = ((int64_t)(blockIdx.x - k * blocks) * kThreads + threadIdx.x) * 4;  // of the stored gradient
   if (o >= n) return;
