@@ -63,7 +63,7 @@ __device__ inline void issue_e(const uint16_t* E, int rk, int R, int k0, int N, 
       const int r = R <= 16 ? k & (R - 1) : k0 + k;
       off = r < rk && (R > 16 || k < 2 * R) ? (uint32_t)(r * N + ((lane % G) ^ swizzle_k<C>(k)) * 8) * 2u : kOutOfRange;
     } else {
-      const int k = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;
+      const int k = ((lane & 3) ^ swizzle_r(lane >> 2)) * 8;
       const int r = R <= 16 ? k & (R - 1) : k0 + k;
       off = r < rk && (R > 16 || k < 2 * R) ? (uint32_t)((L * 16 + (lane >> 2)) * rk + r) * 2u : kOutOfRange;
     }

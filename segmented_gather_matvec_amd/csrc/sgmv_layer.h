@@ -106,10 +106,11 @@ struct LoraGradParams {
   float* planes;          // [nsplit][num_loras][C][rank] or [nsplit][num_loras][rank][C] (nsplit > 1)
   int32_t C, rank, rank_major;  // rank_major: stored [r_k, C]
   int32_t nsplit;
+  int32_t by_segment;     // 1 (fewer segments than LoRAs): a workgroup per segment that is its LoRA's first
   int32_t accumulate;
   SegMeta meta;
 };
-// count gradients (at most 4) in one launch; the plane sum follows when an nsplit > 1.
+// count gradients (at most 4) in one launch; the plane sums and the zeros of unused LoRAs follow where there are any.
 hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipStream_t stream);
 
 // dG = dH * U * act'(G), dU = dH * act(G) (n values each), rounded once to the 16-bit format, or (halves) as hi

@@ -264,6 +264,7 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
       e.rank = c.p.rank;
       e.rank_major = b;
       e.nsplit = nsplit;
+      e.by_segment = c.meta.num_segs < c.meta.num_loras;
       e.accumulate = accumulate;
       e.meta = c.meta;
     }

@@ -95,13 +95,15 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
   constexpr int LZ = COLS / 16 / kWaves, LQ = QC / 16 < kWaves ? 1 : QC / 16 / kWaves;
   constexpr int kPerStep = LZ + LQ + (F16T ? 1 : 0);
   const int ctiles = (p.C + COLS - 1) / COLS;
-  const int k = (int)blockIdx.x / ctiles;
-  if (k >= p.meta.num_loras || (int)blockIdx.z >= p.nsplit) return;
+  const int item = (int)blockIdx.x / ctiles;
+  if (item >= (p.by_segment ? p.meta.num_segs : p.meta.num_loras) || (int)blockIdx.z >= p.nsplit) return;
+  const int k = p.by_segment ? p.meta.lora_idx[item] : item;
+  if (k < 0 || k >= p.meta.num_loras) return;
   const int t = threadIdx.x;
   const int lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int q = lane >> 4, ml = lane & 15;
-  const int c0 = ((int)blockIdx.x - k * ctiles) * COLS;
+  const int c0 = ((int)blockIdx.x - item * ctiles) * COLS;
   const int z = (int)blockIdx.z;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out[k]);
   const int rk = rank_of(p.ranks, R, k);
@@ -127,9 +129,11 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
     const int id = p.meta.lora_idx[sc], lo = p.meta.seg_indptr[sc];
     int hi = p.meta.seg_indptr[sc + 1];
     hi = hi < p.meta.n_rows ? hi : p.meta.n_rows;
-    const bool hit = s < p.meta.num_segs && id == k && lo >= 0 && hi > lo;
+    const bool same = s < p.meta.num_segs && id == k;
+    const bool hit = same && lo >= 0 && hi > lo;
     const unsigned long long m = __ballot(hit);
-    __syncthreads();
+    // By segment: another workgroup has the LoRA if an earlier segment is its.
+    if (__syncthreads_or(p.by_segment && same && s < item)) return;
     if (lane == 0) lds_count[wave] = __popcll(m);
     __syncthreads();
     int at = __popcll(m & ((1ull << lane) - 1)), count = 0;
@@ -284,43 +288,54 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch 
     lora_grad_body<T, R, false>(p, lds, lds_lo, lds_hi, lds_count);
 }
 
-// Sums the splits' planes of one LoRA's gradient (split order), four values per thread.
+// Sums the splits' planes of one LoRA's gradient (split order), and writes the zeros of LoRAs that no
+// workgroup has seen: kSumTurns times four values per thread (one turn took 45 us instead of 25 for 57 LoRAs'
+// zeros: the search for the LoRA's segments outweighed them).
+constexpr int kSumTurns = 8;
+__host__ __device__ constexpr int64_t sum_blocks(int64_t C, int64_t rank) {  // of one LoRA
+  return (C * rank / 4 + kThreads * kSumTurns - 1) / (kThreads * kSumTurns);
+}
 template <class T>
 __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBatch batch) {
   const LoraGradParams& p = batch.p[blockIdx.y];
-  const int64_t blocks = ((int64_t)p.C * p.rank / 4 + kThreads - 1) / kThreads;  // of one LoRA
+  const int64_t blocks = sum_blocks(p.C, p.rank);
   const int k = (int)(blockIdx.x / blocks);
-  if (k >= p.meta.num_loras || p.nsplit <= 1) return;
+  if (k >= p.meta.num_loras) return;
   const int R = p.rank;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out[k]);
   const int rk = rank_of(p.ranks, R, k);
   if (out == nullptr || rk <= 0) return;
-  bool any = false;  // a LoRA without rows has no planes
-  for (int s0 = 0; s0 < p.meta.num_segs && !any; s0 += kThreads) {
+  // A LoRA without rows has no planes; by segment, one without a segment has not been seen at all.
+  bool rows = false, seen = false;
+  for (int s0 = 0; s0 < p.meta.num_segs && !rows; s0 += kThreads) {
     const int s = s0 + (int)threadIdx.x, sc = s < p.meta.num_segs ? s : p.meta.num_segs - 1;
     const int lo = p.meta.seg_indptr[sc], end = p.meta.seg_indptr[sc + 1];
     const int hi = end < p.meta.n_rows ? end : p.meta.n_rows;
-    any = __syncthreads_or(s < p.meta.num_segs && p.meta.lora_idx[sc] == k && lo >= 0 && hi > lo);
+    const bool same = s < p.meta.num_segs && p.meta.lora_idx[sc] == k;
+    rows = __syncthreads_or(same && lo >= 0 && hi > lo);
+    seen = __syncthreads_or(same) || seen;
   }
-  if (!any) return;
+  const bool zeros = !seen && p.by_segment && !p.accumulate;
+  if (!zeros && (!rows || p.nsplit <= 1)) return;
   const int64_t n = (int64_t)p.C * rk;
-  const int64_t o = ((int64_t)(blockIdx.x - k * blocks) * kThreads + threadIdx.x) * 4;  // of the stored gradient
-  if (o >= n) return;
-  // Planes hold [C][rank] or [rank][C]; the stored [C, r_k] has its own row length.
-  const int64_t src = p.rank_major ? o : o / rk * R + o % rk;
   const int64_t stride = (int64_t)p.meta.num_loras * p.C * R;
-  const float* pl = p.planes + (int64_t)k * p.C * R + src;
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  for (int g = 0; g < p.nsplit; ++g) v += *reinterpret_cast<const f32x4*>(pl + g * stride);
-  if (p.accumulate) {
-    const u32x2 old = *reinterpret_cast<const u32x2*>(out + o);
-    v[0] += T::lo(old[0]);
-    v[1] += T::hi(old[0]);
-    v[2] += T::lo(old[1]);
-    v[3] += T::hi(old[1]);
+  for (int turn = 0; turn < kSumTurns; ++turn) {
+    const int64_t o = (((blockIdx.x - k * blocks) * kSumTurns + turn) * kThreads + threadIdx.x) * 4;
+    if (o >= n) return;  // o: of the stored gradient
+    // Planes hold [C][rank] or [rank][C]; the stored [C, r_k] has its own row length.
+    const float* pl = p.planes + (int64_t)k * p.C * R + (p.rank_major || rk == R ? o : o / rk * R + o % rk);
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < (zeros ? 0 : p.nsplit); ++g) v += *reinterpret_cast<const f32x4*>(pl + g * stride);
+    if (p.accumulate) {
+      const u32x2 old = *reinterpret_cast<const u32x2*>(out + o);
+      v[0] += T::lo(old[0]);
+      v[1] += T::hi(old[0]);
+      v[2] += T::lo(old[1]);
+      v[3] += T::hi(old[1]);
+    }
+    *reinterpret_cast<u32x2*>(out + o) = u32x2{(uint32_t)T::round(v[0]) | ((uint32_t)T::round(v[1]) << 16),
+                                               (uint32_t)T::round(v[2]) | ((uint32_t)T::round(v[3]) << 16)};
   }
-  *reinterpret_cast<u32x2*>(out + o) = u32x2{(uint32_t)T::round(v[0]) | ((uint32_t)T::round(v[1]) << 16),
-                                             (uint32_t)T::round(v[2]) | ((uint32_t)T::round(v[3]) << 16)};
 }
 
 // ---------------------------------------------------------------- gated block, elementwise backward
@@ -395,13 +410,16 @@ hipError_t launch_lora_grad_t(const LoraGradParams* p, int count, hipStream_t s)
   for (int i = 0; i < count; ++i) {
     batch.p[i] = p[i];
     const int64_t loras = p[i].meta.num_loras;
-    tiles = std::max(tiles, (p[i].C + kLoraGradCols - 1) / kLoraGradCols * loras);
-    if (p[i].nsplit > 1) blocks = std::max(blocks, ((int64_t)p[i].C * p[i].rank / 4 + kThreads - 1) / kThreads * loras);
+    tiles = std::max(tiles, (p[i].C + kLoraGradCols - 1) / kLoraGradCols *
+                                (p[i].by_segment ? (int64_t)p[i].meta.num_segs : loras));
+    if (p[i].nsplit > 1 || (p[i].by_segment && !p[i].accumulate))
+      blocks = std::max(blocks, sum_blocks(p[i].C, p[i].rank) * loras);
     nsplit = std::max(nsplit, p[i].nsplit);
   }
   if (tiles > 0x7fffffff || blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid((unsigned)tiles, (unsigned)count, (unsigned)nsplit);
-  switch (p[0].rank) {
+  switch (tiles > 0 ? p[0].rank : -1) {
+    case -1: break;  // no segments
     case 8: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 8>), grid, dim3(kThreads), 0, s, batch); break;
     case 16: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 16>), grid, dim3(kThreads), 0, s, batch); break;
     case 32: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 32>), grid, dim3(kThreads), 0, s, batch); break;

@@ -2,7 +2,7 @@
 // straight from memory into LDS, and the reads of matrix operands from there.
 //
 // An operand whose contraction index is contiguous in memory is kept row by
-// row, its 16-byte groups at group ^ (row / 4 % 4), and read with 128-bit reads.  An operand
+// row, its 16-byte groups at group ^ swizzle_r(row), and read with 128-bit reads.  An operand
 // stored the other way round is kept as it lies and read with the
 // transposing 64-bit read; the four rows that one 16-lane group reads fall
 // into different banks, because group g of row k is stored at g ^ f(k).
@@ -25,6 +25,11 @@ template <int COLS>
 __device__ inline int swizzle_k(int k) {
   return (((k & 3) | ((k >> 1) & 4)) << 1) & (COLS / 8 - 1);
 }
+
+// Group swizzle of a tile stored [row][32].  A 128-bit read serves lanes 0-3, 12-15 and 20-27 together (and so on, in
+// turns of eight): four rows of one residue mod 4, at groups q and q ^ 1.  (row / 4) % 4 itself leaves two of
+// them in the same banks, and half of all LDS cycles were conflicts.
+__device__ inline int swizzle_r(int row) { return (-(row >> 2)) & 3; }
 
 // One operand tile of R rows (or columns) x 32 contraction steps.
 template <int R, int LOADS, bool T>
@@ -50,10 +55,10 @@ struct TileLoader {
         voff[j] = (uint32_t)(k * ld + g * 8) * 2u;
       } else {
         const int r = L * 16 + (lane >> 2);
-        voff[j] = (uint32_t)(r * ld + ((lane & 3) ^ ((lane >> 4) & 3)) * 8) * 2u;
+        voff[j] = (uint32_t)(r * ld + ((lane & 3) ^ swizzle_r(r)) * 8) * 2u;
       }
     }
-    g8 = ((lane & 3) ^ ((lane >> 4) & 3)) * 8;
+    g8 = ((lane & 3) ^ swizzle_r(lane >> 2)) * 8;
   }
   // Points at contraction index k0 of an operand with K of them; r0: first row
   // (column) of the tile, rows: how many the matrix has.
@@ -118,7 +123,7 @@ __device__ inline u32x4 read_operand(const uint16_t* lds, int tile, int lane) {
     const u32x2 l = read_transposed(a), h = read_transposed(a + 4 * R);  // k + 4 has the same swizzle
     return u32x4{l[0], l[1], h[0], h[1]};
   } else {
-    return load_vec(lds + (tile + i) * kDenseK + ((q ^ (i >> 2)) << 3));
+    return load_vec(lds + (tile + i) * kDenseK + ((q ^ swizzle_r(i)) << 3));
   }
 }
 

@@ -165,6 +165,7 @@ LARGE = {
     "split_deep": (23, "bf16", 520, 8200, 520, 32, 3, "uncovered", None, False),
     "distinct_wide": (24, "f16", 700, 264, 2056, 16, 40, "distinct", None, False),
     "one_long_segment": (25, "bf16", 3000, 136, 1032, 8, 1, "one", None, False),
+    "many_loras_few_segments": (26, "f16", 1500, 264, 520, 32, 60, "uncovered", (32, 8, 16), True),
 }
 
 
