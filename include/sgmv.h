@@ -491,7 +491,8 @@ sgmv_status_t sgmv_base_lora_apply_partial(const sgmv_problem_t* problem, const 
  * Precision: sums are fp32; every output is rounded once, from fp32 (H from
  * the unrounded G and U).  X @ A_k and dY @ B_k^T stay fp32.  The gated backward
  * rounds dG and dU to the 16-bit format once, since they are operands of the matrix
- * cores (up to 64 rows it carries them as two 16-bit halves each instead).  Results do not depend on timing: no atomics, sums in a fixed order.
+ * cores (up to 64 rows it carries them as two 16-bit halves each instead).  Results
+ * do not depend on timing: no atomics, sums in a fixed order.
  *
  * Gradients (sgmv_projection_grad_t): each of dX, dW, dA_ptrs, dB_ptrs may be
  * NULL (not wanted), and so may entries of the dA and dB tables and the whole
@@ -510,6 +511,9 @@ typedef enum sgmv_act {
   SGMV_ACT_SILU = 0,      /* g / (1 + e^-g) */
   SGMV_ACT_GELU_TANH = 1  /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
 } sgmv_act_t;
+
+/* Most rows a layer call takes; more give SGMV_ERR_UNSUPPORTED. */
+#define SGMV_MAX_LAYER_ROWS (1 << 30)
 
 /* Entry point a workspace is for. */
 typedef enum sgmv_layer_op {

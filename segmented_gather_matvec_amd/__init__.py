@@ -454,64 +454,79 @@ def new_layer_workspace(problem: sgmv_problem_t, op: int, device="cuda"):
     return torch.empty(sgmv_layer_workspace_bytes(problem, op), dtype=torch.uint8, device=device)
 
 
-def _need_shape(t, name, shape):
-    if t is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _need_len(t, name, least):
-    if t is not None and t.numel() < least:
+def _layer_ptr(t, name, index, dtype, shape=None, least=0):
+    """Address of a layer call's argument (None stays None) after the checks that keep the kernels in bounds:
+    a contiguous tensor on device `index` of the right type and shape, or of at least `least` entries."""
+    if t is None:
+        return None
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on X's device, is on {t.device}" if t.is_cuda else
+                         f"{name} must be a device tensor")
+    if t.dtype is not dtype or not t.is_contiguous():
+        _need(t, name, dtype)
+    if shape is not None:
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    elif t.numel() < least:
         raise ValueError(f"{name} must hold {least} entries, got {t.numel()}")
+    return t.data_ptr()
 
 
-def _layer_inputs(problem, X, weights, seg_indptr, lora_idx, ws, others=()):
-    """Checks what every layer call takes; ``others``: (tensor or None, name, width) in the problem's format."""
-    import torch
-    dt, n = _torch_dtype(problem), problem.n_rows
-    _need(X, "X", dt); _need_shape(X, "X", (n, problem.h_in))
-    for W, name in weights:
-        _need(W, name, dt); _need_shape(W, name, (problem.h_in, problem.h_out))
-    for t, name, width in others:
-        _need(t, name, dt); _need_shape(t, name, (n, width))
-    _need(seg_indptr, "seg_indptr", torch.int32); _need(lora_idx, "lora_idx", torch.int32)
-    _need_len(seg_indptr, "seg_indptr", problem.num_segs + 1); _need_len(lora_idx, "lora_idx", problem.num_segs)
-    _need(ws, "ws")
+class _LayerArgs:
+    """The arguments that every layer call takes, checked; methods for the others."""
 
+    def __init__(self, problem, X, weights, seg_indptr, lora_idx, ws):
+        import torch
+        self.problem = problem
+        self.dtype, self.i32, self.i64, self.f32 = _torch_dtype(problem), torch.int32, torch.int64, torch.float32
+        n, h_in, h_out = problem.n_rows, problem.h_in, problem.h_out
+        self.shapes = {"in": (n, h_in), "out": (n, h_out), "W": (h_in, h_out)}
+        _need(X, "X")
+        self.index = X.get_device() if X is not None else torch.cuda.current_device()
+        self.X = self.rows(X, "X", "in")
+        self.W = [self.rows(W, name, "W") for W, name in weights]
+        self.meta = (_layer_ptr(seg_indptr, "seg_indptr", self.index, self.i32, None, problem.num_segs + 1),
+                     _layer_ptr(lora_idx, "lora_idx", self.index, self.i32, None, problem.num_segs))
+        if ws is None:
+            self.ws = (None, 0)
+        else:
+            self.ws = (_layer_ptr(ws, "ws", self.index, ws.dtype), ws.numel() * ws.element_size())
 
-def _layer_projection(problem, pj, name):
-    import torch
-    A_ptrs, B_ptrs, Y, ranks, scales = (tuple(pj) + (None,) * 5)[:5]
-    _need(A_ptrs, f"{name} A_ptrs", torch.int64); _need(B_ptrs, f"{name} B_ptrs", torch.int64)
-    _need(Y, f"{name} Y", _torch_dtype(problem)); _need_shape(Y, f"{name} Y", (problem.n_rows, problem.h_out))
-    _need(ranks, f"{name} ranks", torch.int32); _need(scales, f"{name} scales", torch.float32)
-    for t, what in ((A_ptrs, "A_ptrs"), (B_ptrs, "B_ptrs"), (ranks, "ranks"), (scales, "scales")):
-        _need_len(t, f"{name} {what}", problem.num_loras)
-    return sgmv_projection_t(_ptr(A_ptrs), _ptr(B_ptrs), _ptr(Y), _ptr(ranks), _ptr(scales))
+    def rows(self, t, name, shape):
+        return _layer_ptr(t, name, self.index, self.dtype, self.shapes[shape])
 
+    def table(self, t, name, dtype):
+        return _layer_ptr(t, name, self.index, dtype, None, self.problem.num_loras)
 
-def _layer_grad(problem, grad, name):
-    import torch
-    dW, dA_ptrs, dB_ptrs = (tuple(grad) + (None,) * 3)[:3] if grad is not None else (None,) * 3
-    _need(dW, f"{name} dW", _torch_dtype(problem)); _need_shape(dW, f"{name} dW", (problem.h_in, problem.h_out))
-    _need(dA_ptrs, f"{name} dA_ptrs", torch.int64); _need(dB_ptrs, f"{name} dB_ptrs", torch.int64)
-    _need_len(dA_ptrs, f"{name} dA_ptrs", problem.num_loras); _need_len(dB_ptrs, f"{name} dB_ptrs", problem.num_loras)
-    return sgmv_projection_grad_t(_ptr(dW), _ptr(dA_ptrs), _ptr(dB_ptrs))
+    def projection(self, pj, name):
+        A_ptrs, B_ptrs, Y, ranks, scales = (tuple(pj) + (None,) * 5)[:5]
+        return sgmv_projection_t(self.table(A_ptrs, name + " A_ptrs", self.i64),
+                                 self.table(B_ptrs, name + " B_ptrs", self.i64), self.rows(Y, name + " Y", "out"),
+                                 self.table(ranks, name + " ranks", self.i32), self.table(scales, name + " scales", self.f32))
 
+    def grad(self, grad, name):
+        dW, dA_ptrs, dB_ptrs = (tuple(grad) + (None,) * 3)[:3] if grad is not None else (None,) * 3
+        return sgmv_projection_grad_t(self.rows(dW, name + " dW", "W"),
+                                      self.table(dA_ptrs, name + " dA_ptrs", self.i64),
+                                      self.table(dB_ptrs, name + " dB_ptrs", self.i64))
 
-def _ws_bytes(ws):
-    return ws.numel() * ws.element_size() if ws is not None else 0
+    def launch(self, call, stream, *args):
+        """The entry point with X's device current, on `stream` or that device's current stream."""
+        import torch
+        entry = getattr(load_library(), call)
+        if self.index == torch.cuda.current_device():
+            _check(entry(ctypes.byref(self.problem), self.X, *args, *self.meta, *self.ws, _stream(stream)), call)
+            return
+        with torch.cuda.device(self.index):
+            _check(entry(ctypes.byref(self.problem), self.X, *args, *self.meta, *self.ws, _stream(stream)), call)
 
 
 def sgmv_dense_lora_apply(problem, X, W, proj, seg_indptr, lora_idx, ws, stream=None):
     """Y[i] = X[i] @ W + s_k * (X[i] @ A_k) @ B_k for any number of rows (Y written, rounded once);
     asynchronous.  `proj` is (A_ptrs, B_ptrs, Y) or (A_ptrs, B_ptrs, Y, ranks, scales), as in
     sgmv_lora_apply_batched; `ws` from new_layer_workspace(problem, SGMV_DENSE_FORWARD)."""
-    _layer_inputs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws)
-    pj = _layer_projection(problem, proj, "proj")
-    st = load_library().sgmv_dense_lora_apply(ctypes.byref(problem), _ptr(X), _ptr(W), ctypes.byref(pj),
-                                              _ptr(seg_indptr), _ptr(lora_idx), _ptr(ws), _ws_bytes(ws),
-                                              _stream(stream))
-    _check(st, "sgmv_dense_lora_apply")
+    a = _LayerArgs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws)
+    a.launch("sgmv_dense_lora_apply", stream, *a.W, ctypes.byref(a.projection(proj, "proj")))
 
 
 def sgmv_gated_lora_apply(problem, X, Wg, Wu, gate, up, H, seg_indptr, lora_idx, ws, act=SGMV_ACT_SILU, stream=None):
@@ -519,12 +534,9 @@ def sgmv_gated_lora_apply(problem, X, Wg, Wu, gate, up, H, seg_indptr, lora_idx,
     asynchronous.  `gate` and `up` are projections as in sgmv_dense_lora_apply whose Y is where to
     store G and U (what sgmv_gated_lora_backward reads), or None; `ws` from
     new_layer_workspace(problem, SGMV_GATED_FORWARD)."""
-    _layer_inputs(problem, X, [(Wg, "Wg"), (Wu, "Wu")], seg_indptr, lora_idx, ws, [(H, "H", problem.h_out)])
-    g, u = _layer_projection(problem, gate, "gate"), _layer_projection(problem, up, "up")
-    st = load_library().sgmv_gated_lora_apply(ctypes.byref(problem), _ptr(X), _ptr(Wg), _ptr(Wu), ctypes.byref(g),
-                                              ctypes.byref(u), int(act), _ptr(H), _ptr(seg_indptr), _ptr(lora_idx),
-                                              _ptr(ws), _ws_bytes(ws), _stream(stream))
-    _check(st, "sgmv_gated_lora_apply")
+    a = _LayerArgs(problem, X, [(Wg, "Wg"), (Wu, "Wu")], seg_indptr, lora_idx, ws)
+    a.launch("sgmv_gated_lora_apply", stream, *a.W, ctypes.byref(a.projection(gate, "gate")),
+             ctypes.byref(a.projection(up, "up")), int(act), a.rows(H, "H", "out"))
 
 
 def sgmv_dense_lora_backward(problem, X, W, proj, dY, seg_indptr, lora_idx, ws, dX=None, grad=None, accumulate=False,
@@ -532,13 +544,9 @@ def sgmv_dense_lora_backward(problem, X, W, proj, dY, seg_indptr, lora_idx, ws, 
     """Gradients of sgmv_dense_lora_apply from dY: dX (written), and `grad` = (dW, dA_ptrs, dB_ptrs), each or
     None; accumulate adds dW, dA and dB to what is there, else they are written (zero for a LoRA without rows).
     `ws` from new_layer_workspace(problem, SGMV_DENSE_BACKWARD).  Asynchronous."""
-    _layer_inputs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws,
-                  [(dY, "dY", problem.h_out), (dX, "dX", problem.h_in)])
-    pj, g = _layer_projection(problem, proj, "proj"), _layer_grad(problem, grad, "grad")
-    st = load_library().sgmv_dense_lora_backward(ctypes.byref(problem), _ptr(X), _ptr(W), ctypes.byref(pj), _ptr(dY),
-                                                 _ptr(dX), ctypes.byref(g), int(accumulate), _ptr(seg_indptr),
-                                                 _ptr(lora_idx), _ptr(ws), _ws_bytes(ws), _stream(stream))
-    _check(st, "sgmv_dense_lora_backward")
+    a = _LayerArgs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws)
+    a.launch("sgmv_dense_lora_backward", stream, *a.W, ctypes.byref(a.projection(proj, "proj")),
+             a.rows(dY, "dY", "out"), a.rows(dX, "dX", "in"), ctypes.byref(a.grad(grad, "grad")), int(accumulate))
 
 
 def sgmv_gated_lora_backward(problem, X, Wg, Wu, gate, up, dH, seg_indptr, lora_idx, ws, dX=None, gate_grad=None,
@@ -546,15 +554,10 @@ def sgmv_gated_lora_backward(problem, X, Wg, Wu, gate, up, dH, seg_indptr, lora_
     """Gradients of sgmv_gated_lora_apply from dH and the stored G and U (the Y of `gate` and `up`): dX (written),
     and per projection (dW, dA_ptrs, dB_ptrs), each or None, accumulated or written as in
     sgmv_dense_lora_backward.  `ws` from new_layer_workspace(problem, SGMV_GATED_BACKWARD).  Asynchronous."""
-    _layer_inputs(problem, X, [(Wg, "Wg"), (Wu, "Wu")], seg_indptr, lora_idx, ws,
-                  [(dH, "dH", problem.h_out), (dX, "dX", problem.h_in)])
-    g, u = _layer_projection(problem, gate, "gate"), _layer_projection(problem, up, "up")
-    gg, ug = _layer_grad(problem, gate_grad, "gate_grad"), _layer_grad(problem, up_grad, "up_grad")
-    st = load_library().sgmv_gated_lora_backward(ctypes.byref(problem), _ptr(X), _ptr(Wg), _ptr(Wu), ctypes.byref(g),
-                                                 ctypes.byref(u), int(act), _ptr(dH), _ptr(dX), ctypes.byref(gg),
-                                                 ctypes.byref(ug), int(accumulate), _ptr(seg_indptr), _ptr(lora_idx),
-                                                 _ptr(ws), _ws_bytes(ws), _stream(stream))
-    _check(st, "sgmv_gated_lora_backward")
+    a = _LayerArgs(problem, X, [(Wg, "Wg"), (Wu, "Wu")], seg_indptr, lora_idx, ws)
+    a.launch("sgmv_gated_lora_backward", stream, *a.W, ctypes.byref(a.projection(gate, "gate")),
+             ctypes.byref(a.projection(up, "up")), int(act), a.rows(dH, "dH", "out"), a.rows(dX, "dX", "in"),
+             ctypes.byref(a.grad(gate_grad, "gate_grad")), ctypes.byref(a.grad(up_grad, "up_grad")), int(accumulate))
 
 
 def batched_workspace_bytes(problem: sgmv_problem_t, num_projections: int) -> int:

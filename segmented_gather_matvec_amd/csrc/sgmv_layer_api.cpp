@@ -288,7 +288,7 @@ extern "C" {
 sgmv_status_t sgmv_dense_lora_apply(const sgmv_problem_t* p, const void* X, const void* W,
                                     const sgmv_projection_t* proj, const int32_t* seg_indptr,
                                     const int32_t* lora_idx, void* ws, size_t ws_bytes, void* stream) {
-  sgmv_status_t st = sgmv_check_problem(p);
+  sgmv_status_t st = check_layer(p);
   if (st != SGMV_OK) return st;
   if (p->n_rows == 0) return SGMV_OK;
   if (!proj || !proj->Y) return SGMV_ERR_INVALID_ARG;
@@ -305,7 +305,7 @@ sgmv_status_t sgmv_gated_lora_apply(const sgmv_problem_t* p, const void* X, cons
                                     const sgmv_projection_t* gate, const sgmv_projection_t* up, int32_t act, void* H,
                                     const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
                                     void* stream) {
-  sgmv_status_t st = sgmv_check_problem(p);
+  sgmv_status_t st = check_layer(p);
   if (st != SGMV_OK) return st;
   if (act != SGMV_ACT_SILU && act != SGMV_ACT_GELU_TANH) return SGMV_ERR_INVALID_ARG;
   if (p->n_rows == 0) return SGMV_OK;
@@ -327,7 +327,7 @@ sgmv_status_t sgmv_dense_lora_backward(const sgmv_problem_t* p, const void* X, c
                                        const sgmv_projection_grad_t* grad, int32_t accumulate,
                                        const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
                                        void* stream) {
-  sgmv_status_t st = sgmv_check_problem(p);
+  sgmv_status_t st = check_layer(p);
   if (st != SGMV_OK) return st;
   if (accumulate != 0 && accumulate != 1) return SGMV_ERR_INVALID_ARG;
   const sgmv_projection_grad_t none{};
@@ -353,7 +353,7 @@ sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* p, const void* X, c
                                        const sgmv_projection_grad_t* up_grad, int32_t accumulate,
                                        const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
                                        void* stream) {
-  sgmv_status_t st = sgmv_check_problem(p);
+  sgmv_status_t st = check_layer(p);
   if (st != SGMV_OK) return st;
   if (act != SGMV_ACT_SILU && act != SGMV_ACT_GELU_TANH) return SGMV_ERR_INVALID_ARG;
   if (accumulate != 0 && accumulate != 1) return SGMV_ERR_INVALID_ARG;

@@ -110,6 +110,11 @@ int plan_grad_split(const sgmv_problem_t& p, int64_t C, int products) {
 
 }  // namespace
 
+sgmv_status_t check_layer(const sgmv_problem_t* p) {
+  const sgmv_status_t st = sgmv_check_problem(p);
+  return st == SGMV_OK && p->n_rows > SGMV_MAX_LAYER_ROWS ? SGMV_ERR_UNSUPPORTED : st;
+}
+
 LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   LayerPlan l;
   l.projections = layer_gated(op) ? 2 : 1;
@@ -175,7 +180,7 @@ using namespace sgmv_host;
 extern "C" {
 
 sgmv_status_t sgmv_layer_workspace_bytes(const sgmv_problem_t* p, int32_t op, size_t* bytes) {
-  const sgmv_status_t st = sgmv_check_problem(p);
+  const sgmv_status_t st = check_layer(p);
   if (st != SGMV_OK) return st;
   if (!bytes || op < SGMV_DENSE_FORWARD || op > SGMV_GATED_BACKWARD) return SGMV_ERR_INVALID_ARG;
   *bytes = plan_layer(*p, op).total;

@@ -44,6 +44,8 @@ struct LayerPlan {
 
 inline bool layer_gated(int op) { return op == SGMV_GATED_FORWARD || op == SGMV_GATED_BACKWARD; }
 inline bool layer_backward(int op) { return op == SGMV_DENSE_BACKWARD || op == SGMV_GATED_BACKWARD; }
+// sgmv_check_problem, and the rows that the tiles' 32-bit row numbers reach.
+sgmv_status_t check_layer(const sgmv_problem_t* p);
 LayerPlan plan_layer(const sgmv_problem_t& p, int op);
 
 }  // namespace sgmv_host

@@ -70,8 +70,8 @@ __global__ __launch_bounds__(kThreads) void sgmv_thin_sum_kernel(ThinBatch batch
 // own.  The contraction index is the row, so both operands (Z, and V16's rows
 // [hi | lo]) are kept as they lie and read with the transposing read; they
 // stream through a ring of LDS slots (sgmv_tile.h).  Bound by reading Z.
-// fp16 rows of V16 may be kept scaled down by a power of two each: then the sums run
-// in units of the largest scale so far.
+// fp16 rows of V16 are kept divided by a power of two each (store_v): the sums run
+// in units of the largest so far, and rows kept in smaller units are brought to it.
 // Up to four gradients in one launch (grid y).
 struct LoraGradBatch {
   LoraGradParams p[4];
@@ -118,7 +118,7 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float unit = 1.f;  // of the sums (fp16 only)
+  float unit = 0.f;  // of the sums (fp16 only): the largest row scale so far
   bool any = false;  // LoRA k has rows
   int counter = 0;   // steps of 32 rows so far, over all of its segments
 
@@ -202,18 +202,27 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
             // Rows 8 q .. 8 q + 7 are this lane's contraction steps.
             const float* sp = reinterpret_cast<const float*>(now + S0) + q * 8;
             const f32x4 u0 = *reinterpret_cast<const f32x4*>(sp), u1 = *reinterpret_cast<const f32x4*>(sp + 4);
-            float big = fmaxf(fmaxf(fmaxf(u0[0], u0[1]), fmaxf(u0[2], u0[3])), fmaxf(fmaxf(u1[0], u1[1]), fmaxf(u1[2], u1[3])));
-            big = fmaxf(big, shfl_xor(big, 16));
-            big = fmaxf(big, shfl_xor(big, 32));
-            if (big > 1.f || unit > 1.f) {  // uniform over the wave
-              if (big > unit) {
-                const float f = unit / big;
+            float big = 0.f, small = 3e38f;  // of the step's rows; rows past the segment have scale 0
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int x8 = 0; x8 < 8; ++x8) {
+              const float u = x8 < 4 ? u0[x8 & 3] : u1[x8 & 3];
+              big = fmaxf(big, u);
+              small = fminf(small, u > 0.f ? u : 3e38f);
+            }
 #pragma unroll
-                  for (int j = 0; j < JT; ++j) acc[i][j] *= f;
-                unit = big;
-              }
+            for (int d = 16; d < 64; d <<= 1) {
+              big = fmaxf(big, shfl_xor(big, d));
+              small = fminf(small, shfl_xor(small, d));
+            }
+            if (big > unit) {  // uniform over the wave, as all of this
+              const float f = unit / big;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < JT; ++j) acc[i][j] *= f;
+              unit = big;
+            }
+            if (small < unit) {
               float f[8];
 #pragma unroll
               for (int x8 = 0; x8 < 8; ++x8) f[x8] = (x8 < 4 ? u0[x8 & 3] : u1[x8 & 3]) / unit;
@@ -222,7 +231,7 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
                 float v[8];
                 unpack8<T>(qf[j], v);
 #pragma unroll
-                for (int x8 = 0; x8 < 8; ++x8) v[x8] = f[x8] > 0.f ? v[x8] * f[x8] : v[x8];
+                for (int x8 = 0; x8 < 8; ++x8) v[x8] *= f[x8];
                 qf[j] = pack8<T>(v);
               }
             }

@@ -16,20 +16,24 @@ __device__ inline void store_v(const ThinParams& p, int row, int c, float (&v)[8
     *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
   }
   if (p.V16 == nullptr) return;
-  // fp16 halves hold V only below 65504: a row with a value beyond 32768 is kept
-  // scaled down by a power of two (exact), which the reader puts back.
+  // fp16 halves hold V well only within some binades (above 65504 they overflow, far below 1 the lo
+  // half and then the hi half run out of denormals): the row is kept divided by the power 2^(16 b) that
+  // brings its largest value to [2^-4, 2^12) (exact), and the reader puts it back.  Steps of 2^16
+  // around 1, so that most rows share one.
   if constexpr (T::kMaxFinite < 1e6f) {
-    float big = 0.f, up = 1.f;
+    float big = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(v[e]));
-    for (int d = 1; d < p.rank / 8; d <<= 1) big = fmaxf(big, shfl_xor(big, d));
-    if (big > 32768.f && big < 3.4e38f) {
-      const int e = ((int)(__float_as_uint(big) >> 23) & 255) - 127 - 14;  // 1 .. 113
-      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-      up = __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) v[x] *= down;
+    for (int e = 0; e < 8; ++e) {
+      const float a = fabsf(v[e]);
+      big = fmaxf(big, a < 3.4e38f ? a : 0.f);  // not of infinities and NaN
     }
+    for (int d = 1; d < p.rank / 8; d <<= 1) big = fmaxf(big, shfl_xor(big, d));
+    int b = (((int)(__float_as_uint(big) >> 23) & 255) - 127 + 4) >> 4;
+    b = b < -7 ? -7 : b > 7 ? 7 : b;
+    const float up = __uint_as_float((uint32_t)(127 + 16 * b) << 23);
+    const float down = __uint_as_float((uint32_t)(127 - 16 * b) << 23);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= down;
     if (c == 0) p.row_scale[row] = up;
   }
   u32x4 hi, lo;

@@ -7,7 +7,9 @@ Bounds, per element, with h = eps / 2 of the 16-bit format (half a step: 2^-8 bf
 * a sum of K products in fp32, in any order: (K + 8) 2^-23 sum |terms| (one unit in the last
   place per addition covers matrix cores that truncate);
 * V = s x@A and dV = s dy@B^T enter matrix products as hi + lo halves: h^2 of each value, plus, in
-  fp16, half of the smallest denormal (2^-25) where lo underflows (relative to a row or tile scaled by 2^-e: below h^2 there);
+  fp16, half of the smallest denormal (2^-25) where lo underflows, in units of the power 2^(16 b) that brings the row's largest
+  value to [2^-4, 2^12).  The gradients of A_k and B_k sum rows in the LoRA's largest unit: bringing hi and lo there
+  rounds each by another 2^-25 at most, 3 * 2^-25 < 2^-23 in all;
 * dG, dU of the gated backward are rounded once: h of each; up to 64 rows they are two halves: h^2;
 * the activation in fp32: 2^-20 of the terms it is made of (exp and the divisions are good to a few
   units in the last place each).
@@ -84,8 +86,14 @@ def scale_of(p, k):
     return float(p["scales"][k]) if p["scales"] is not None else 1.0
 
 
-def lo_floor(dtype):
-    return 2.0 ** -25 if dtype == torch.float16 else 0.0
+def lo_floor(dtype, v, ev):
+    """Per row of V (known up to ev): 2^-25 in the row's unit."""
+    if dtype != torch.float16:
+        return v.new_zeros(v.shape[0], 1)
+    big = (v.abs() + ev).amax(1, keepdim=True) if v.shape[1] else v.new_zeros(v.shape[0], 1)
+    exponent = torch.frexp(big).exponent - 1        # big in [2^exponent, 2^(exponent + 1)); fp32's range
+    band = torch.div(exponent + 4, 16, rounding_mode="floor").clamp(-7, 7)
+    return 2.0 ** -25 * torch.where(big > 0, 2.0 ** (16.0 * band.to(v.dtype)), 2.0 ** -112)
 
 
 def project(c, p):
@@ -99,7 +107,8 @@ def project(c, p):
         x = X[lo:hi]
         v, va = s * (x @ A), s * (x.abs() @ A.abs())
         y[lo:hi] += v @ B
-        ev = (c.h_in + 8) * U * va + h * h * v.abs() + lo_floor(c.dtype)
+        ev = (c.h_in + 8) * U * va
+        ev = ev + h * h * v.abs() + lo_floor(c.dtype, v, ev)
         err[lo:hi] += ev @ B.abs() + (c.rank + c.h_in + 16) * U * (v.abs() @ B.abs())
     return y, err
 
@@ -128,13 +137,14 @@ def gate(c, kind):
 def backward(c, p, d, ed, train_w=True):
     """Gradients from the layer's output gradient d (64 bits) known up to ed, not rounded:
     dX, (dA_k), (dB_k), dW as (value, bound of the unrounded sum) pairs."""
-    h, fl = half_step(c.dtype), lo_floor(c.dtype)
+    h = half_step(c.dtype)
     X, W = c.X.double(), p["W"].double()
     dX = d @ W.t()
     eX = ed @ W.abs().t() + (2 * c.h_out + 8) * U * (d.abs() @ W.abs().t())
     dA = [torch.zeros_like(a, dtype=torch.float64) for a in p["A"]]
     dB = [torch.zeros_like(b, dtype=torch.float64) for b in p["B"]]
     eA, eB = [torch.zeros_like(a) for a in dA], [torch.zeros_like(b) for b in dB]
+    rows = [[] for _ in range(c.P)]
     for lo, hi, k in c.pieces:
         A, B, s = p["A"][k].double(), p["B"][k].double(), scale_of(p, k)
         x, dy, e = X[lo:hi], d[lo:hi], ed[lo:hi]
@@ -142,14 +152,22 @@ def backward(c, p, d, ed, train_w=True):
         ev = (c.h_in + 8) * U * s * (x.abs() @ A.abs())
         dv = s * (dy @ B.t())
         edv = s * (e @ B.abs().t()) + (c.h_out + 8) * U * s * (dy.abs() @ B.abs().t())
-        sv, sdv = ev + h * h * v.abs() + fl, edv + h * h * dv.abs() + fl
+        sv, sdv = ev + h * h * v.abs(), edv + h * h * dv.abs()
+        fv, fdv = lo_floor(c.dtype, v, ev), lo_floor(c.dtype, dv, edv)
+        # What the sums over rows multiply, and the row's unit floor (the LoRA's largest comes below).
+        rows[k].append((x.abs(), fdv, dy.abs(), fv))
         n = (2 * c.n + 16) * U  # sums over rows, LoRAs of several segments and splits among them
         dX[lo:hi] += dv @ A.t()
-        eX[lo:hi] += sdv @ A.abs().t() + (c.rank + 16) * U * (dv.abs() @ A.abs().t())
+        eX[lo:hi] += (sdv + fdv) @ A.abs().t() + (c.rank + 16) * U * (dv.abs() @ A.abs().t())
         dA[k] += x.t() @ dv
         eA[k] += x.abs().t() @ sdv + n * (x.abs().t() @ dv.abs())
         dB[k] += v.t() @ dy
         eB[k] += sv.t() @ dy.abs() + v.abs().t() @ e + n * (v.abs().t() @ dy.abs())
+    for k, parts in enumerate(rows):
+        if parts:
+            x, fdv, dy, fv = (torch.cat(t) for t in zip(*parts))
+            eA[k] += 4 * fdv.max() * x.sum(0)[:, None]
+            eB[k] += 4 * fv.max() * dy.sum(0)[None, :]
     dW = X.t() @ d if train_w else None
     eW = X.abs().t() @ ed + (c.n + 8) * U * (X.abs().t() @ d.abs()) if train_w else None
     return (dX, eX), list(zip(dA, eA)), list(zip(dB, eB)), (dW, eW)

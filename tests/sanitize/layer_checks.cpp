@@ -42,7 +42,7 @@ static void check_dense(const DensePlan& d, int64_t M, int64_t N, int64_t steps,
 static void check_problem(const sgmv_problem_t& p, int op) {
   size_t bytes = 0;
   if (sgmv_layer_workspace_bytes(&p, op, &bytes) != SGMV_OK) {
-    CHECK(sgmv_check_problem(&p) != SGMV_OK);
+    CHECK(sgmv_check_problem(&p) != SGMV_OK || p.n_rows > SGMV_MAX_LAYER_ROWS);
     return;
   }
   const LayerPlan l = plan_layer(p, op);

@@ -392,6 +392,28 @@ def test_fp16_intermediates_beyond_fp16():
         lr.check(grads[0][1][k], *ref[1][k], c.dtype, "dA")
 
 
+@pytest.mark.parametrize("n", [40, 200, 1100])
+def test_fp16_intermediates_below_fp16(n):
+    """V and dV far below 1, in steps from row to row: fp32 holds them, so outputs and gradients of ordinary size
+    must not lose them to fp16's denormals."""
+    c = lr.Layer(63, "f16", n, 264, 136, 16, 3, "mixed", 1, None, False)
+    p = c.proj[0]
+    step = torch.tensor([1.0, 2.0 ** -8, 2.0 ** -5, 2.0 ** -10], device="cuda").repeat(n)[:n, None]
+    c.X.mul_(step.half())
+    c.dY.mul_(step.flip(0).half())
+    for k in range(3):
+        p["A"][k].mul_(2.0 ** -7)           # V ~ 2^-7 .. 2^-17
+        p["B"][k].mul_(2.0 ** (4 - 3 * k))
+    p["W"].mul_(2.0 ** -12)                 # the LoRA term is what is left to see
+    p["scales"] = torch.tensor([2.0 ** 7, 2.0 ** -9, 1.0], device="cuda")
+    lr.check(run_dense(c, "f16"), *lr.project(c, p), c.dtype, "Y")
+    dX, grads = run_dense_back(c, "f16")
+    d = c.dY.double()
+    ref = lr.backward(c, p, d, torch.zeros_like(d))
+    lr.check(dX, *ref[0], c.dtype, "dX")
+    check_grads(c, grads, [ref])
+
+
 def test_gate_far_out():
     """Gates at the ends of the format: silu and its slope go to 0 and to the identity without NaN."""
     c = lr.Layer(71, "bf16", 16, 64, 64, 8, 1, "none", 2, None, False)

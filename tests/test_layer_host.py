@@ -122,6 +122,18 @@ def test_bad_problems(op, kw):
         sg.sgmv_layer_workspace_bytes(p, op)
 
 
+@pytest.mark.parametrize("op", OPS)
+def test_rows_beyond_the_tiles_reach(op):
+    most = int(re.search(r"#define SGMV_MAX_LAYER_ROWS \(1 << (\d+)\)", open(HEADER).read()).group(1))
+    kw = dict(h_in=8, h_out=8, num_segs=0, max_seg_len=0)
+    assert sg.sgmv_layer_workspace_bytes(good(n_rows=1 << most, **kw), op) >= 0
+    p = good(n_rows=(1 << most) + 1, **kw)
+    assert sg.sgmv_check_problem(p) == sg.SGMV_OK
+    assert Raw(p).call(op) == sg.SGMV_ERR_UNSUPPORTED
+    with pytest.raises(sg.SgmvError):
+        sg.sgmv_layer_workspace_bytes(p, op)
+
+
 def test_workspace_arguments():
     lib = sg.load_library()
     out = ctypes.c_size_t(0)
@@ -154,5 +166,26 @@ def test_binding_checks_shapes_and_devices():
     X, W, Y = torch.zeros(40, 128).half(), torch.zeros(128, 256).half(), torch.zeros(40, 256).half()
     with pytest.raises(ValueError, match="device tensor"):
         sg.sgmv_dense_lora_apply(p, X, W, (None, None, Y), None, None, None)
-    with pytest.raises(ValueError, match=r"must be \[40, 128\]"):
-        sg._need_shape(torch.zeros(40, 120), "X", (40, 128))
+    for t, kw, why in ((torch.zeros(40, 120), dict(shape=(40, 128)), r"must be \[40, 128\], got \[40, 120\]"),
+                       (torch.zeros(3), dict(least=4), "must hold 4 entries, got 3"),
+                       (torch.zeros(3).half(), dict(least=3), "must be torch.float32"),
+                       (torch.zeros(4, 4).t()[:, :2], dict(shape=(4, 2)), "must be contiguous")):
+        class OnDevice(torch.Tensor):
+            is_cuda = True
+            get_device = lambda self: 0  # noqa: E731
+        with pytest.raises(ValueError, match="T " + why):
+            sg._layer_ptr(t.as_subclass(OnDevice), "T", 0, torch.float32, **kw)
+
+
+def test_binding_refuses_tensors_of_two_devices():
+    class On:
+        is_cuda = True
+
+        def __init__(self, index):
+            self.index, self.device = index, torch.device("cuda", index)
+
+        def get_device(self):
+            return self.index
+
+    with pytest.raises(ValueError, match="W must be on X's device, is on cuda:0"):
+        sg._layer_ptr(On(0), "W", 1, torch.float16)
