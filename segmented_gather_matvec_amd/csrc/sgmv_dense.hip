@@ -35,13 +35,13 @@ struct DenseShape {
   static constexpr bool B_T = MODE != kDenseDx;
   static constexpr int NB = GATED ? 2 : 1;            // column sub-tiles (gate, up)
   static constexpr int C = BN / NB;                   // columns of one sub-tile
-  // 1 KiB loads per wave and step.  (A 32-row tile is two of them: two waves
-  // load each, the same bytes twice, so that every wave counts alike.)
-  static constexpr int LA = BM / 16 < NW ? 1 : BM / 16 / NW;
+  // 1 KiB loads per wave and step.  (A 32-row tile is two of them and a 192-row tile twelve: some
+  // are loaded twice, the same bytes, so that every wave counts alike.)
+  static constexpr int LA = (BM / 16 + NW - 1) / NW;
   static constexpr int LB = BN / 16 / NW;
   static constexpr int TNP = TN / NB;                 // 16-column tiles of one projection per wave
   static constexpr int SLOT = (BM + BN) * kDenseK;    // halves of one ring slot
-  static_assert((LA * 16 * NW) % BM == 0 && LB * 16 * NW == BN, "tile loads split evenly over the waves");
+  static_assert(LA * 16 * NW >= BM && LB * 16 * NW == BN, "tile loads split evenly over the waves");
   static_assert(TM * 16 * WM == BM && TNP * NB * 16 * WN == BN, "tile splits evenly over the waves");
 };
 
@@ -664,6 +664,7 @@ template <class T, int MODE>
 hipError_t launch_mode(int cfg, const DenseParams& p, hipStream_t s) {
   switch (cfg) {
     case kTile256: return launch_tile<T, MODE, 256, 256, 2, 4, 4, 2>(p, s);
+    case kTile192: return launch_tile<T, MODE, 192, 256, 2, 4, 4, 2>(p, s);
     case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 4, 2>(p, s);
     case kTile64: return launch_tile<T, MODE, 64, 256, 1, 4, 4, 2>(p, s);
     case kTile32: return launch_tile<T, MODE, 32, 256, 1, 4, 4, 2>(p, s);

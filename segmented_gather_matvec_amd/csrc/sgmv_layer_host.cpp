@@ -17,14 +17,22 @@ constexpr int kHalvesRows = 64;
 constexpr int kShortRun = 16;  // rows per segment from which the tiles' matrix cores add the LoRA term
 
 // Workgroups of a tile shape that run at once on one CU (LDS).
-int resident(int cfg) { return cfg == sgmv::kTile256 ? 1 : 2; }
+int resident(int cfg) { return cfg <= sgmv::kTile192 ? 1 : 2; }
 
 // The model that picks between tile shapes and splits; only ratios matter.
 // Large tiles are bound by the matrix cores: microseconds of one contraction
-// step of one workgroup alone on its CU (measured: 8192 x 4096 -> 11008 in 6 rounds of 128 steps 616 us; 512 x 4096
-// -> 4096 in 128 x 128 tiles, two splits, one workgroup a CU, 24 us, and 26 us with four splits, two a CU).
+// step of one workgroup on its CU.  Measured, bf16, r = 16: 8192 x 4096 -> 11008 in 6 rounds of 128 steps of 256 x 256
+// tiles 616 us; 2011 x 5120 -> 5120 in one round of 160 steps 142 us of 256 x 256 tiles (160 workgroups) and
+// 127 us of 192 x 256 (220); in 128 x 128 tiles 900 rows 4096 -> 4096 50 us (one workgroup a CU), 1300 rows
+// 4096 -> 11008 146 us (four) but dX of 5000 rows 11008 -> 4096 590 us (five; 192 rows: 520).  Without the 192-row tile (its rows fill the rounds that 256 leave short): 1500 rows 4096 -> 11008 199 us,
+// with it 166; 5000 rows 4096 -> 4096 208 and 179; 2400 gated rows 4096 -> 4096 216 and 181.
+constexpr double kStep256Us = 0.8, kStep192Us = 0.68, kStep128Us = 0.33, kStep128PairUs = 0.3;
+double step_us(int cfg, int64_t per_cu) {
+  if (cfg == sgmv::kTile256) return kStep256Us;
+  if (cfg == sgmv::kTile192) return kStep192Us;
+  return per_cu < 2 ? kStep128Us : kStep128PairUs;
+}
 // The two small ones are bound by streaming B.
-constexpr double kStep256Us = 0.8, kStep128Us = 0.35;
 constexpr double kStreamBytesPerUs = 5.2e6;  // B of the small tiles, with every slot of the device taken
 constexpr double kPlaneBytesPerUs = 4.0e6;   // partial planes, written and read again
 
@@ -36,7 +44,8 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
   for (int cfg = sgmv::kTile256; cfg <= sgmv::kTile32; ++cfg) {
     const int bm = sgmv::dense_tile_rows(cfg);
     // A tile with more than half of its rows empty only where none is smaller.
-    if (cfg == sgmv::kTile256 && M <= 128) continue;
+    if (cfg <= sgmv::kTile192 && M <= 128) continue;
+    if (cfg == sgmv::kTile192 && !may_split) continue;
     if (cfg == sgmv::kTile128 && M <= 64 && may_split) continue;  // dW has no smaller tile
     if (cfg == sgmv::kTile64 && (M <= 32 || M > 64)) continue;
     if (cfg == sgmv::kTile32 && M > 32) continue;
@@ -50,7 +59,8 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
       const int64_t wgs = tm * tn * ks, rounds = ceil_div(wgs, slots);
       double cost;
       if (cfg <= sgmv::kTile128) {
-        cost = (double)ceil_div(wgs, kCus) * ((double)per * (cfg == sgmv::kTile256 ? kStep256Us : kStep128Us)) + 4.0;
+        const int64_t per_cu = ceil_div(wgs, kCus);
+        cost = (double)per_cu * (double)per * step_us(cfg, per_cu) + 4.0;
       } else {
         // Gated 4096 -> 11008, one row: 344, 430 and 516 workgroups on 512 slots took 37.8, 34.9 and 39.1 us.
         const double fill = (double)wgs / (double)(rounds * slots);
@@ -152,8 +162,8 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   l.out = plan_dense(M, N, kt * (op == SGMV_GATED_BACKWARD ? 2 : 1), cols, true);
   l.out.term_in_tile = in_tile ? 1 : 0;
   l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile) || l.halves > 1;
-  // (The largest tile's workgroups are too big to share a launch with.)
-  l.one_launch = l.lora && !back && l.out.to_planes && !in_tile && l.out.cfg != sgmv::kTile256;
+  // (The large tiles' workgroups are too big to share a launch with.)
+  l.one_launch = l.lora && !back && l.out.to_planes && !in_tile && l.out.cfg > sgmv::kTile192;
   if (l.one_launch) l.row_k_off = take((size_t)n * sizeof(int32_t));
   if (l.out.to_planes) l.out.plane_bytes = (size_t)l.out.ksplit * M * N * cols * sizeof(float);
   size_t area = l.out.plane_bytes;

@@ -10,11 +10,14 @@ constexpr int kDenseK = 32;  // contraction length of one tile step
 // are half gate, half up).
 enum DenseTile : int {
   kTile256 = 0,  // 256 x 256, 8 waves
-  kTile128 = 1,  // 128 x 128, 4 waves
-  kTile64 = 2,   // 64 x 256, 4 waves
-  kTile32 = 3    // 32 x 256, 4 waves
+  kTile192 = 1,  // 192 x 256, 8 waves (not for dW)
+  kTile128 = 2,  // 128 x 128, 4 waves
+  kTile64 = 3,   // 64 x 256, 4 waves
+  kTile32 = 4    // 32 x 256, 4 waves
 };
-constexpr int dense_tile_rows(int t) { return t == kTile256 ? 256 : t == kTile128 ? 128 : t == kTile64 ? 64 : 32; }
+constexpr int dense_tile_rows(int t) {
+  return t == kTile256 ? 256 : t == kTile192 ? 192 : t == kTile128 ? 128 : t == kTile64 ? 64 : 32;
+}
 constexpr int dense_tile_cols(int t) { return t == kTile128 ? 128 : 256; }
 
 constexpr int kThinRows = 64;      // rows of one segment per thin-product workgroup

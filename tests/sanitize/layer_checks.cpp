@@ -24,10 +24,10 @@ static int failures = 0;
     }                                                                     \
   } while (0)
 
-static int seen_cfg[4], seen_split, seen_one_launch, seen_in_tile;
+static int seen_cfg[5], seen_split, seen_one_launch, seen_in_tile;
 
 static void check_dense(const DensePlan& d, int64_t M, int64_t N, int64_t steps, int cols) {
-  CHECK(d.cfg >= 0 && d.cfg <= 3);
+  CHECK(d.cfg >= 0 && d.cfg <= 4);
   CHECK((int64_t)d.tiles_m * sgmv::dense_tile_rows(d.cfg) >= M);
   CHECK((int64_t)(d.tiles_m - 1) * sgmv::dense_tile_rows(d.cfg) < std::max<int64_t>(M, 1));
   const int64_t c = sgmv::dense_tile_cols(d.cfg) / cols;
@@ -123,7 +123,7 @@ int main() {
     p.max_seg_len = p.num_segs ? (int32_t)std::min<int64_t>(p.n_rows, ceil_div(p.n_rows, p.num_segs) + (int64_t)(rng() % 500)) : 0;
     for (int op = 0; op < 4; ++op) check_problem(p, op);
   }
-  for (int i = 0; i < 4; ++i) CHECK(seen_cfg[i] > 100);
+  for (int i = 0; i < 5; ++i) CHECK(seen_cfg[i] > 100);
   CHECK(seen_split > 100 && seen_one_launch > 100 && seen_in_tile > 100);
   if (failures) return 1;
   std::puts("layer checks ok");

@@ -165,6 +165,8 @@ LARGE = {
     "split_deep": (23, "bf16", 520, 8200, 520, 32, 3, "uncovered", None, False),
     "distinct_wide": (24, "f16", 700, 264, 2056, 16, 40, "distinct", None, False),
     "one_long_segment": (25, "bf16", 3000, 136, 1032, 8, 1, "one", None, False),
+    "tile192_out": (27, "f16", 190, 72, 33000, 64, 3, "uncovered", (64, 8, 32), True),
+    "tile192_in": (28, "bf16", 181, 33000, 72, 16, 3, "mixed", None, False),
     "many_loras_few_segments": (26, "f16", 1500, 264, 520, 32, 60, "uncovered", (32, 8, 16), True),
 }
 
