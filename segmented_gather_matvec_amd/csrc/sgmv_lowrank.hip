@@ -298,16 +298,16 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch 
 }
 
 // Sums the splits' planes of one LoRA's gradient (split order), and writes the zeros of LoRAs that no
-// workgroup has seen: kSumTurns times four values per thread (one turn took 45 us instead of 25 for 57 LoRAs'
-// zeros: the search for the LoRA's segments outweighed them).
-constexpr int kSumTurns = 8;
-__host__ __device__ constexpr int64_t sum_blocks(int64_t C, int64_t rank) {  // of one LoRA
-  return (C * rank / 4 + kThreads * kSumTurns - 1) / (kThreads * kSumTurns);
+// workgroup has seen: p.turns times four values per thread.  Many turns only where workgroups abound: eight took 19 us for
+// six planes of 8 gradients of 4096 x 16 (64 workgroups), one takes 6; and one took 45 us instead of 25 for
+// 57 LoRAs' zeros (the search for the LoRA's segments outweighed them).
+__host__ __device__ constexpr int64_t sum_blocks(int64_t C, int64_t rank, int turns) {  // of one LoRA
+  return (C * rank / 4 + kThreads * turns - 1) / (kThreads * turns);
 }
 template <class T>
 __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBatch batch) {
   const LoraGradParams& p = batch.p[blockIdx.y];
-  const int64_t blocks = sum_blocks(p.C, p.rank);
+  const int64_t blocks = sum_blocks(p.C, p.rank, p.turns);
   const int k = (int)(blockIdx.x / blocks);
   if (k >= p.meta.num_loras) return;
   const int R = p.rank;
@@ -328,13 +328,24 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBa
   if (!zeros && (!rows || p.nsplit <= 1)) return;
   const int64_t n = (int64_t)p.C * rk;
   const int64_t stride = (int64_t)p.meta.num_loras * p.C * R;
-  for (int turn = 0; turn < kSumTurns; ++turn) {
-    const int64_t o = (((blockIdx.x - k * blocks) * kSumTurns + turn) * kThreads + threadIdx.x) * 4;
+  constexpr int kBatch = 8;  // planes in flight
+  const int planes = zeros ? 0 : p.nsplit;
+  for (int turn = 0; turn < p.turns; ++turn) {
+    const int64_t o = (((blockIdx.x - k * blocks) * p.turns + turn) * kThreads + threadIdx.x) * 4;
     if (o >= n) return;  // o: of the stored gradient
     // Planes hold [C][rank] or [rank][C]; the stored [C, r_k] has its own row length.
     const float* pl = p.planes + (int64_t)k * p.C * R + (p.rank_major || rk == R ? o : o / rk * R + o % rk);
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
-    for (int g = 0; g < (zeros ? 0 : p.nsplit); ++g) v += *reinterpret_cast<const f32x4*>(pl + g * stride);
+    for (int g0 = 0; g0 < planes; g0 += kBatch) {
+      f32x4 x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+        x[u] = *reinterpret_cast<const f32x4*>(pl + (g0 + u < planes ? g0 + u : planes - 1) * stride);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = g0 + u < planes ? v[e] + x[u][e] : v[e];
+    }
     if (p.accumulate) {
       const u32x2 old = *reinterpret_cast<const u32x2*>(out + o);
       v[0] += T::lo(old[0]);
@@ -414,16 +425,22 @@ hipError_t launch_thin_t(const ThinParams* p, int count, hipStream_t s) {
 template <class T>
 hipError_t launch_lora_grad_t(const LoraGradParams* p, int count, hipStream_t s) {
   LoraGradBatch batch{};
-  int64_t tiles = 0, blocks = 0;
+  int64_t tiles = 0, items = 0, blocks = 0;
   int nsplit = 1;
+  bool sums = false;
   for (int i = 0; i < count; ++i) {
-    batch.p[i] = p[i];
     const int64_t loras = p[i].meta.num_loras;
     tiles = std::max(tiles, (p[i].C + kLoraGradCols - 1) / kLoraGradCols *
                                 (p[i].by_segment ? (int64_t)p[i].meta.num_segs : loras));
-    if (p[i].nsplit > 1 || (p[i].by_segment && !p[i].accumulate))
-      blocks = std::max(blocks, sum_blocks(p[i].C, p[i].rank) * loras);
     nsplit = std::max(nsplit, p[i].nsplit);
+    sums = sums || p[i].nsplit > 1 || (p[i].by_segment && !p[i].accumulate);
+    items += loras * sum_blocks(p[i].C, p[i].rank, 1);
+  }
+  const int turns = (int)std::max<int64_t>(1, std::min<int64_t>(8, items / 2048));
+  for (int i = 0; i < count; ++i) {
+    batch.p[i] = p[i];
+    batch.p[i].turns = turns;
+    if (sums) blocks = std::max(blocks, sum_blocks(p[i].C, p[i].rank, turns) * p[i].meta.num_loras);
   }
   if (tiles > 0x7fffffff || blocks > 0x7fffffff) return hipErrorInvalidValue;
   const dim3 grid((unsigned)tiles, (unsigned)count, (unsigned)nsplit);
