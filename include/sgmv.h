@@ -491,8 +491,9 @@ sgmv_status_t sgmv_base_lora_apply_partial(const sgmv_problem_t* problem, const 
  * Precision: sums are fp32; every output is rounded once, from fp32 (H from
  * the unrounded G and U).  X @ A_k and dY @ B_k^T stay fp32.  The gated backward
  * rounds dG and dU to the 16-bit format once, since they are operands of the matrix
- * cores (up to 64 rows it carries them as two 16-bit halves each instead).  Results
- * do not depend on timing: no atomics, sums in a fixed order.
+ * cores (where that would be few values, up to 128 rows and 2^18 values of dG, it
+ * carries them as two 16-bit halves each instead).  Results do not depend on
+ * timing: no atomics, sums in a fixed order.
  *
  * Gradients (sgmv_projection_grad_t): each of dX, dW, dA_ptrs, dB_ptrs may be
  * NULL (not wanted), and so may entries of the dA and dB tables and the whole

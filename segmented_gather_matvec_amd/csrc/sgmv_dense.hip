@@ -15,6 +15,19 @@
 // The LoRA term joins before the output: per run of rows that share a LoRA, V's
 // hi + lo 16-bit halves (together 16 or 22 bits of fp32's V) times E_k on the
 // matrix cores, added to the accumulators in fp32; outputs are rounded once.
+//
+// Bound, many rows: the matrix cores, and past them the power limit.  The gated 8192 x 4096 -> 11008 product
+// runs 1.32 ms, 1.12 PFLOP/s, with the matrix cores busy in 56% of all cycles at a clock that the load
+// holds near 1.9 GHz; a plain library product of the same size reaches 1.24 PFLOP/s.  What it took: both operands of
+// a step read from LDS between the products of the step before (1.81 -> 1.60 ms), steps of 32 in a ring of four
+// slots instead of 64 in two (1.47), LDS swizzles without bank conflicts (the dX product's GPU cycles
+// -6%), the LoRA term from LDS behind one barrier (r = 64, 1777 rows: 520 -> 500 us).
+// Tile: 8 waves of 128 x 64 accumulators hold 256 x 256; four waves of 128 x 128 spilled.  256 x 256
+// reads each operand from LDS least per product; 192 x 256 fills rounds that 256 rows leave short, and
+// 128 x 128 small grids (the host's plan has the figures).
+// Few rows: HBM, reading W once.  32 x 256 and 64 x 256 tiles, two workgroups a CU with 64 KiB or more of W's loads in
+// flight each: one gated row of 4096 -> 11008 streams 181 MB in 33.6 us, 5.4 TB/s.  Contraction splits
+// fill the device there; their fp32 planes stay in the Infinity Cache until the epilogue sums them.
 #include "sgmv_thin.h"
 
 namespace sgmv {
@@ -132,7 +145,7 @@ __device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x
         lv.init(wave, lane, 2 * R);
         for (int a = 0; a < steps; ++a) {
           const int col = a / chunks * R + a % chunks * 32;
-          lv.start(t.V16, 2 * R, m0, p.M, col, col + (2 * R < 32 ? 2 * R : 32));
+          lv.start(t.V16, 2 * R, m0, sm.n_rows, col, col + (2 * R < 32 ? 2 * R : 32));
           lv.issue(ring + a * S::SLOT);
         }
         first = false;
@@ -436,11 +449,11 @@ __global__ __launch_bounds__(kThreads, S::WAVES_PER_SIMD) void sgmv_dense_thin_k
 // ---------------------------------------------------------------- epilogue of the partial planes
 // One wave per (row i, 256 columns): lane l owns columns c .. c+3.  Sums the
 // planes in plane order; when the tiles did not add the LoRA term, adds
-// V[i] @ E_k with vector FMA in fp32 (short segments: a row brings its own E_k).
+// V[i] @ E_k with vector FMA in fp32 (decode, short segments: a row brings its own E_k).
 // Bound by the latency of its dependent loads: the first kPlanes planes, V's planes and
-// the row's LoRA are all asked for before any of them is waited for, then 16 ranks of E_k of both terms.
-// (Eight columns per lane and four planes at a time took 11.2 us for one gated row of 11008, against
-// 4.6 us for a dense row of 4096.)
+// the row's LoRA are all asked for before any of them is waited for, then 16 ranks of E_k of both terms:
+// 5.0 us for a dense row of 4096, 9.4 us for a gated row of 11008, 12.0 us for 32 gated rows of as many
+// LoRAs (22 MB of E_k).  Eight columns per lane and four planes at a time took 11.2 us for the gated row.
 constexpr int kPlanes = 8;
 constexpr int kEpilogueCols = 256;
 typedef const __attribute__((address_space(1))) u32x2* global_u32x2_ptr;

@@ -10,22 +10,41 @@ namespace {
 
 constexpr int64_t kCus = 256;                          // compute units of an MI355X
 constexpr int64_t kGradPlaneBytes = (int64_t)256 << 20;  // most the splits of a LoRA gradient may take
-// Rows up to which the gated backward carries dG and dU unrounded (hi + lo halves): its products are
-// bound by reading W there, and a few large values' rounding would show in dX and dA (up to 1.7 times the
-// error of an output's own rounding; 1.4 times where it averages out over many rows).
-constexpr int kHalvesRows = 64;
-constexpr int kShortRun = 16;  // rows per segment from which the tiles' matrix cores add the LoRA term
+// Rows, and values of dG, up to which the gated backward carries dG and dU unrounded (hi + lo halves): a few large
+// values' rounding would show in dX and dA, up to 1.7 times the error of an output's own rounding at 5 rows and
+// 1.5 times at 77 x 1048, where 1.4 times is what averages out over many.  Few rows are bound by reading W, so
+// that twice the rows cost little: 4096 -> 11008, r = 64, 16 rows 68.4 -> 76.5 us; 4096 -> 4096, 64 rows 43 -> 44
+// us; but 4096 -> 11008 of 128 rows 82 -> 116.
+constexpr int kHalvesRows = 128;
+constexpr int64_t kHalvesValues = 1 << 18;
+
+// Whether the tiles' matrix cores add the LoRA term, run by run of rows that share a LoRA (a tile's runs come one
+// after another), or the epilogue, row by row from fp32 planes.  Microseconds of either; measured, tiles and
+// epilogue: forward, 1024 rows 4096 -> 4096, r = 16: 2 rows a segment 120 and 89 us, 4 rows 84 and 80, 8 rows 65
+// and 77; r = 64: 2 rows 200 and 202, 4 rows 131 and 154.  dX, whose epilogue reads A_k row by row: 128 rows,
+// r = 64, 4 segments 34 and 84 us, 128 segments 181 and 115; r = 16, 128 segments 128 and 50; 8 rows, r = 16,
+// 1 segment 22 and 23, 8 segments 26 and 23; 1024 rows, a LoRA each, r = 16: 210 and 200, r = 64: 338 and 780.
+bool tiles_add_term(const sgmv_problem_t& p, bool back, int terms, int64_t N) {
+  const double n = p.n_rows;
+  const double runs = std::max(1.0, p.num_segs * std::min(1.0, 256.0 / n));  // of one tile
+  const double tiles = terms * runs * (p.rank > 32 ? 1.2 : 0.8);
+  const double rows = 2.0 + terms * (back ? 2.0 : 1.0) * n * (double)N * p.rank * 1e-6;
+  return tiles < rows;
+}
+// Up to here the forward's thin products share the dense launch, and the epilogue follows in any case.
+constexpr int64_t kDecodeRows = 128;
 
 // Workgroups of a tile shape that run at once on one CU (LDS).
 int resident(int cfg) { return cfg <= sgmv::kTile192 ? 1 : 2; }
 
 // The model that picks between tile shapes and splits; only ratios matter.
 // Large tiles are bound by the matrix cores: microseconds of one contraction
-// step of one workgroup on its CU.  Measured, bf16, r = 16: 8192 x 4096 -> 11008 in 6 rounds of 128 steps of 256 x 256
-// tiles 616 us; 2011 x 5120 -> 5120 in one round of 160 steps 142 us of 256 x 256 tiles (160 workgroups) and
-// 127 us of 192 x 256 (220); in 128 x 128 tiles 900 rows 4096 -> 4096 50 us (one workgroup a CU), 1300 rows
-// 4096 -> 11008 146 us (four) but dX of 5000 rows 11008 -> 4096 590 us (five; 192 rows: 520).  Without the 192-row tile (its rows fill the rounds that 256 leave short): 1500 rows 4096 -> 11008 199 us,
-// with it 166; 5000 rows 4096 -> 4096 208 and 179; 2400 gated rows 4096 -> 4096 216 and 181.
+// step of one workgroup on its CU.  Measured, bf16, r = 16: 8192 x 4096 -> 11008 in 6 rounds of 128 steps of
+// 256 x 256 tiles 616 us; 2011 x 5120 -> 5120 (r = 64) in one round of 160 steps 142 us of 256 x 256 tiles (160
+// workgroups) and 127 us of 192 x 256 (220); 900 rows 4096 -> 4096 in 128 x 128 tiles 50 us (one workgroup a
+// CU), 1300 rows 4096 -> 11008 146 us (four), but dX of 5000 rows 11008 -> 4096 590 us (five; 192 rows: 520).
+// Without the 192-row tile (it fills rounds that 256 rows leave short) and with it: 1500 rows 4096 -> 11008
+// 199 and 166 us; 5000 rows 4096 -> 4096 208 and 174; 2400 gated rows 4096 -> 4096 216 and 179.
 constexpr double kStep256Us = 0.8, kStep192Us = 0.68, kStep128Us = 0.33, kStep128PairUs = 0.3;
 double step_us(int cfg, int64_t per_cu) {
   if (cfg == sgmv::kTile256) return kStep256Us;
@@ -129,8 +148,8 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   LayerPlan l;
   l.projections = layer_gated(op) ? 2 : 1;
   l.lora = !nothing_to_do(p);
-  l.halves = op == SGMV_GATED_BACKWARD && p.n_rows <= kHalvesRows ? 2 : 1;
   const int64_t n = p.n_rows;
+  l.halves = op == SGMV_GATED_BACKWARD && n <= kHalvesRows && n * p.h_out <= kHalvesValues ? 2 : 1;
   const bool back = layer_backward(op);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
@@ -153,10 +172,8 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   }
   if (op == SGMV_GATED_BACKWARD)
     for (int i = 0; i < 2; ++i) l.gate_off[i] = take((size_t)n * l.halves * p.h_out * 2);
-  // The LoRA term joins in the tiles where segments are long enough for a
-  // matrix instruction's 16 rows; else the epilogue launch adds it row by row.
-  const bool in_tile = l.lora && n > 128 && n >= (int64_t)kShortRun * p.num_segs;
   const int64_t M = n * l.halves, N = back ? p.h_in : p.h_out;
+  const bool in_tile = l.lora && (back || n > kDecodeRows) && tiles_add_term(p, back, l.projections, N);
   const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK);
   const int cols = op == SGMV_GATED_FORWARD ? 2 : 1;
   l.out = plan_dense(M, N, kt * (op == SGMV_GATED_BACKWARD ? 2 : 1), cols, true);

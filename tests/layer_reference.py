@@ -10,7 +10,7 @@ Bounds, per element, with h = eps / 2 of the 16-bit format (half a step: 2^-8 bf
   fp16, half of the smallest denormal (2^-25) where lo underflows, in units of the power 2^(16 b) that brings the row's largest
   value to [2^-4, 2^12).  The gradients of A_k and B_k sum rows in the LoRA's largest unit: bringing hi and lo there
   rounds each by another 2^-25 at most, 3 * 2^-25 < 2^-23 in all;
-* dG, dU of the gated backward are rounded once: h of each; up to 64 rows they are two halves: h^2;
+* dG, dU of the gated backward are rounded once: h of each; up to 128 rows and 2^18 values they are two halves: h^2;
 * the activation in fp32: 2^-20 of the terms it is made of (exp and the divisions are good to a few
   units in the last place each).
 Errors of intermediate values propagate through the absolute values of what multiplies them.
@@ -180,7 +180,7 @@ def gate_backward(c, kind):
     a, slope = act(kind, g)
     floor = 2.0 ** -25 if c.dtype == torch.float16 else 0.0
     dg, du = dh * u * slope, dh * a
-    if c.n <= 64:
+    if c.n <= 128 and c.n * c.h_out <= 2 ** 18:
         h = h * h
     eg = h * dg.abs() + 2.0 ** -20 * (dh * u).abs() * 1.13 * (1 + g.abs()) + floor
     eu = h * du.abs() + 2.0 ** -20 * (dh * g).abs() + floor

@@ -53,7 +53,7 @@ static void check_problem(const sgmv_problem_t& p, int op) {
     const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK) * (op == SGMV_GATED_BACKWARD ? 2 : 1);
     check_dense(l.out, n * l.halves, back ? p.h_in : p.h_out, kt, op == SGMV_GATED_FORWARD ? 2 : 1);
     CHECK(l.out.ksplit == 1 || l.out.to_planes);
-    CHECK(l.halves == 1 || (op == SGMV_GATED_BACKWARD && l.out.to_planes && !l.out.term_in_tile));
+    CHECK(l.halves == 1 || (op == SGMV_GATED_BACKWARD && l.out.to_planes));
     CHECK(!l.lora || l.out.term_in_tile || l.out.to_planes);  // the term is added somewhere
     seen_one_launch += l.one_launch;
     seen_in_tile += l.out.term_in_tile;
