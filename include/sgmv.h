@@ -376,9 +376,8 @@ sgmv_status_t sgmv_lora_apply_batched(const sgmv_problem_t* problem, const void*
  *           when num_segs == 0 or max_seg_len == 0: then Y = X @ W).
  *   ws      device workspace of sgmv_base_workspace_bytes bytes (any contents;
  *           it holds the fp32 partial planes of V and of X @ W).
- * Supported: n_rows <= SGMV_BASE_MAX_ROWS (SGMV_ERR_UNSUPPORTED above; a
- * prefill-sized base projection is a dense GEMM for a GEMM library, followed by
- * sgmv_lora_apply);
+ * Supported: n_rows <= SGMV_BASE_MAX_ROWS (SGMV_ERR_UNSUPPORTED above;
+ * sgmv_dense_lora_apply takes any number of rows);
  * ranks, formats and alignment as for sgmv_lora_apply.  Two launches (split-K
  * partial products of X @ W on the matrix cores together with the partial
  * planes of V = X @ A_k; an epilogue that sums them, adds V @ B_k and rounds);

@@ -167,6 +167,9 @@ LARGE = {
     "one_long_segment": (25, "bf16", 3000, 136, 1032, 8, 1, "one", None, False),
     "tile192_out": (27, "f16", 190, 72, 33000, 64, 3, "uncovered", (64, 8, 32), True),
     "tile192_in": (28, "bf16", 181, 33000, 72, 16, 3, "mixed", None, False),
+    "few_rows_term_in_tile": (29, "f16", 20, 1160, 264, 64, 3, "uncovered", (64, 8, 24), True),
+    "few_rows_one_segment": (30, "bf16", 60, 2056, 136, 32, 2, "one", None, False),
+    "hundred_rows_r64": (31, "f16", 100, 1032, 4104, 64, 4, "mixed", None, True),
     "many_loras_few_segments": (26, "f16", 1500, 264, 520, 32, 60, "uncovered", (32, 8, 16), True),
 }
 
