@@ -58,10 +58,11 @@ struct DenseShape {
   static_assert(TM * 16 * WM == BM && TNP * NB * 16 * WN == BN, "tile splits evenly over the waves");
 };
 
-// Loads a step of E_k (columns n0 .. n0 + C of the forward's B_k [r_k, N], or rows of dX's A_k [N, r_k]) as a B operand tile:
-// ranks k0 .. k0+31, or, at ranks up to 16, all of them twice, for V's hi and lo halves.
+// Loads a step of E_k (columns n0 .. n0 + C of the forward's B_k [r_k, N], or rows of dX's A_k [N, r_k]) as a B
+// operand tile: ranks k0 .. k0+31, or, at ranks up to 16, all of them twice, for V's hi and lo halves.
 template <int C, int LOADS, bool T>
-__device__ inline void issue_e(const uint16_t* E, int rk, int R, int k0, int N, int n0, uint16_t* lds, int wave, int lane) {
+__device__ inline void issue_e(const uint16_t* E, int rk, int R, int k0, int N, int n0, uint16_t* lds, int wave,
+                               int lane) {
   const int cols = N - n0 < C ? N - n0 : C;
   const uint32_t bytes = T ? (uint32_t)((rk - 1) * N + (N - n0)) * 2u : (uint32_t)(cols * rk) * 2u;
   const auto rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(E + (T ? (int64_t)n0 : (int64_t)n0 * rk)), 0,
@@ -105,7 +106,8 @@ __device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x
   for (int s0 = first_segment_past(sm, m0); s0 < sm.num_segs; s0 += 64) {
     // Metadata of 64 segments at a time, one per lane.
     const int sl = s0 + lane < sm.num_segs ? s0 + lane : sm.num_segs - 1;
-    const int lo_l = sm.seg_indptr[sl], hi_l = sm.seg_indptr[sl + 1];
+    const int lo_l = sm.seg_indptr[sl], end_l = sm.seg_indptr[sl + 1];
+    const int hi_l = end_l < sm.n_rows ? end_l : sm.n_rows;
     int k_l = sm.lora_idx[sl];
     if (k_l < 0 || k_l >= sm.num_loras) k_l = -1;
     const uint64_t e_l = k_l >= 0 ? t.ptrs[k_l] : 0ull;
@@ -345,7 +347,8 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
       if (p.term[1].V16 != nullptr) add_term<T, MODE, S, TNP>(p, p.term[1], acc, ring, m0, n0, wave, lane);
     } else {
       for (int t = 0; t < (MODE == kDenseDx ? p.pairs : 1); ++t) {
-        const LowRankTerm term{nullptr, t ? p.term[1].V16 : p.term[0].V16, t ? p.term[1].row_scale : p.term[0].row_scale,
+        const LowRankTerm term{nullptr, t ? p.term[1].V16 : p.term[0].V16,
+                               t ? p.term[1].row_scale : p.term[0].row_scale,
                                t ? p.term[1].ptrs : p.term[0].ptrs, t ? p.term[1].ranks : p.term[0].ranks};
         if (term.V16 != nullptr) add_term<T, MODE, S, 0>(p, term, acc, ring, m0, n0, wave, lane);
       }
@@ -464,7 +467,8 @@ __device__ inline void load_planes(const DenseParams& p, int proj, int64_t o, in
   const float* src = p.planes + (int64_t)proj * p.ksplit * p.plane_stride + o;
 #pragma unroll
   for (int u = 0; u < kPlanes; ++u)
-    x.a[u] = *reinterpret_cast<const f32x4*>(src + (int64_t)(g0 + u < p.ksplit ? g0 + u : p.ksplit - 1) * p.plane_stride);
+    x.a[u] = *reinterpret_cast<const f32x4*>(src + (int64_t)(g0 + u < p.ksplit ? g0 + u : p.ksplit - 1) *
+                                                       p.plane_stride);
 }
 // y = the sum of all planes; x holds the first kPlanes of them.
 __device__ inline void plane_sum(const DenseParams& p, int proj, int64_t o, PlaneBatch& x, f32x4& y) {

@@ -48,7 +48,7 @@ struct DenseParams {
   int32_t rank;
   int32_t act;
   int32_t accumulate;    // dW: add to what is there
-  int32_t to_planes;     // 1: fp32 partial planes instead of the outputs (ksplit > 1, or a term added by the epilogue kernel)
+  int32_t to_planes;     // 1: fp32 partial planes instead of the outputs (ksplit > 1, or the epilogue adds a term)
   int32_t term_in_tile;  // 1: split 0 of every tile adds the LoRA term
   int32_t v_planes;      // partial planes of term[].V that the epilogue sums
   const int32_t* row_k;  // [n_rows] LoRA of each covered row (see ThinParams); null: the epilogue searches

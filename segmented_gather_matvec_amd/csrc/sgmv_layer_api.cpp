@@ -213,8 +213,8 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
     if (sgmv::launch_thin(c.p.dtype, t, count, c.stream) != hipSuccess) return SGMV_ERR_HIP;
   }
   if (dX && rows) {
-    sgmv::DenseParams q = dense_params(c, c.plan.out, (int64_t)c.p.n_rows * c.plan.halves, c.p.h_in, c.p.h_out, c.p.h_out,
-                                       c.p.h_out);
+    sgmv::DenseParams q = dense_params(c, c.plan.out, (int64_t)c.p.n_rows * c.plan.halves, c.p.h_in, c.p.h_out,
+                                       c.p.h_out, c.p.h_out);
     q.pairs = c.np;
     for (int i = 0; i < c.np; ++i) {
       q.A[i] = half(dY[i]);
@@ -296,7 +296,8 @@ sgmv_status_t sgmv_dense_lora_apply(const sgmv_problem_t* p, const void* X, cons
   st = check_call(X, &W, &proj, 1, seg_indptr, lora_idx, ws, ws_bytes, plan);
   if (st != SGMV_OK) return st;
   const Call c{*p, SGMV_DENSE_FORWARD, plan, 1, X, {W, nullptr}, {proj, nullptr},
-               seg_meta(*p, plan.lora, seg_indptr, lora_idx), static_cast<char*>(ws), static_cast<hipStream_t>(stream), 0};
+               seg_meta(*p, plan.lora, seg_indptr, lora_idx), static_cast<char*>(ws),
+               static_cast<hipStream_t>(stream), 0};
   void* out[1] = {proj->Y};
   return forward(c, out);
 }
@@ -343,7 +344,8 @@ sgmv_status_t sgmv_dense_lora_backward(const sgmv_problem_t* p, const void* X, c
   st = check_grads(&g, 1, dX);
   if (st != SGMV_OK) return st;
   const Call c{*p, SGMV_DENSE_BACKWARD, plan, 1, X, {W, nullptr}, {proj, nullptr},
-               seg_meta(*p, plan.lora, seg_indptr, lora_idx), static_cast<char*>(ws), static_cast<hipStream_t>(stream), 0};
+               seg_meta(*p, plan.lora, seg_indptr, lora_idx), static_cast<char*>(ws),
+               static_cast<hipStream_t>(stream), 0};
   return backward(c, &dY, dX, &g, accumulate);
 }
 
@@ -373,7 +375,8 @@ sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* p, const void* X, c
   if (st != SGMV_OK) return st;
   const Call c{*p, SGMV_GATED_BACKWARD, plan, 2, X, {Wg, Wu}, {gate, up}, seg_meta(*p, plan.lora, seg_indptr, lora_idx),
                static_cast<char*>(ws), static_cast<hipStream_t>(stream), act};
-  uint16_t* d[2] = {reinterpret_cast<uint16_t*>(c.at(plan.gate_off[0])), reinterpret_cast<uint16_t*>(c.at(plan.gate_off[1]))};
+  uint16_t* d[2] = {reinterpret_cast<uint16_t*>(c.at(plan.gate_off[0])),
+                    reinterpret_cast<uint16_t*>(c.at(plan.gate_off[1]))};
   if (p->n_rows > 0 &&
       sgmv::launch_gate_backward(p->dtype, act, plan.halves > 1, half(gate->Y), half(up->Y), half(dH), d[0], d[1],
                                  (int64_t)p->n_rows * p->h_out, c.stream) != hipSuccess)
