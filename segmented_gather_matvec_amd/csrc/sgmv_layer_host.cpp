@@ -24,15 +24,18 @@ constexpr int64_t kHalvesValues = 1 << 18;
 // and 77; r = 64: 2 rows 200 and 202, 4 rows 131 and 154.  dX, whose epilogue reads A_k row by row: 128 rows,
 // r = 64, 4 segments 34 and 84 us, 128 segments 181 and 115; r = 16, 128 segments 128 and 50; 8 rows, r = 16,
 // 1 segment 22 and 23, 8 segments 26 and 23; 1024 rows, a LoRA each, r = 16: 210 and 200, r = 64: 338 and 780.
+// Decode, forward: the tiles' term costs launches of its own for V, which the epilogue's shares with W's stream:
+// 128 gated rows 4096 -> 11008, r = 64, 1 segment 83 and 121 us; 64 rows, 4 segments 82 and 98; 128 rows, r = 16, 81
+// and 91; 64 rows, r = 16, 75 and 73; one projection, 128 rows, r = 64, 42 and 47, of 4096 columns 32 and 26.
+constexpr int64_t kDecodeRows = 128;
 bool tiles_add_term(const sgmv_problem_t& p, bool back, int terms, int64_t N) {
   const double n = p.n_rows;
   const double runs = std::max(1.0, p.num_segs * std::min(1.0, 256.0 / n));  // of one tile
   const double tiles = terms * runs * (p.rank > 32 ? 1.2 : 0.8);
-  const double rows = 2.0 + terms * (back ? 2.0 : 1.0) * n * (double)N * p.rank * 1e-6;
-  return tiles < rows;
+  const double products = terms * n * (double)N * p.rank * 1e-6;
+  if (!back && p.n_rows <= kDecodeRows) return tiles + 10.0 < products * (terms > 1 ? 0.3 : 0.2);
+  return tiles < 2.0 + products * (back ? 2.0 : 1.0);
 }
-// Up to here the forward's thin products share the dense launch, and the epilogue follows in any case.
-constexpr int64_t kDecodeRows = 128;
 
 // Workgroups of a tile shape that run at once on one CU (LDS).
 int resident(int cfg) { return cfg <= sgmv::kTile192 ? 1 : 2; }
@@ -173,7 +176,7 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   if (op == SGMV_GATED_BACKWARD)
     for (int i = 0; i < 2; ++i) l.gate_off[i] = take((size_t)n * l.halves * p.h_out * 2);
   const int64_t M = n * l.halves, N = back ? p.h_in : p.h_out;
-  const bool in_tile = l.lora && (back || n > kDecodeRows) && tiles_add_term(p, back, l.projections, N);
+  const bool in_tile = l.lora && tiles_add_term(p, back, l.projections, N);
   const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK);
   const int cols = op == SGMV_GATED_FORWARD ? 2 : 1;
   l.out = plan_dense(M, N, kt * (op == SGMV_GATED_BACKWARD ? 2 : 1), cols, true);

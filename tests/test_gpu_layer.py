@@ -170,6 +170,8 @@ LARGE = {
     "few_rows_term_in_tile": (29, "f16", 20, 1160, 264, 64, 3, "uncovered", (64, 8, 24), True),
     "few_rows_one_segment": (30, "bf16", 60, 2056, 136, 32, 2, "one", None, False),
     "hundred_rows_r64": (31, "f16", 100, 1032, 4104, 64, 4, "mixed", None, True),
+    "hundred_rows_term_in_tile": (32, "bf16", 100, 136, 11016, 64, 2, "one", None, True),
+    "forty_rows_term_in_tile": (33, "f16", 40, 72, 24008, 64, 2, "one", None, False),
     "many_loras_few_segments": (26, "f16", 1500, 264, 520, 32, 60, "uncovered", (32, 8, 16), True),
 }
 
