@@ -25,7 +25,7 @@ struct SegMeta {
 struct LowRankTerm {
   const float* V;          // [v_planes][n_rows][rank] fp32, read by the epilogue kernel (null: no term)
   const uint16_t* V16;     // [n_rows][2][rank] V's hi, then lo halves, read by the tiles (null: no term)
-  const float* row_scale;  // fp16: [n_rows] the power of two that V16's rows are divided by
+  const float* row_scale;  // fp16: [n_rows] the power of two that V16's rows are divided by (0: a row of zeros)
   const uint64_t* ptrs;    // [num_loras] -> B_k [r_k, N], or A_k [N, r_k] for dX
   const int32_t* ranks;    // null, or rank of each LoRA
 };

@@ -74,8 +74,10 @@ __global__ __launch_bounds__(kThreads) void sgmv_thin_sum_kernel(ThinBatch batch
 // r = 64, 94 us (2.6 TB/s).  V16 comes from L2 once per column tile: at 256 columns and r = 64 half as many
 // bytes as Z.  Splits of the rows fill the device when there are few LoRAs; their planes are not atomics, so that sums keep
 // one order.
-// fp16 rows of V16 are kept divided by a power of two each (store_v): the sums run
-// in units of the largest so far, and rows kept in smaller units are brought to it.
+// fp16 rows of V16 are kept divided by a power of two each (store_v), and rows of different powers may not
+// meet in a product (bringing one row to another's power would cost it bits): the matrix cores sum rows of one power, and where it
+// changes, their sum joins the total in fp32.  A step whose rows differ is multiplied once per power, the other rows
+// masked to zeros.  Most steps have one power and cost a comparison.
 // Up to four gradients in one launch (grid y).
 struct LoraGradBatch {
   LoraGradParams p[4];
@@ -122,7 +124,45 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < JT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float unit = 0.f;  // of the sums (fp16 only): the largest row scale so far
+  // fp16: what acc is to be multiplied by, and the sums of other powers.
+  float unit = 0.f;
+  f32x4 total[F16T ? 4 : 1][F16T ? JT : 1];
+#pragma unroll
+  for (int i = 0; i < (F16T ? 4 : 1); ++i)
+#pragma unroll
+    for (int j = 0; j < (F16T ? JT : 1); ++j) total[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto fold = [&](float next) {
+    if constexpr (F16T) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < JT; ++j) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) total[i][j][e] = __builtin_fmaf(acc[i][j][e], unit, total[i][j][e]);
+          acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+      unit = next;
+    }
+  };
+  // acc += the products of a slot's rows; lane q holds rows 8 q .. 8 q + 7, two to a word of `mask`.
+  auto multiply = [&](const uint16_t* now, const u32x4& mask) {
+    u32x4 zf[4], qf[QC / 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) zf[i] = read_operand<COLS, true>(now, wave * 64 + i * 16, lane);
+#pragma unroll
+    for (int j = 0; j < QC / 16; ++j) qf[j] = read_operand<QC, true>(now + B0, j * 16, lane);
+    if constexpr (F16T) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) zf[i] &= mask;  // both: an infinity times a masked zero is NaN
+#pragma unroll
+      for (int j = 0; j < QC / 16; ++j) qf[j] &= mask;
+    }
+#pragma unroll
+    for (int j = QC / 16 - 1; j >= 0; --j)  // lo halves first
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        acc[i][j % JT] = RANK_MAJOR ? mfma<T>(zf[i], qf[j], acc[i][j % JT]) : mfma<T>(qf[j], zf[i], acc[i][j % JT]);
+  };
   bool any = false;  // LoRA k has rows
   int counter = 0;   // steps of 32 rows so far, over all of its segments
 
@@ -197,54 +237,44 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
           __builtin_amdgcn_s_barrier();
           issue(lds + (slot == 0 ? STAGES - 1 : slot - 1) * SLOT);
           const uint16_t* now = lds + slot * SLOT;
-          u32x4 zf[4], qf[QC / 16];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) zf[i] = read_operand<COLS, true>(now, wave * 64 + i * 16, lane);
-#pragma unroll
-          for (int j = 0; j < QC / 16; ++j) qf[j] = read_operand<QC, true>(now + B0, j * 16, lane);
+          bool mixed = false;  // a row of another power than the sums'
+          float u[8];
           if constexpr (F16T) {
-            // Rows 8 q .. 8 q + 7 are this lane's contraction steps.
             const float* sp = reinterpret_cast<const float*>(now + S0) + q * 8;
             const f32x4 u0 = *reinterpret_cast<const f32x4*>(sp), u1 = *reinterpret_cast<const f32x4*>(sp + 4);
-            float big = 0.f, small = 3e38f;  // of the step's rows; rows past the segment have scale 0
 #pragma unroll
-            for (int x8 = 0; x8 < 8; ++x8) {
-              const float u = x8 < 4 ? u0[x8 & 3] : u1[x8 & 3];
-              big = fmaxf(big, u);
-              small = fminf(small, u > 0.f ? u : 3e38f);
+            for (int r = 0; r < 8; ++r) {
+              u[r] = r < 4 ? u0[r & 3] : u1[r & 3];
+              mixed = mixed || (u[r] > 0.f && u[r] != unit);
             }
-#pragma unroll
-            for (int d = 16; d < 64; d <<= 1) {
-              big = fmaxf(big, shfl_xor(big, d));
-              small = fminf(small, shfl_xor(small, d));
-            }
-            if (big > unit) {  // uniform over the wave, as all of this
-              const float f = unit / big;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < JT; ++j) acc[i][j] *= f;
-              unit = big;
-            }
-            if (small < unit) {
-              float f[8];
-#pragma unroll
-              for (int x8 = 0; x8 < 8; ++x8) f[x8] = (x8 < 4 ? u0[x8 & 3] : u1[x8 & 3]) / unit;
-#pragma unroll
-              for (int j = 0; j < QC / 16; ++j) {
-                float v[8];
-                unpack8<T>(qf[j], v);
-#pragma unroll
-                for (int x8 = 0; x8 < 8; ++x8) v[x8] *= f[x8];
-                qf[j] = pack8<T>(v);
-              }
-            }
+            mixed = __ballot(mixed) != 0;
           }
+          // Once, or power by power, largest first; rows of zeros (and past the segment) go with the first.
+          float above = __builtin_inff();
+          u32x4 mask = {~0u, ~0u, ~0u, ~0u};
+          do {
+            if (mixed) {
+              float next = 0.f;
 #pragma unroll
-          for (int j = QC / 16 - 1; j >= 0; --j)  // lo halves first
+              for (int r = 0; r < 8; ++r) next = fmaxf(next, u[r] < above ? u[r] : 0.f);
+              next = fmaxf(next, shfl_xor(next, 16));
+              next = fmaxf(next, shfl_xor(next, 32));
+              next = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(next)));
+              if (!(next > 0.f)) break;
+              if (next != unit) fold(next);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[i][j % JT] = RANK_MAJOR ? mfma<T>(zf[i], qf[j], acc[i][j % JT]) : mfma<T>(qf[j], zf[i], acc[i][j % JT]);
+              for (int w = 0; w < 4; ++w) {
+                mask[w] = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  const float ur = u[2 * w + h];
+                  if (ur == next || (ur == 0.f && above > 3.4e38f)) mask[w] |= 0xffffu << (16 * h);
+                }
+              }
+              above = next;
+            }
+            multiply(now, mask);
+          } while (mixed);
           slot = slot + 1 == STAGES ? 0 : slot + 1;
         }
         wait_loads_and_lds<0>();
@@ -252,6 +282,7 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
       __syncthreads();  // the list and the slots are read before the next pass or window overwrites them
     }
   }
+  fold(0.f);
   // A LoRA without rows: zeros, written by split 0, or what it has when gradients accumulate.
   if (!any && (p.accumulate || z > 0)) return;
   const bool planes = p.nsplit > 1 && any;
@@ -261,13 +292,16 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
     for (int j = 0; j < JT; ++j) {
       const int c = c0 + wave * 64 + i * 16 + (RANK_MAJOR ? q * 4 : ml);
       const int r = j * 16 + (RANK_MAJOR ? ml : q * 4);
-      f32x4 v = acc[i][j];
+      f32x4 v;
+      if constexpr (F16T)
+        v = total[i][j];
+      else
+        v = acc[i][j];
       if constexpr (R == 8) {  // ranks 8..15 are the lo halves' sums of ranks 0..7
 #pragma unroll
         for (int x = 0; x < 4; ++x) v[x] += RANK_MAJOR ? shfl_xor(v[x], 8) : shfl_xor(v[x], 32);
       }
       if (c >= p.C || r >= rk) continue;
-      if constexpr (F16T) v *= unit;
       if (planes) {
         float* dst = p.planes + ((int64_t)z * p.meta.num_loras + k) * p.C * R +
                      (RANK_MAJOR ? (int64_t)r * p.C + c : (int64_t)c * R + r);
@@ -289,7 +323,7 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
 }
 
 template <class T, int R>
-__global__ __launch_bounds__(kThreads) void sgmv_lora_grad_kernel(LoraGradBatch batch) {
+__global__ __launch_bounds__(kThreads, 2) void sgmv_lora_grad_kernel(LoraGradBatch batch) {
   using S = LoraGradShape<T, R>;
   __shared__ __attribute__((aligned(1024))) uint16_t lds[S::STAGES * S::SLOT];
   __shared__ int lds_lo[kThreads], lds_hi[kThreads];

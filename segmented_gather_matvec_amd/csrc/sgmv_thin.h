@@ -19,22 +19,26 @@ __device__ inline void store_v(const ThinParams& p, int row, int c, float (&v)[8
   // fp16 halves hold V well only within some binades (above 65504 they overflow, far below 1 the lo
   // half and then the hi half run out of denormals): the row is kept divided by the power 2^(16 b) that
   // brings its largest value to [2^-4, 2^12) (exact), and the reader puts it back.  Steps of 2^16
-  // around 1, so that most rows share one.
+  // around 1, so that most rows share one.  A row of zeros has the power 0: it goes with any.
   if constexpr (T::kMaxFinite < 1e6f) {
-    float big = 0.f;
+    float big = 0.f, any = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float a = fabsf(v[e]);
       big = fmaxf(big, a < 3.4e38f ? a : 0.f);  // not of infinities and NaN
+      any = a == 0.f ? any : 1.f;
     }
-    for (int d = 1; d < p.rank / 8; d <<= 1) big = fmaxf(big, shfl_xor(big, d));
+    for (int d = 1; d < p.rank / 8; d <<= 1) {
+      big = fmaxf(big, shfl_xor(big, d));
+      any = fmaxf(any, shfl_xor(any, d));
+    }
     int b = (((int)(__float_as_uint(big) >> 23) & 255) - 127 + 4) >> 4;
     b = b < -7 ? -7 : b > 7 ? 7 : b;
     const float up = __uint_as_float((uint32_t)(127 + 16 * b) << 23);
     const float down = __uint_as_float((uint32_t)(127 - 16 * b) << 23);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= down;
-    if (c == 0) p.row_scale[row] = up;
+    if (c == 0) p.row_scale[row] = any * up;
   }
   u32x4 hi, lo;
   split8<T>(v, hi, lo);
