@@ -91,6 +91,18 @@ struct LoraGradShape {
   static constexpr int B0 = COLS * ROWS, S0 = B0 + QC * ROWS, SLOT = S0 + (F16T ? 128 : 0);  // Z, V16, row scales
 };
 
+// All bits set where x is 0, else none.
+__device__ inline uint32_t is_zero(uint32_t x) { return (x < 1u ? x : 1u) - 1u; }
+// The largest value of lanes l, l + 16, l + 32, l + 48 (the same for all l): uniform.
+__device__ inline uint32_t max_over_q(uint32_t x) {
+#pragma unroll
+  for (int d = 16; d < 64; d <<= 1) {
+    const uint32_t y = (uint32_t)__shfl_xor((int)x, d, 64);
+    x = x > y ? x : y;
+  }
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+}
+
 // RANK_MAJOR: a lane ends up with 4 columns of one rank; else with 4 ranks of one column.
 template <class T, int R, bool RANK_MAJOR>
 __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, int* lds_lo, int* lds_hi, int* lds_count) {
@@ -237,41 +249,43 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
           __builtin_amdgcn_s_barrier();
           issue(lds + (slot == 0 ? STAGES - 1 : slot - 1) * SLOT);
           const uint16_t* now = lds + slot * SLOT;
+          // Powers as bits (positive floats compare like integers; arithmetic instead of conditions, whose many scalar
+          // masks would spill).
           bool mixed = false;  // a row of another power than the sums'
-          float u[8];
+          uint32_t u[8];
           if constexpr (F16T) {
-            const float* sp = reinterpret_cast<const float*>(now + S0) + q * 8;
-            const f32x4 u0 = *reinterpret_cast<const f32x4*>(sp), u1 = *reinterpret_cast<const f32x4*>(sp + 4);
+            const uint32_t* sp = reinterpret_cast<const uint32_t*>(now + S0) + q * 8;
+            const u32x4 u0 = *reinterpret_cast<const u32x4*>(sp), u1 = *reinterpret_cast<const u32x4*>(sp + 4);
+            uint32_t other = 0;
 #pragma unroll
             for (int r = 0; r < 8; ++r) {
               u[r] = r < 4 ? u0[r & 3] : u1[r & 3];
-              mixed = mixed || (u[r] > 0.f && u[r] != unit);
+              other |= (u[r] ^ __float_as_uint(unit)) & ~is_zero(u[r]);
             }
-            mixed = __ballot(mixed) != 0;
+            mixed = __ballot(other != 0) != 0;
           }
           // Once, or power by power, largest first; rows of zeros (and past the segment) go with the first.
-          float above = __builtin_inff();
+          uint32_t later = 0;
           u32x4 mask = {~0u, ~0u, ~0u, ~0u};
           do {
             if (mixed) {
-              float next = 0.f;
+              uint32_t next = 0;
 #pragma unroll
-              for (int r = 0; r < 8; ++r) next = fmaxf(next, u[r] < above ? u[r] : 0.f);
-              next = fmaxf(next, shfl_xor(next, 16));
-              next = fmaxf(next, shfl_xor(next, 32));
-              next = __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(next)));
-              if (!(next > 0.f)) break;
-              if (next != unit) fold(next);
+              for (int r = 0; r < 8; ++r) next = next > u[r] ? next : u[r];
+              next = max_over_q(next);
+              if (next == 0) break;
+              if (next != __float_as_uint(unit)) fold(__uint_as_float(next));
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
-                mask[w] = 0;
+                uint32_t m[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                  const float ur = u[2 * w + h];
-                  if (ur == next || (ur == 0.f && above > 3.4e38f)) mask[w] |= 0xffffu << (16 * h);
+                  m[h] = is_zero(u[2 * w + h] ^ next) | is_zero(u[2 * w + h] | later);
+                  u[2 * w + h] &= ~m[h];  // done
                 }
+                mask[w] = (m[0] & 0xffffu) | (m[1] & 0xffff0000u);
               }
-              above = next;
+              later = 1;
             }
             multiply(now, mask);
           } while (mixed);
