@@ -87,8 +87,10 @@ template <class T, int R>
 struct LoraGradShape {
   static constexpr bool F16T = T::kMaxFinite < 1e6f;
   static constexpr int ROWS = kDenseK, COLS = kLoraGradCols, QC = 2 * R, JT = R < 16 ? 1 : R / 16;
-  static constexpr int STAGES = R == 64 ? 3 : 4;  // two workgroups per CU
+  static constexpr int STAGES = R >= 32 ? 3 : 4;
   static constexpr int B0 = COLS * ROWS, S0 = B0 + QC * ROWS, SLOT = S0 + (F16T ? 128 : 0);  // Z, V16, row scales
+  static constexpr int LIST = 2 * kThreads + kWaves;  // ints: the segments of one window
+  static_assert(2 * (STAGES * SLOT * 2 + LIST * 4) <= 160 << 10, "two workgroups per CU");
 };
 
 // All bits set where x is 0, else none.
