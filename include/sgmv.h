@@ -488,11 +488,17 @@ sgmv_status_t sgmv_base_lora_apply_partial(const sgmv_problem_t* problem, const 
  * sgmv_dense_lora_backward.
  *
  * Precision: sums are fp32; every output is rounded once, from fp32 (H from
- * the unrounded G and U).  X @ A_k and dY @ B_k^T stay fp32.  The gated backward
+ * the unrounded G and U).  X @ A_k and dY @ B_k^T are summed in fp32 and, where the
+ * matrix cores multiply them further, held as two 16-bit halves (16 significant
+ * bits in bf16; 22 in fp16, or 2^-21 of the row's largest value where that is
+ * more, whatever the row's magnitude).  The gated backward
  * rounds dG and dU to the 16-bit format once, since they are operands of the matrix
  * cores (where that would be few values, up to 128 rows and 2^18 values of dG, it
- * carries them as two 16-bit halves each instead).  Results do not depend on
- * timing: no atomics, sums in a fixed order.
+ * carries them as two 16-bit halves each instead).  In fp16 a row of both is
+ * kept divided by a power of two of its own, so that neither 65504 nor
+ * denormals cut them: a value keeps its 11 bits down to 2^-21 of the row's
+ * largest |dH| max(1.13 |U|, |G|), and in dW, where rows meet, down to 2^-21 of the largest
+ * row's.  Results do not depend on timing: no atomics, sums in a fixed order.
  *
  * Gradients (sgmv_projection_grad_t): each of dX, dW, dA_ptrs, dB_ptrs may be
  * NULL (not wanted), and so may entries of the dA and dB tables and the whole

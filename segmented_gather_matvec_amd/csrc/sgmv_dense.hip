@@ -206,6 +206,76 @@ __device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x
   }
 }
 
+// The largest and the smallest of the powers of rows 0 .. n-1 but for rows of zeros (kZeroRow and its opposite: all are).
+template <int WAVES>
+__device__ inline void power_range(const int8_t* power, int n, int* lds, int& top, int& low) {
+  const int t = threadIdx.x;
+  top = kZeroRow;
+  low = -kZeroRow;
+  for (int i = t * 4; i < n; i += WAVES * 64 * 4) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(power + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int b = (int8_t)(w >> (8 * e));
+      const bool row = i + e < n && b != kZeroRow;
+      top = row && b > top ? b : top;
+      low = row && b < low ? b : low;
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int a = __shfl_xor(top, d, 64), b = __shfl_xor(low, d, 64);
+    top = a > top ? a : top;
+    low = b < low ? b : low;
+  }
+  if ((t & 63) == 0) {
+    lds[t >> 6] = top;
+    lds[WAVES + (t >> 6)] = low;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) {
+    top = lds[w] > top ? lds[w] : top;
+    low = lds[WAVES + w] < low ? lds[WAVES + w] : low;
+  }
+  __syncthreads();  // lds may be filled
+  top = __builtin_amdgcn_readfirstlane(top);
+  low = __builtin_amdgcn_readfirstlane(low);
+}
+
+// The fp16 factor 2^(8 (b - top)) of a row with power b <= top, in the low half (0 below the smallest denormal).
+__device__ inline uint32_t power_factor(int b, int top) {
+  const uint32_t d = (uint32_t)(top - b);
+  const uint32_t f = (uint32_t)(0x000101001c003c00ull >> (16 * (d & 3))) & 0xffffu;
+  return d < 4 ? f : 0u;
+}
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x8 __attribute__((ext_vector_type(8)));
+typedef const __attribute__((address_space(4))) u32x8* const_u32x8_ptr;  // read by scalar loads: no vector load to wait for
+// Brings operands of contraction rows row .. row + 31 (lane q: rows 8 q .. 8 q + 7, two to a word) to the power top.
+template <int TN>
+__device__ inline void bring_to_power(const int8_t* power, int row, int top, int q, u32x4 (&v)[TN]) {
+  const u32x8 words = *(const_u32x8_ptr)(power + row);
+  const auto word = [&](int e) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)words[e]); };  // (keeps the load scalar)
+  const uint32_t odd = 0u - (uint32_t)(q & 1), upper = 0u - (uint32_t)(q >> 1);
+  uint32_t f[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = (word(h) & ~odd) | (word(2 + h) & odd), hi = (word(4 + h) & ~odd) | (word(6 + h) & odd);
+    const uint32_t w = (lo & ~upper) | (hi & upper);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      f[2 * h + e] = power_factor((int8_t)(w >> (16 * e)), top) | (power_factor((int8_t)(w >> (16 * e + 8)), top) << 16);
+  }
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const uint32_t x = v[j][w];  // (a bit cast of the vector's element itself would take element 0)
+      v[j][w] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, x) * __builtin_bit_cast(f16x2, f[w]));
+    }
+}
+
 template <class T>
 __device__ inline u32x2 round4(const f32x4& v) {
   return u32x2{(uint32_t)T::round(v[0]) | ((uint32_t)T::round(v[1]) << 16),
@@ -277,6 +347,15 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
     }
   };
 
+  // fp16 dG and dU come with a power of two per row.  dX puts it back row by row.  In dW rows meet: where
+  // their powers differ, all are brought to the largest on their way from LDS to the matrix cores (a row's values keep
+  // their bits down to 2^-21 .. 2^-28 of the largest row's largest value, and count down to 2^-32 .. 2^-40 of it).
+  constexpr bool POWERS = T::kMaxFinite < 1e6f && PAIRS;
+  int top = 0, low = 0;
+  if constexpr (POWERS && MODE == kDenseDw) {
+    if (p.row_power != nullptr) power_range<S::NW>(p.row_power, p.K, reinterpret_cast<int*>(ring), top, low);
+  }
+
   f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -318,6 +397,12 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
       for (int s = 0; s < TURN; ++s) {
         constexpr int kAhead = kPerStep * (STAGES - 2);
         const int slot = s % STAGES, next = (s + 1) % STAGES;
+        if constexpr (POWERS && MODE == kDenseDw) {
+          if (low < top) {
+            const int in_pair = step + s < kt ? step + s : step + s - kt;  // (steps past the end hold zeros)
+            bring_to_power(p.row_power, (in_pair < kt ? in_pair : kt - 1) * kDenseK, top, q, b[s % 2]);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < HB; ++i) multiply(i, b[s % 2]);
         wait_loads_and_lds<kAhead>();
@@ -341,6 +426,22 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
   // Epilogue.  acc[i][j][e]: row m0 + (wm TM + i) 16 + ml, column 16-tile j, 4 q + e.
   const int mw = m0 + wm * TM * 16;
   const int cw = n0 + wn * TNP * 16;
+  if constexpr (POWERS) {
+    if (p.row_power != nullptr) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
+        float w = power_of(top);
+        if constexpr (MODE == kDenseDx) {
+          const int m = mw + i * 16 + ml;
+          w = m < p.M ? power_of(p.row_power[m < p.meta.n_rows ? m : m - p.meta.n_rows]) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] *= w;
+      }
+    }
+  }
   if (MODE != kDenseDw && p.term_in_tile && g == 0) {
     if constexpr (S::GATED) {
       if (p.term[0].V16 != nullptr) add_term<T, MODE, S, 0>(p, p.term[0], acc, ring, m0, n0, wave, lane);
@@ -412,6 +513,8 @@ __device__ inline ThinParams pick(const ThinParams& a, const ThinParams& b, bool
   t.to_planes = a.to_planes;
   t.sum_planes = 0;
   t.row_k = first ? a.row_k : nullptr;  // the same for both
+  t.z_power = nullptr;
+  t.q_power = nullptr;
   t.K = a.K;
   t.rank = a.rank;
   t.transposed = 0;

@@ -52,6 +52,8 @@ struct DenseParams {
   int32_t term_in_tile;  // 1: split 0 of every tile adds the LoRA term
   int32_t v_planes;      // partial planes of term[].V that the epilogue sums
   const int32_t* row_k;  // [n_rows] LoRA of each covered row (see ThinParams); null: the epilogue searches
+  const int8_t* row_power;  // null, or [n_rows] (32-byte aligned, readable to the next 32) the powers that the rows of
+                            // dX's A (its n_rows further rows too), or dW's B, are divided by (power_of)
   int64_t plane_stride;  // floats between planes of one projection's output (M * N)
   const uint16_t* A[2];
   const uint16_t* B[2];
@@ -75,6 +77,8 @@ struct ThinParams {
   int32_t to_planes;      // 1: partial planes (ksplit > 1, or a sum over several products)
   int32_t sum_planes;     // planes from `planes` on that make V (0: another product's sum has them)
   int32_t* row_k;         // null, or [n_rows] the LoRA of each covered row, written
+  const int8_t* z_power;  // null, or [n_rows] the powers that Z's rows are divided by (power_of): V gets them back
+  const int8_t* q_power;  // null, or [n_rows] powers that row_scale takes on, for a product of V16 with such rows
   int32_t K, rank, transposed;
   int32_t units, direct;  // units of <= kThinRows rows of one segment
   int32_t ksplit, kc;     // K per split, a multiple of 32
@@ -114,9 +118,10 @@ struct LoraGradParams {
 // count gradients (at most 4) in one launch; the plane sums and the zeros of unused LoRAs follow where there are any.
 hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipStream_t stream);
 
-// dG = dH * U * act'(G), dU = dH * act(G) (n values each), rounded once to the 16-bit format, or (halves) as hi
-// halves followed by lo halves.
+// dG = dH * U * act'(G), dU = dH * act(G) ([n, F] each), rounded once to the 16-bit format, or (halves) as hi
+// halves followed by lo halves.  fp16: every row divided by its power_of(row_power[i]), written.
 hipError_t launch_gate_backward(int dtype, int act, bool halves, const uint16_t* G, const uint16_t* U,
-                                const uint16_t* dH, uint16_t* dG, uint16_t* dU, int64_t n, hipStream_t stream);
+                                const uint16_t* dH, uint16_t* dG, uint16_t* dU, int8_t* row_power, int32_t n, int32_t F,
+                                hipStream_t stream);
 
 }  // namespace sgmv

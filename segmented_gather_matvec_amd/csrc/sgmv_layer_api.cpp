@@ -30,6 +30,7 @@ struct Call {
   int32_t act;
 
   float* at(size_t off) const { return reinterpret_cast<float*>(ws + off); }
+  int8_t* row_power() const { return plan.row_powers ? reinterpret_cast<int8_t*>(ws + plan.row_power_off) : nullptr; }
 };
 
 // Checks shared by the four entry points.
@@ -86,6 +87,8 @@ void thin_params(const Call& c, bool up, const void* const* Z, bool full, bool h
     t[i].direct = plan.direct;
     t[i].ksplit = plan.ksplit;
     t[i].kc = plan.kc;
+    t[i].z_power = up ? c.row_power() : nullptr;
+    t[i].q_power = up ? nullptr : c.row_power();  // V meets dY in dB
     t[i].meta = c.meta;
   }
 }
@@ -127,6 +130,7 @@ sgmv::DenseParams dense_params(const Call& c, const DensePlan& d, int64_t M, int
   q.plane_stride = M * N;
   q.v_planes = 1;
   q.planes = c.at(c.plan.planes_off);
+  q.row_power = c.row_power();
   q.meta = c.meta;
   return q;
 }
@@ -379,7 +383,7 @@ sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* p, const void* X, c
                     reinterpret_cast<uint16_t*>(c.at(plan.gate_off[1]))};
   if (p->n_rows > 0 &&
       sgmv::launch_gate_backward(p->dtype, act, plan.halves > 1, half(gate->Y), half(up->Y), half(dH), d[0], d[1],
-                                 (int64_t)p->n_rows * p->h_out, c.stream) != hipSuccess)
+                                 c.row_power(), p->n_rows, p->h_out, c.stream) != hipSuccess)
     return SGMV_ERR_HIP;
   const void* dY[2] = {d[0], d[1]};
   return backward(c, dY, dX, g, accumulate);

@@ -173,8 +173,11 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
       }
     }
   }
-  if (op == SGMV_GATED_BACKWARD)
+  if (op == SGMV_GATED_BACKWARD) {
     for (int i = 0; i < 2; ++i) l.gate_off[i] = take((size_t)n * l.halves * p.h_out * 2);
+    l.row_powers = p.dtype == SGMV_F16;
+    if (l.row_powers) l.row_power_off = take((size_t)n);
+  }
   const int64_t M = n * l.halves, N = back ? p.h_in : p.h_out;
   const bool in_tile = l.lora && tiles_add_term(p, back, l.projections, N);
   const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK);

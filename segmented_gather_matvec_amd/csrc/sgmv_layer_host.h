@@ -37,7 +37,8 @@ struct LayerPlan {
   // Byte offsets into the workspace.
   // [0][i]: V of projection i, [1][i]: dV; as fp32, as 16-bit halves, the halves' row scales, partial planes.
   size_t v_off[2][2] = {}, half_off[2][2] = {}, row_scale_off[2][2] = {}, thin_off[2][2] = {};
-  size_t gate_off[2] = {0, 0}, row_k_off = 0;
+  bool row_powers = false;  // dG and dU are kept divided by a power of two per row (fp16)
+  size_t gate_off[2] = {0, 0}, row_power_off = 0, row_k_off = 0;
   size_t planes_off = 0;  // partial planes of the dense product, then of the LoRA gradients (never both live)
   size_t total = 0;
 };

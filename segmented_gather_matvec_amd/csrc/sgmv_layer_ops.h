@@ -49,6 +49,11 @@ __device__ inline void split8(const float (&v)[8], u32x4& hi, u32x4& lo) {
   }
 }
 
+// What fp16 dG and dU of a row are divided by: 2^(8 b), b = row_power[i], or kZeroRow (as 0) for a row of zeros.
+__device__ inline float power_of(int b) {
+  return b == kZeroRow ? 0.f : __uint_as_float((uint32_t)(127 + 8 * b) << 23);
+}
+
 // First segment whose end lies beyond row i (num_segs: none), by a 64-ary
 // search over the non-decreasing seg_indptr; uniform over the wave.
 __device__ inline int first_segment_past(const SegMeta& m, int i) {
@@ -78,6 +83,7 @@ __device__ inline int rank_of(const int32_t* ranks, int rank, int k) {
 
 // Activations of the gated block (sgmv_act_t): value and derivative in fp32.
 // silu: g * sig, sig = 1 / (1 + e^-g);  sig * (1 + g * (1 - sig)).
+// Both sigmoids of one exponential that cannot overflow: sig(x) = 1 / (1 + e^-x), sig(-x) = e^-x / (1 + e^-x) for x >= 0.
 // tanh gelu: 0.5 g (1 + t) = g * sig(2z), z = sqrt(2/pi) (g + 0.044715 g^3).
 __device__ inline float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
 __device__ inline float gelu_arg2(float g) {
@@ -87,8 +93,9 @@ __device__ inline float gelu_arg2(float g) {
 __device__ inline float act_value(int act, float g) { return g * sigmoid(act == 0 ? g : gelu_arg2(g)); }
 __device__ inline void act_both(int act, float g, float& value, float& slope) {
   const float z2 = act == 0 ? g : gelu_arg2(g);
-  const float s = sigmoid(z2);
-  const float c = sigmoid(-z2);  // 1 - s without cancellation
+  const float x = expf(-fabsf(z2)), r = 1.f / (1.f + x);
+  const float s = z2 >= 0.f ? r : x * r;
+  const float c = z2 >= 0.f ? x * r : r;  // 1 - s without cancellation
   // d(2z)/dg = 1, or 2 sqrt(2/pi) (1 + 3 * 0.044715 g^2)
   const float d = act == 0 ? 1.f : 1.5957691216057308f * __builtin_fmaf(0.134145f * g, g, 1.f);
   const float t = s * c;  // 0 far out, where d may have overflowed

@@ -23,4 +23,7 @@ constexpr int dense_tile_cols(int t) { return t == kTile128 ? 128 : 256; }
 constexpr int kThinRows = 64;      // rows of one segment per thin-product workgroup
 constexpr int kLoraGradCols = 256; // columns of X or dY per LoRA-gradient workgroup
 
+// fp16 dG and dU of a row are kept divided by 2^(8 b), -kMaxRowPower <= b <= kMaxRowPower; b of a row of zeros.
+constexpr int kMaxRowPower = 15, kZeroRow = -128;
+
 }  // namespace sgmv

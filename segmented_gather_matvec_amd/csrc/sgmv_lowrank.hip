@@ -413,38 +413,132 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBa
 }
 
 // ---------------------------------------------------------------- gated block, elementwise backward
-// Eight values per thread; bound by memory (three reads, two writes: 4096 x 11008 99 us, 4.6 TB/s).  dG and
-// dU are the matrix cores' operands of everything that follows, so they are
+// dG = dH * U * act'(G), dU = dH * act(G).  They are the matrix cores' operands of everything that follows, so they are
 // rounded to the 16-bit format here, once.  HALVES (few rows): kept as hi halves and,
-// n values behind them, lo halves, which go through the same products as further rows: those
+// n F values behind them, lo halves, which go through the same products as further rows: those
 // are bound by reading W then, and the error of a handful of large values does not average out.
+template <class T>
+__device__ inline void gate_slopes(int act, const u32x4& G, const u32x4& U, const u32x4& dH, float (&a)[8],
+                                   float (&b)[8]) {
+  float g[8], u[8], h[8];
+  unpack8<T>(G, g);
+  unpack8<T>(U, u);
+  unpack8<T>(dH, h);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float value, slope;
+    act_both(act, g[e], value, slope);
+    a[e] = h[e] * u[e] * slope;
+    b[e] = h[e] * value;
+  }
+}
 template <class T, bool HALVES>
+__device__ inline void store_slopes(const float (&v)[8], uint16_t* dst, int64_t i, int64_t n8) {
+  if constexpr (HALVES) {
+    u32x4 hi, lo;
+    split8<T>(v, hi, lo);
+    store_vec(dst + i * 8, hi);
+    store_vec(dst + (n8 + i) * 8, lo);
+  } else {
+    store_vec(dst + i * 8, pack8<T>(v));
+  }
+}
+
+// bf16: eight values per thread; bound by memory (three reads, two writes: 2048 x 11008 37 us, 6.1 TB/s, part of them from
+// the Infinity Cache; with two exponentials per value 50 us).
+template <bool HALVES>
 __global__ __launch_bounds__(kThreads) void sgmv_gate_backward_kernel(int act, const uint16_t* G, const uint16_t* U,
                                                                       const uint16_t* dH, uint16_t* dG, uint16_t* dU,
                                                                       int64_t n8) {
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n8; i += (int64_t)gridDim.x * kThreads) {
-    float g[8], u[8], h[8], a[8], b[8];
-    unpack8<T>(load_stream(G + i * 8), g);
-    unpack8<T>(load_stream(U + i * 8), u);
-    unpack8<T>(load_stream(dH + i * 8), h);
+    float a[8], b[8];
+    gate_slopes<BF16>(act, load_stream(G + i * 8), load_stream(U + i * 8), load_stream(dH + i * 8), a, b);
+    store_slopes<BF16, HALVES>(a, dG, i, n8);
+    store_slopes<BF16, HALVES>(b, dU, i, n8);
+  }
+}
+
+// fp16: |dG| may pass 65504 where the gradients do not, and small values' lo and then hi halves run out of denormals. So a
+// row of both is kept divided by a power 2^(8 b) (exact), and the readers put it back.  b brings the row's largest
+// |dH| max(1.13 |U|, |G|) to [2^7, 2^15): no |dG| or |dU| is larger, since |act'| <= 1.13 and |act(g)| <= |g|, and it costs
+// no exponential; a value then keeps its 11 bits down to 2^-21 of it.  TPR threads share a row, or with few rows
+// several workgroups do: each finds the row's power for itself and computes every splits-th piece of TPR eights.
+// A thread's first KEEP eights stay in registers meanwhile, the others are read again.
+template <bool HALVES, int TPR, int KEEP>
+__global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void sgmv_gate_backward_rows_kernel(
+    int act, const uint16_t* G, const uint16_t* U, const uint16_t* dH, uint16_t* dG, uint16_t* dU, int8_t* power,
+    int32_t n, int32_t f8, int32_t splits) {
+  constexpr int ROWS = TPR < kThreads ? kThreads / TPR : 1;  // of a workgroup
+  static_assert(TPR == 64 || ROWS == 1, "a wave or a workgroup per row");
+  __shared__ uint32_t most[TPR / 64];
+  const int t = (int)threadIdx.x % TPR;
+  const int split = (int)blockIdx.x % splits;
+  const int64_t n8 = (int64_t)n * f8;
+  const int64_t first = (int64_t)(blockIdx.x / splits) * ROWS + threadIdx.x / TPR;
+  for (int64_t row = first; row < n; row += (int64_t)(gridDim.x / splits) * ROWS) {
+    const int64_t at = row * f8;
+    u32x4 g[KEEP ? KEEP : 1], u[KEEP ? KEEP : 1], h[KEEP ? KEEP : 1];
+    // Bits of the largest finite magnitude; 1 (the smallest denormal) for what is neither finite nor 0.
+    uint32_t big = 0;
+    const auto see = [&](const u32x4& G8, const u32x4& U8, const u32x4& H8) {
+      float x[8], y[8], z[8];
+      unpack8<F16>(G8, x);
+      unpack8<F16>(U8, y);
+      unpack8<F16>(H8, z);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float value, slope;
-      act_both(act, g[e], value, slope);
-      a[e] = h[e] * u[e] * slope;
-      b[e] = h[e] * value;
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t m = __float_as_uint(fabsf(z[e]) * fmaxf(1.13f * fabsf(y[e]), fabsf(x[e])));
+        const uint32_t f = m < 0x7f800000u ? m : 1u;
+        big = big > f ? big : f;
+      }
+    };
+#pragma unroll
+    for (int c = 0; c < KEEP; ++c) {  // (past the end: the row's last eight again, so that all loads are in flight at once)
+      const int64_t i = at + (c * TPR + t < f8 ? c * TPR + t : f8 - 1);
+      g[c] = load_vec(G + i * 8);
+      u[c] = load_vec(U + i * 8);
+      h[c] = load_vec(dH + i * 8);
     }
-    if constexpr (HALVES) {
-      u32x4 hi, lo;
-      split8<T>(a, hi, lo);
-      store_vec(dG + i * 8, hi);
-      store_vec(dG + (n8 + i) * 8, lo);
-      split8<T>(b, hi, lo);
-      store_vec(dU + i * 8, hi);
-      store_vec(dU + (n8 + i) * 8, lo);
-    } else {
-      store_vec(dG + i * 8, pack8<T>(a));
-      store_vec(dU + i * 8, pack8<T>(b));
+#pragma unroll
+    for (int c = 0; c < KEEP; ++c) see(g[c], u[c], h[c]);
+#pragma unroll 4
+    for (int c = KEEP * TPR; c < f8; c += TPR) {
+      const int64_t i = at + (c + t < f8 ? c + t : f8 - 1);
+      see(load_vec(G + i * 8), load_vec(U + i * 8), load_vec(dH + i * 8));
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const uint32_t y = (uint32_t)__shfl_xor((int)big, d, 64);
+      big = big > y ? big : y;
+    }
+    if constexpr (TPR > 64) {
+      __syncthreads();  // the row before has been read
+      if ((t & 63) == 0) most[t >> 6] = big;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < TPR / 64; ++w) big = big > most[w] ? big : most[w];
+    }
+    int e = ((int)(big >> 23) - 127 - 7) >> 3;
+    e = e < -kMaxRowPower ? -kMaxRowPower : e > kMaxRowPower ? kMaxRowPower : e;
+    const float down = power_of(-e);
+    if (t == 0 && split == 0) power[row] = (int8_t)(big == 0 ? kZeroRow : e);
+    const auto put = [&](const u32x4& G8, const u32x4& U8, const u32x4& H8, int64_t i) {
+      float a[8], b[8];
+      gate_slopes<F16>(act, G8, U8, H8, a, b);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        a[x] *= down;
+        b[x] *= down;
+      }
+      store_slopes<F16, HALVES>(a, dG, i, n8);
+      store_slopes<F16, HALVES>(b, dU, i, n8);
+    };
+#pragma unroll
+    for (int c = 0; c < KEEP; ++c)
+      if (c * TPR + t < f8) put(g[c], u[c], h[c], at + c * TPR + t);
+    for (int c = (KEEP + split) * TPR + t; c < f8; c += splits * TPR) {
+      const int64_t i = at + c;
+      put(load_vec(G + i * 8), load_vec(U + i * 8), load_vec(dH + i * 8), i);
     }
   }
 }
@@ -513,6 +607,16 @@ hipError_t launch_lora_grad_t(const LoraGradParams* p, int count, hipStream_t s)
   return hipGetLastError();
 }
 
+template <bool HALVES, int TPR, int KEEP>
+hipError_t launch_gate_rows(int act, const uint16_t* G, const uint16_t* U, const uint16_t* dH, uint16_t* dG, uint16_t* dU,
+                            int8_t* power, int32_t n, int32_t f8, int32_t splits, hipStream_t s) {
+  constexpr int rows = TPR < kThreads ? kThreads / TPR : 1;
+  const dim3 grid((unsigned)(std::min<int64_t>(((int64_t)n + rows - 1) / rows, 8192) * splits));
+  hipLaunchKernelGGL((sgmv_gate_backward_rows_kernel<HALVES, TPR, KEEP>), grid, dim3(TPR < kThreads ? kThreads : TPR), 0, s,
+                     act, G, U, dH, dG, dU, power, n, f8, splits);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_thin(int dtype, const ThinParams* p, int count, hipStream_t stream) {
@@ -528,19 +632,35 @@ hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipSt
 }
 
 hipError_t launch_gate_backward(int dtype, int act, bool halves, const uint16_t* G, const uint16_t* U,
-                                const uint16_t* dH, uint16_t* dG, uint16_t* dU, int64_t n, hipStream_t stream) {
-  const int64_t n8 = n / 8;
+                                const uint16_t* dH, uint16_t* dG, uint16_t* dU, int8_t* row_power, int32_t n, int32_t F,
+                                hipStream_t stream) {
+  const int f8 = F / 8;
+  const int64_t n8 = (int64_t)n * f8;
   if (n8 <= 0) return hipSuccess;
-  const dim3 grid((unsigned)(n8 < (int64_t)kThreads * 8192 ? (n8 + kThreads - 1) / kThreads : 8192)), block(kThreads);
-  if (dtype == 1 && halves)
-    hipLaunchKernelGGL((sgmv_gate_backward_kernel<BF16, true>), grid, block, 0, stream, act, G, U, dH, dG, dU, n8);
-  else if (dtype == 1)
-    hipLaunchKernelGGL((sgmv_gate_backward_kernel<BF16, false>), grid, block, 0, stream, act, G, U, dH, dG, dU, n8);
-  else if (halves)
-    hipLaunchKernelGGL((sgmv_gate_backward_kernel<F16, true>), grid, block, 0, stream, act, G, U, dH, dG, dU, n8);
-  else
-    hipLaunchKernelGGL((sgmv_gate_backward_kernel<F16, false>), grid, block, 0, stream, act, G, U, dH, dG, dU, n8);
-  return hipGetLastError();
+  if (dtype == 1) {
+    const dim3 grid((unsigned)std::min<int64_t>((n8 + kThreads - 1) / kThreads, 8192));
+    if (halves)
+      hipLaunchKernelGGL((sgmv_gate_backward_kernel<true>), grid, dim3(kThreads), 0, stream, act, G, U, dH, dG, dU, n8);
+    else
+      hipLaunchKernelGGL((sgmv_gate_backward_kernel<false>), grid, dim3(kThreads), 0, stream, act, G, U, dH, dG, dU, n8);
+    return hipGetLastError();
+  }
+  const auto rows = [&](auto launch, int splits) {
+    return launch(act, G, U, dH, dG, dU, row_power, n, f8, splits, stream);
+  };
+  // Threads a row, measured on 11008 columns: up to 63 rows several workgroups a row (1 row 6.6 us; one workgroup 12),
+  // to 512 rows 1024 threads that hold all (256 rows 12.5 us; 256 threads that read twice 21), beyond, 256
+  // threads of up to six eights each (2048 rows 60 us; without rows' powers 55).
+  if (halves || n < 64 || (n <= 512 && f8 <= 256)) {
+    const int pieces = (f8 + kThreads - 1) / kThreads, splits = std::max(1, std::min(pieces, 1024 / n));
+    return halves ? rows(launch_gate_rows<true, 256, 0>, splits) : rows(launch_gate_rows<false, 256, 0>, splits);
+  }
+  if (n <= 512) return rows(launch_gate_rows<false, 1024, 2>, 1);
+  if (f8 <= 256) return rows(launch_gate_rows<false, 64, 4>, 1);
+  if (f8 <= 512) return rows(launch_gate_rows<false, 256, 2>, 1);
+  if (f8 <= 1024) return rows(launch_gate_rows<false, 256, 4>, 1);
+  if (f8 <= 1536) return rows(launch_gate_rows<false, 256, 6>, 1);
+  return rows(launch_gate_rows<false, 512, 6>, 1);
 }
 
 }  // namespace sgmv

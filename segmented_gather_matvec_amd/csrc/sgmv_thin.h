@@ -38,7 +38,15 @@ __device__ inline void store_v(const ThinParams& p, int row, int c, float (&v)[8
     const float down = __uint_as_float((uint32_t)(127 - 16 * b) << 23);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= down;
-    if (c == 0) p.row_scale[row] = any * up;
+    if (c == 0) {
+      float s = any * up;
+      if (p.q_power != nullptr) {
+        // (Clamped far below and beyond anything an fp16 output can show: 0 stands for a row of zeros.)
+        const float w = power_of(p.q_power[row]);
+        s = s > 0.f && w > 0.f ? fminf(fmaxf(s * w, 0x1p-126f), 0x1p126f) : 0.f;
+      }
+      p.row_scale[row] = s;
+    }
   }
   u32x4 hi, lo;
   split8<T>(v, hi, lo);
@@ -135,6 +143,13 @@ __device__ inline void thin_body(const ThinParams& p, int block, uint16_t* lds) 
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c < rk ? res[r * RST + c + e] * scale : 0.f;
+    if constexpr (T::kMaxFinite < 1e6f) {
+      if (p.z_power != nullptr) {
+        const float w = power_of(p.z_power[un.r0 + r]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= w;
+      }
+    }
     if (p.to_planes) {
       float* dst = p.planes + ((int64_t)g * p.meta.n_rows + un.r0 + r) * p.rank + c;
       *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};

@@ -5,9 +5,9 @@ a unit of the row's own, so a row's value is off by h^2 of itself plus 2^-25 of 
 import pytest
 import torch
 
-import segmented_gather_matvec_amd as sg  # noqa: F401  (the library under test)
+import segmented_gather_matvec_amd as sg
 from tests import layer_reference as lr
-from tests.test_gpu_layer import run_dense_back
+from tests.test_gpu_layer import run_dense_back, run_gated_back
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,78 @@ def test_rows_of_zeros_and_of_infinities_among_others():
     others = [i for i in range(c.h_in) if i != 3]
     assert torch.equal(broken[0][1][0][others], grads[0][1][0][others])
     assert not torch.isfinite(broken[0][1][0][3]).any()
+
+
+def gate_backward(c, kind):
+    """dG, dU in 64 bits from the stored G, U and dH, the bounds of the values that the products read, and the unit of
+    the largest row.  A row of both is kept in the unit 2^(8 b) that puts its largest |dH| max(1.13 |U|, |G|) into
+    [2^7, 2^15): rounded once there (h, or h^2 as two halves), or by half of fp16's smallest denormal, 2^-25 units."""
+    h = lr.half_step(c.dtype)
+    g, u, dh = c.proj[0]["G"].double(), c.proj[1]["G"].double(), c.dY.double()
+    a, slope = lr.act(kind, g)
+    dg, du = dh * u * slope, dh * a
+    if c.n <= 128 and c.n * c.h_out <= 2 ** 18:
+        h = h * h
+    eg = 2.0 ** -20 * (dh * u).abs() * 1.13 * (1 + g.abs())
+    eu = 2.0 ** -20 * (dh * g).abs()
+    big = (dh.abs() * torch.maximum(1.13 * u.abs(), g.abs())).amax(1) * (1 + 2.0 ** -20)
+    power = torch.div(torch.frexp(big).exponent - 1 - 7, 8, rounding_mode="floor").clamp(-15, 15)
+    unit = torch.where(big > 0, 2.0 ** (8.0 * power.double()), 0.0)[:, None]
+    return (dg, eg + h * dg.abs() + 2.0 ** -25 * unit), (du, eu + h * du.abs() + 2.0 ** -25 * unit), float(unit.max())
+
+
+MAGNITUDES = {"beyond": [(10, 8)], "small": [(-12, 0)], "both": [(10, 8), (-12, 0), (-4, -6)]}  # of dH and U, as 2^m
+SIZES = {  # n, h_in, h_out: waves or workgroups per row, few rows as halves, rows longer than what a workgroup holds
+    "few": (77, 136, 264), "one": (1, 72, 520), "rows": (300, 136, 264), "wide_few": (20, 136, 2056),
+    "waves": (1100, 72, 1048), "wide": (600, 136, 2056), "wide4": (600, 72, 5000), "wide6": (520, 72, 12280),
+    "wider": (520, 72, 12296), "widest": (515, 16, 26000), "middle": (150, 72, 4200), "widest_few": (20, 72, 16648),
+}
+
+
+@pytest.mark.parametrize("act", [sg.SGMV_ACT_SILU, sg.SGMV_ACT_GELU_TANH])
+@pytest.mark.parametrize("magnitude", sorted(MAGNITUDES))
+@pytest.mark.parametrize("size", sorted(SIZES))
+def test_gated_gradients_beyond_fp16_and_far_below(size, magnitude, act):
+    """dG and dU past 65504, or so small that fp16 would cut them, or both in one batch: gradients that fit come out right."""
+    n, h_in, h_out = SIZES[size]
+    c = lr.Layer(131, "f16", n, h_in, h_out, 16, 3, "mixed", 2, None, True)
+    steps = MAGNITUDES[magnitude]
+    power = torch.tensor([steps[i % len(steps)] for i in range(n)], device="cuda").double()
+    c.dY.copy_((c.dY.double() * 2.0 ** power[:, :1]).half())
+    c.proj[1]["G"].copy_((c.proj[1]["G"].double() * 2.0 ** power[:, 1:]).half())
+    if magnitude != "small":        # outputs of the large rows stay in the format
+        c.X.mul_(2.0 ** -8)
+        for p in c.proj:
+            p["W"].mul_(2.0 ** -8)
+            for k in range(c.P):
+                p["B"][k].mul_(2.0 ** -8)
+    if n > 4:
+        c.dY[n // 2] = 0            # a row of zeros
+    dX, grads = run_gated_back(c, "f16", act)
+    dg, du, top = gate_backward(c, act)
+    ref = bound = 0
+    for i, (p, d) in enumerate(zip(c.proj, (dg, du))):
+        (x, ex), _, _, (w, ew) = lr.backward(c, p, *d)
+        ref, bound = ref + x, bound + ex
+        halves = 2 if n <= 128 and n * h_out <= 2 ** 18 else 1
+        ew = ew + halves * 2.0 ** -25 * top * c.X.double().abs().sum(0)[:, None]     # rows brought to the largest unit
+        check(grads[i][0], w, ew, c.dtype, f"dW[{i}]")
+        for name, got, refs in zip(("dA", "dB"), grads[i][1:3], lora_gradients(c, p, *d)):
+            for k in range(c.P):
+                check(got[k], *refs[k], c.dtype, f"{name}[{i}][{k}]")
+    check(dX, ref, bound, c.dtype, "dX")
+
+
+def test_an_infinite_row_of_the_gated_block_stays_its_own():
+    """An infinite dH reaches its row of dX, its LoRA and dW; other rows and LoRAs keep their values bit for bit."""
+    c = lr.Layer(9, "f16", 200, 136, 264, 16, 2, "none", 2, None, False)
+    c.seg, c.ids = [0, 90, 200], [0, 1]
+    dX, grads = run_gated_back(c, "f16", 0)
+    c.dY[30, 5] = float("inf")
+    broken, other = run_gated_back(c, "f16", 0)
+    rows = [i for i in range(200) if i != 30]
+    assert torch.equal(broken[rows], dX[rows]) and not torch.isfinite(broken[30]).any()
+    for i in range(2):
+        assert torch.equal(other[i][1][1], grads[i][1][1]) and torch.equal(other[i][2][1], grads[i][2][1])
+        columns = [j for j in range(264) if j != 5]
+        assert torch.equal(other[i][0][:, columns], grads[i][0][:, columns])
