@@ -481,8 +481,9 @@ sgmv_status_t sgmv_base_lora_apply_partial(const sgmv_problem_t* problem, const 
  * sgmv_lora_apply (they and the tables may be NULL when num_segs == 0 or max_seg_len == 0).
  *
  * sgmv_projection_t: A_ptrs, B_ptrs, ranks and scales as in
- * sgmv_lora_apply_batched; entries of LoRAs no segment uses are not read, a
- * null A_k or B_k of a used LoRA counts as rank 0.  Y: the output of
+ * sgmv_lora_apply_batched; entries of LoRAs without rows are not used, a
+ * null A_k or B_k of a LoRA with rows counts as rank 0: there is no LoRA term,
+ * and its dA_k and dB_k are not written.  Y: the output of
  * sgmv_dense_lora_apply (written); for sgmv_gated_lora_apply where to store G
  * (U), or NULL; for sgmv_gated_lora_backward the stored G (U), read; not used by
  * sgmv_dense_lora_backward.

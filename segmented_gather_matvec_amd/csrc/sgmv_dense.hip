@@ -111,7 +111,8 @@ __device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x
     int k_l = sm.lora_idx[sl];
     if (k_l < 0 || k_l >= sm.num_loras) k_l = -1;
     const uint64_t e_l = k_l >= 0 ? t.ptrs[k_l] : 0ull;
-    const int r_l = k_l >= 0 && e_l != 0ull ? rank_of(t.ranks, R, k_l) : 0;
+    const uint64_t pair_l = k_l >= 0 ? t.pair[k_l] : 0ull;
+    const int r_l = k_l >= 0 && e_l != 0ull && pair_l != 0ull ? rank_of(t.ranks, R, k_l) : 0;
     const int ns = sm.num_segs - s0 < 64 ? sm.num_segs - s0 : 64;
     int u = 0;
     while (u < ns) {
@@ -282,7 +283,8 @@ __device__ inline u32x2 round4(const f32x4& v) {
                (uint32_t)T::round(v[2]) | ((uint32_t)T::round(v[3]) << 16)};
 }
 
-template <class T, int MODE, class S>
+// TERM: compiled with the LoRA term in the tiles.
+template <class T, int MODE, class S, bool TERM>
 __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* ring) {
   constexpr int STAGES = S::STAGES, TM = S::TM, TN = S::TN, TNP = S::TNP;
   constexpr int B0 = S::BM * kDenseK;  // a slot: A, then B
@@ -442,16 +444,19 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
       }
     }
   }
-  if (MODE != kDenseDw && p.term_in_tile && g == 0) {
-    if constexpr (S::GATED) {
-      if (p.term[0].V16 != nullptr) add_term<T, MODE, S, 0>(p, p.term[0], acc, ring, m0, n0, wave, lane);
-      if (p.term[1].V16 != nullptr) add_term<T, MODE, S, TNP>(p, p.term[1], acc, ring, m0, n0, wave, lane);
-    } else {
-      for (int t = 0; t < (MODE == kDenseDx ? p.pairs : 1); ++t) {
-        const LowRankTerm term{nullptr, t ? p.term[1].V16 : p.term[0].V16,
-                               t ? p.term[1].row_scale : p.term[0].row_scale,
-                               t ? p.term[1].ptrs : p.term[0].ptrs, t ? p.term[1].ranks : p.term[0].ranks};
-        if (term.V16 != nullptr) add_term<T, MODE, S, 0>(p, term, acc, ring, m0, n0, wave, lane);
+  if constexpr (TERM) {
+    if (p.term_in_tile && g == 0) {
+      if constexpr (S::GATED) {
+        if (p.term[0].V16 != nullptr) add_term<T, MODE, S, 0>(p, p.term[0], acc, ring, m0, n0, wave, lane);
+        if (p.term[1].V16 != nullptr) add_term<T, MODE, S, TNP>(p, p.term[1], acc, ring, m0, n0, wave, lane);
+      } else {
+        for (int t = 0; t < (MODE == kDenseDx ? p.pairs : 1); ++t) {
+          const LowRankTerm term{nullptr, t ? p.term[1].V16 : p.term[0].V16,
+                                 t ? p.term[1].row_scale : p.term[0].row_scale,
+                                 t ? p.term[1].ptrs : p.term[0].ptrs, t ? p.term[1].pair : p.term[0].pair,
+                                 t ? p.term[1].ranks : p.term[0].ranks};
+          if (term.V16 != nullptr) add_term<T, MODE, S, 0>(p, term, acc, ring, m0, n0, wave, lane);
+        }
       }
     }
   }
@@ -495,7 +500,7 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
 template <class T, int MODE, class S>
 __global__ __launch_bounds__(S::NW * 64, S::WAVES_PER_SIMD) void sgmv_dense_kernel(DenseParams p) {
   __shared__ __attribute__((aligned(1024))) uint16_t lds[S::STAGES * S::SLOT];
-  dense_body<T, MODE, S>(p, (int)blockIdx.x, lds);
+  dense_body<T, MODE, S, MODE != kDenseDw>(p, (int)blockIdx.x, lds);
 }
 
 // One of two parameter blocks, field by field: a conditional copy of the struct
@@ -512,7 +517,7 @@ __device__ inline ThinParams pick(const ThinParams& a, const ThinParams& b, bool
   t.planes = first ? a.planes : b.planes;
   t.to_planes = a.to_planes;
   t.sum_planes = 0;
-  t.row_k = first ? a.row_k : nullptr;  // the same for both
+  t.row_k = first ? a.row_k : b.row_k;
   t.z_power = nullptr;
   t.q_power = nullptr;
   t.K = a.K;
@@ -538,7 +543,7 @@ __global__ __launch_bounds__(kThreads, S::WAVES_PER_SIMD) void sgmv_dense_thin_k
   __shared__ __attribute__((aligned(1024))) uint16_t lds[RING];
   const int b = (int)blockIdx.x;
   if (b < dense_grid) {
-    dense_body<T, MODE, S>(p, b, lds);
+    dense_body<T, MODE, S, false>(p, b, lds);  // the epilogue adds the term
     return;
   }
   const int x = b - dense_grid;
@@ -634,11 +639,14 @@ __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) 
   const int c = blockIdx.y * kEpilogueCols + lane * 4;
   if (i >= p.M) return;
   const bool terms = !p.term_in_tile && p.meta.num_segs > 0 && p.term[0].V != nullptr;
-  int k = -1, end = 0;
+  int k[NT], end = 0;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) k[t] = -1;
   if (terms && p.row_k != nullptr) {
     // Covered rows are those before the last segment's end.
     end = p.meta.seg_indptr[p.meta.num_segs];
-    k = p.row_k[i];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) k[t] = p.row_k[(int64_t)t * p.meta.n_rows + i];
   }
   const int64_t vs = (int64_t)p.meta.n_rows * p.rank;
   float vx[NT][kBatch];
@@ -659,22 +667,26 @@ __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) 
   for (int n = 0; n < NP; ++n) load_planes(p, n, o, 0, x[n]);
 
   if (terms) {
-    if (p.row_k != nullptr) {
-      k = i < end ? k : -1;
-    } else {
+    if (p.row_k == nullptr) {
       const int s = first_segment_past(p.meta, i);
-      if (s < p.meta.num_segs && p.meta.seg_indptr[s] <= i) k = p.meta.lora_idx[s];
+      if (s < p.meta.num_segs && p.meta.seg_indptr[s] <= i) k[0] = p.meta.lora_idx[s];
+#pragma unroll
+      for (int t = 1; t < NT; ++t) k[t] = k[0];
     }
-    if (k >= p.meta.num_loras) k = -1;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+      if (k[t] >= p.meta.num_loras || (p.row_k != nullptr && i >= end)) k[t] = -1;
   }
-  k = __builtin_amdgcn_readfirstlane(k);
   const uint16_t* E[NT];
+  bool whole[NT];  // both matrices are there (row_k has looked already)
   int rk[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const bool on = k >= 0 && vp[t] != nullptr;
-    E[t] = on ? reinterpret_cast<const uint16_t*>(p.term[t].ptrs[k]) : nullptr;
-    rk[t] = on ? rank_of(p.term[t].ranks, p.rank, k) : 0;
+    k[t] = __builtin_amdgcn_readfirstlane(k[t]);
+    const bool on = k[t] >= 0 && vp[t] != nullptr;
+    E[t] = on ? reinterpret_cast<const uint16_t*>(p.term[t].ptrs[k[t]]) : nullptr;
+    whole[t] = p.row_k != nullptr || (on && p.term[t].pair[k[t]] != 0ull);
+    rk[t] = on ? rank_of(p.term[t].ranks, p.rank, k[t]) : 0;
   }
   u32x2 m[NT][16];
 #pragma unroll
@@ -696,6 +708,7 @@ __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) 
       for (int u = 0; u < kBatch; ++u) v = g0 + u < p.v_planes ? v + vx[t][u] : v;
     }
     lds_v[t][lane] = v;
+    if (!whole[t]) rk[t] = 0;
   }
   __syncthreads();
   if (!col) return;
@@ -764,7 +777,7 @@ hipError_t launch_tile_thin(const DenseParams& p, const ThinParams* t, int count
   using S = DenseShape<MODE, BM, BN, WM, WN, STAGES, WPS>;
   const int64_t total = (int64_t)p.tiles_m * p.tiles_n * p.ksplit;
   const int64_t dense = (total + kXcds - 1) / kXcds * kXcds, thin = (int64_t)t[0].units * t[0].ksplit;
-  if (dense <= 0 || thin <= 0 || dense + thin * count > 0x7fffffff) return hipErrorInvalidValue;
+  if (dense <= 0 || thin <= 0 || dense + thin * count > 0x7fffffff || p.term_in_tile) return hipErrorInvalidValue;
   hipLaunchKernelGGL((sgmv_dense_thin_kernel<T, MODE, S>), dim3((unsigned)(dense + thin * count)), dim3(kThreads), 0, s,
                      p, t[0], t[count - 1], (int)dense, (int)thin);
   return hipGetLastError();

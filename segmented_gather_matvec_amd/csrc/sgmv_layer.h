@@ -27,6 +27,7 @@ struct LowRankTerm {
   const uint16_t* V16;     // [n_rows][2][rank] V's hi, then lo halves, read by the tiles (null: no term)
   const float* row_scale;  // fp16: [n_rows] the power of two that V16's rows are divided by (0: a row of zeros)
   const uint64_t* ptrs;    // [num_loras] -> B_k [r_k, N], or A_k [N, r_k] for dX
+  const uint64_t* pair;    // [num_loras] -> A_k, or B_k for dX: where that is null there is no term either
   const int32_t* ranks;    // null, or rank of each LoRA
 };
 
@@ -51,7 +52,7 @@ struct DenseParams {
   int32_t to_planes;     // 1: fp32 partial planes instead of the outputs (ksplit > 1, or the epilogue adds a term)
   int32_t term_in_tile;  // 1: split 0 of every tile adds the LoRA term
   int32_t v_planes;      // partial planes of term[].V that the epilogue sums
-  const int32_t* row_k;  // [n_rows] LoRA of each covered row (see ThinParams); null: the epilogue searches
+  const int32_t* row_k;  // [term][n_rows] LoRA of each covered row (see ThinParams); null: the epilogue searches
   const int8_t* row_power;  // null, or [n_rows] (32-byte aligned, readable to the next 32) the powers that the rows of
                             // dX's A (its n_rows further rows too), or dW's B, are divided by (power_of)
   int64_t plane_stride;  // floats between planes of one projection's output (M * N)
@@ -76,7 +77,7 @@ struct ThinParams {
   float* planes;          // [ksplit][n_rows][rank], written when to_planes
   int32_t to_planes;      // 1: partial planes (ksplit > 1, or a sum over several products)
   int32_t sum_planes;     // planes from `planes` on that make V (0: another product's sum has them)
-  int32_t* row_k;         // null, or [n_rows] the LoRA of each covered row, written
+  int32_t* row_k;         // null, or [n_rows] the LoRA of each covered row (-1: it lacks this matrix), written
   const int8_t* z_power;  // null, or [n_rows] the powers that Z's rows are divided by (power_of): V gets them back
   const int8_t* q_power;  // null, or [n_rows] powers that row_scale takes on, for a product of V16 with such rows
   int32_t K, rank, transposed;
@@ -106,6 +107,8 @@ struct LoraGradParams {
   const uint16_t* Q;      // [n_rows][2][rank] hi and lo halves (see LowRankTerm)
   const float* row_scale; // fp16: of Q's rows
   const uint64_t* out;    // [num_loras] -> gradient (0: not wanted)
+  const uint64_t* A;      // [num_loras] -> A_k, B_k: a LoRA with rows that lacks one has no gradient
+  const uint64_t* B;
   const int32_t* ranks;
   float* planes;          // [nsplit][num_loras][C][rank] or [nsplit][num_loras][rank][C] (nsplit > 1)
   int32_t C, rank, rank_major;  // rank_major: stored [r_k, C]

@@ -135,7 +135,7 @@ sgmv::DenseParams dense_params(const Call& c, const DensePlan& d, int64_t M, int
   return q;
 }
 
-sgmv::LowRankTerm term(const Call& c, int i, bool up, const void* ptrs) {
+sgmv::LowRankTerm term(const Call& c, int i, bool up) {
   sgmv::LowRankTerm t{};
   if (c.plan.out.term_in_tile) {
     t.V16 = reinterpret_cast<const uint16_t*>(c.at(c.plan.half_off[up][i]));
@@ -143,7 +143,8 @@ sgmv::LowRankTerm term(const Call& c, int i, bool up, const void* ptrs) {
   } else {
     t.V = c.at(c.plan.v_off[up][i]);
   }
-  t.ptrs = table(ptrs);
+  t.ptrs = table(up ? c.proj[i]->A_ptrs : c.proj[i]->B_ptrs);
+  t.pair = table(up ? c.proj[i]->B_ptrs : c.proj[i]->A_ptrs);
   t.ranks = c.proj[i]->ranks;
   return t;
 }
@@ -171,7 +172,7 @@ sgmv_status_t forward(const Call& c, void* const* out) {
   q.A[0] = half(c.X);
   for (int i = 0; i < c.np; ++i) {
     q.B[i] = half(c.W[i]);
-    if (c.plan.lora) q.term[i] = term(c, i, false, c.proj[i]->B_ptrs);
+    if (c.plan.lora) q.term[i] = term(c, i, false);
   }
   for (int i = 0; i < (gated ? 3 : 1); ++i) q.out[i] = static_cast<uint16_t*>(out[i]);
   if (!c.plan.one_launch) return run_dense(c, mode, c.plan.out, q);
@@ -181,7 +182,7 @@ sgmv_status_t forward(const Call& c, void* const* out) {
   q.row_k = row_k;
   q.v_planes = c.plan.down.ksplit;
   for (int i = 0; i < c.np; ++i) {
-    t[i].row_k = row_k;
+    t[i].row_k = row_k + (size_t)i * c.p.n_rows;
     if (q.v_planes > 1) q.term[i].V = t[i].planes;
   }
   if (sgmv::launch_dense_thin(c.p.dtype, mode, c.plan.out.cfg, q, t, c.np, c.stream) != hipSuccess) return SGMV_ERR_HIP;
@@ -223,7 +224,7 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
     for (int i = 0; i < c.np; ++i) {
       q.A[i] = half(dY[i]);
       q.B[i] = half(c.W[i]);
-      if (c.plan.lora) q.term[i] = term(c, i, true, c.proj[i]->A_ptrs);
+      if (c.plan.lora) q.term[i] = term(c, i, true);
     }
     q.out[0] = static_cast<uint16_t*>(dX);
     const sgmv_status_t st = run_dense(c, sgmv::kDenseDx, c.plan.out, q, c.plan.halves);
@@ -261,6 +262,8 @@ sgmv_status_t backward(const Call& c, const void* const* dY, void* dX, const sgm
       e.Q = reinterpret_cast<const uint16_t*>(c.at(c.plan.half_off[!b][i]));
       e.row_scale = c.at(c.plan.row_scale_off[!b][i]);
       e.out = table(out);
+      e.A = table(c.proj[i]->A_ptrs);
+      e.B = table(c.proj[i]->B_ptrs);
       e.ranks = c.proj[i]->ranks;
       e.planes = planes;
       if (nsplit > 1) planes += (size_t)nsplit * c.p.num_loras * C * c.p.rank;

@@ -187,7 +187,7 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile) || l.halves > 1;
   // (The large tiles' workgroups are too big to share a launch with.)
   l.one_launch = l.lora && !back && l.out.to_planes && !in_tile && l.out.cfg > sgmv::kTile192;
-  if (l.one_launch) l.row_k_off = take((size_t)n * sizeof(int32_t));
+  if (l.one_launch) l.row_k_off = take((size_t)n * l.projections * sizeof(int32_t));
   if (l.out.to_planes) l.out.plane_bytes = (size_t)l.out.ksplit * M * N * cols * sizeof(float);
   size_t area = l.out.plane_bytes;
   if (back) {

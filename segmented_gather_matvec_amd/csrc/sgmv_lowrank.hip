@@ -301,6 +301,7 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
   fold(0.f);
   // A LoRA without rows: zeros, written by split 0, or what it has when gradients accumulate.
   if (!any && (p.accumulate || z > 0)) return;
+  if (any && (p.A[k] == 0 || p.B[k] == 0)) return;
   const bool planes = p.nsplit > 1 && any;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -379,7 +380,7 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBa
     seen = __syncthreads_or(same) || seen;
   }
   const bool zeros = !seen && p.by_segment && !p.accumulate;
-  if (!zeros && (!rows || p.nsplit <= 1)) return;
+  if (!zeros && (!rows || p.nsplit <= 1 || p.A[k] == 0 || p.B[k] == 0)) return;
   const int64_t n = (int64_t)p.C * rk;
   const int64_t stride = (int64_t)p.meta.num_loras * p.C * R;
   constexpr int kBatch = 8;  // planes in flight

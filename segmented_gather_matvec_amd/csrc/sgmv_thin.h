@@ -92,7 +92,7 @@ __device__ inline void thin_body(const ThinParams& p, int block, uint16_t* lds) 
   const int k1 = p.K < k0 + p.kc ? p.K : k0 + p.kc;
   const int steps = rk > 0 ? (k1 - k0 + 2 * kDenseK - 1) / (2 * kDenseK) : 0;
 
-  if (p.row_k != nullptr && g == 0 && t < un.L) p.row_k[un.r0 + t] = un.k;
+  if (p.row_k != nullptr && g == 0 && t < un.L) p.row_k[un.r0 + t] = D != nullptr ? un.k : -1;
 
   f32x4 acc[JT];
 #pragma unroll
