@@ -513,14 +513,20 @@ sgmv_status_t sgmv_base_lora_apply_partial(const sgmv_problem_t* problem, const 
  * `stream`; the calls can be captured into a graph.  n_rows = 0: the forward
  * calls do nothing, the backward calls write zero gradients (accumulate = 0).  Errors
  * as for sgmv_lora_apply; SGMV_ERR_INVALID_ARG for an act, op or accumulate
- * outside its values. */
+ * outside its values.  The problem is checked for its shape, format and rank and
+ * for the limits below, not for those of sgmv_check_problem that other
+ * kernels set. */
 typedef enum sgmv_act {
   SGMV_ACT_SILU = 0,      /* g / (1 + e^-g) */
   SGMV_ACT_GELU_TANH = 1  /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
 } sgmv_act_t;
 
-/* Most rows a layer call takes; more give SGMV_ERR_UNSUPPORTED. */
+/* Most rows a layer call takes, and most blocks of up to 64 rows of one segment
+ * (num_segs where max_seg_len <= 64, else the smaller of num_segs *
+ * ceil(max_seg_len / 64) and ceil(n_rows / 64) + num_segs); more give
+ * SGMV_ERR_UNSUPPORTED. */
 #define SGMV_MAX_LAYER_ROWS (1 << 30)
+#define SGMV_MAX_LAYER_UNITS ((1 << 24) - 1)
 
 /* Entry point a workspace is for. */
 typedef enum sgmv_layer_op {

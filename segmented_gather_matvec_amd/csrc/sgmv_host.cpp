@@ -14,8 +14,8 @@ namespace {
 
 int pick_rb(int max_seg_len) { return max_seg_len <= 1 ? 1 : (max_seg_len <= 4 ? 4 : 16); }
 
-// Units of at most `rows` rows of one segment: one per segment when every
-// segment fits one block (direct), else an upper bound from max_seg_len.
+}  // namespace
+
 int64_t units_for(const sgmv_problem_t& p, int rows, int* direct) {
   if (p.max_seg_len <= rows) {
     *direct = 1;
@@ -25,7 +25,17 @@ int64_t units_for(const sgmv_problem_t& p, int rows, int* direct) {
   return std::min<int64_t>((int64_t)p.num_segs * ceil_div(p.max_seg_len, rows), ceil_div(p.n_rows, rows) + p.num_segs);
 }
 
-}  // namespace
+sgmv_status_t check_shape(const sgmv_problem_t& p) {
+  if (p.n_rows < 0 || p.h_in <= 0 || p.h_out <= 0 || p.num_segs < 0 || p.num_loras < 0 || p.max_seg_len < 0 ||
+      p.max_seg_len > p.n_rows)
+    return SGMV_ERR_INVALID_ARG;
+  if (p.num_segs > 0 && p.num_loras < 1) return SGMV_ERR_INVALID_ARG;
+  if (p.dtype != SGMV_F16 && p.dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
+  if (!rank_supported(p.rank)) return SGMV_ERR_UNSUPPORTED;
+  if (p.h_in % 8 != 0 || p.h_out % 8 != 0) return SGMV_ERR_UNSUPPORTED;
+  if (p.h_in > SGMV_MAX_HIDDEN || p.h_out > SGMV_MAX_HIDDEN) return SGMV_ERR_UNSUPPORTED;
+  return SGMV_OK;
+}
 
 VecPlan plan_vec(const sgmv_problem_t& p, int64_t target_wgs) {
   VecPlan v;
@@ -312,16 +322,10 @@ sgmv_status_t sgmv_build_segments(const int32_t* req_lora, int32_t n, int32_t nu
 }
 
 sgmv_status_t sgmv_check_problem(const sgmv_problem_t* p) {
-  if (!p) return SGMV_ERR_INVALID_ARG;
-  if (p->n_rows < 0 || p->h_in <= 0 || p->h_out <= 0 || p->num_segs < 0 || p->num_loras < 0 ||
-      p->max_seg_len < 0 || p->max_seg_len > p->n_rows || p->splits < 0)
+  if (!p || p->splits < 0 || p->variant < SGMV_VARIANT_AUTO || p->variant > SGMV_VARIANT_MFMA)
     return SGMV_ERR_INVALID_ARG;
-  if (p->num_segs > 0 && p->num_loras < 1) return SGMV_ERR_INVALID_ARG;
-  if (p->variant < SGMV_VARIANT_AUTO || p->variant > SGMV_VARIANT_MFMA) return SGMV_ERR_INVALID_ARG;
-  if (p->dtype != SGMV_F16 && p->dtype != SGMV_BF16) return SGMV_ERR_UNSUPPORTED;
-  if (!rank_supported(p->rank)) return SGMV_ERR_UNSUPPORTED;
-  if (p->h_in % 8 != 0 || p->h_out % 8 != 0) return SGMV_ERR_UNSUPPORTED;
-  if (p->h_in > SGMV_MAX_HIDDEN || p->h_out > SGMV_MAX_HIDDEN) return SGMV_ERR_UNSUPPORTED;
+  const sgmv_status_t st = check_shape(*p);
+  if (st != SGMV_OK) return st;
   if (p->variant == SGMV_VARIANT_MFMA && !sgmv::mfma_supported(p->rank)) return SGMV_ERR_UNSUPPORTED;
   const VecPlan v = plan_vec(*p, kTargetWorkgroups);
   if (2 * v.num_units > kCounterSlots) return SGMV_ERR_UNSUPPORTED;

@@ -29,6 +29,12 @@ inline bool nothing_to_do(const sgmv_problem_t& p) {
   return p.num_segs == 0 || p.n_rows == 0 || p.max_seg_len == 0;
 }
 
+// The part of sgmv_check_problem that does not depend on a kernel family: sizes, format, rank.
+sgmv_status_t check_shape(const sgmv_problem_t& p);
+// Units of at most `rows` rows of one segment: one per segment when every
+// segment fits one block (direct), else an upper bound from max_seg_len.
+int64_t units_for(const sgmv_problem_t& p, int rows, int* direct);
+
 // Plan of one vector-kernel launch (split-K shrink or expand).
 struct VecPlan {
   int rb = 1;

@@ -114,6 +114,7 @@ struct LoraGradParams {
   int32_t C, rank, rank_major;  // rank_major: stored [r_k, C]
   int32_t nsplit;
   int32_t turns;          // of the sum kernel (set by the launch)
+  int32_t first, last;    // segments or LoRAs first .. last - 1 are this launch's (set by the launch)
   int32_t by_segment;     // 1 (fewer segments than LoRAs): a workgroup per segment that is its LoRA's first
   int32_t accumulate;
   SegMeta meta;

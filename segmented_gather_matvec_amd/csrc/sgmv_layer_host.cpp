@@ -106,14 +106,7 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
 // products: that share the launch; summed: whose planes make one V.
 ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products, int summed) {
   ThinPlan t;
-  if (p.max_seg_len <= sgmv::kThinRows) {
-    t.units = p.num_segs;
-    t.direct = 1;
-  } else {
-    t.direct = 0;
-    t.units = (int)std::min<int64_t>((int64_t)p.num_segs * ceil_div(p.max_seg_len, sgmv::kThinRows),
-                                     ceil_div(p.n_rows, sgmv::kThinRows) + p.num_segs);
-  }
+  t.units = (int)units_for(p, sgmv::kThinRows, &t.direct);
   // About four workgroups per CU, each of at least 256 contraction steps.
   const int64_t want = ceil_div(1024, std::max<int64_t>(1, (int64_t)t.units * products));
   const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(want, ceil_div(K, 256)));
@@ -143,8 +136,13 @@ int plan_grad_split(const sgmv_problem_t& p, int64_t C, int products) {
 }  // namespace
 
 sgmv_status_t check_layer(const sgmv_problem_t* p) {
-  const sgmv_status_t st = sgmv_check_problem(p);
-  return st == SGMV_OK && p->n_rows > SGMV_MAX_LAYER_ROWS ? SGMV_ERR_UNSUPPORTED : st;
+  if (!p) return SGMV_ERR_INVALID_ARG;
+  const sgmv_status_t st = check_shape(*p);
+  if (st != SGMV_OK) return st;
+  int direct;
+  if (p->n_rows > SGMV_MAX_LAYER_ROWS || (!nothing_to_do(*p) && units_for(*p, sgmv::kThinRows, &direct) > SGMV_MAX_LAYER_UNITS))
+    return SGMV_ERR_UNSUPPORTED;
+  return SGMV_OK;
 }
 
 LayerPlan plan_layer(const sgmv_problem_t& p, int op) {

@@ -45,7 +45,8 @@ struct LayerPlan {
 
 inline bool layer_gated(int op) { return op == SGMV_GATED_FORWARD || op == SGMV_GATED_BACKWARD; }
 inline bool layer_backward(int op) { return op == SGMV_DENSE_BACKWARD || op == SGMV_GATED_BACKWARD; }
-// sgmv_check_problem, and the rows that the tiles' 32-bit row numbers reach.
+// The shape's checks, the rows that the tiles' 32-bit row numbers reach, and the units that one launch holds (a
+// workgroup each; a launch has fewer than 2^32 threads).
 sgmv_status_t check_layer(const sgmv_problem_t* p);
 LayerPlan plan_layer(const sgmv_problem_t& p, int op);
 

@@ -115,15 +115,15 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
   constexpr int LZ = COLS / 16 / kWaves, LQ = QC / 16 < kWaves ? 1 : QC / 16 / kWaves;
   constexpr int kPerStep = LZ + LQ + (F16T ? 1 : 0);
   const int ctiles = (p.C + COLS - 1) / COLS;
-  const int item = (int)blockIdx.x / ctiles;
-  if (item >= (p.by_segment ? p.meta.num_segs : p.meta.num_loras) || (int)blockIdx.z >= p.nsplit) return;
+  const int tile = (int)blockIdx.x % ctiles, item = p.first + (int)blockIdx.x / ctiles;
+  if (item >= p.last || (int)blockIdx.z >= p.nsplit) return;
   const int k = p.by_segment ? p.meta.lora_idx[item] : item;
   if (k < 0 || k >= p.meta.num_loras) return;
   const int t = threadIdx.x;
   const int lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int q = lane >> 4, ml = lane & 15;
-  const int c0 = ((int)blockIdx.x - item * ctiles) * COLS;
+  const int c0 = tile * COLS;
   const int z = (int)blockIdx.z;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out[k]);
   const int rk = rank_of(p.ranks, R, k);
@@ -363,8 +363,9 @@ template <class T>
 __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBatch batch) {
   const LoraGradParams& p = batch.p[blockIdx.y];
   const int64_t blocks = sum_blocks(p.C, p.rank, p.turns);
-  const int k = (int)(blockIdx.x / blocks);
-  if (k >= p.meta.num_loras) return;
+  const int k = p.first + (int)(blockIdx.x / blocks);
+  const int64_t block = blockIdx.x % blocks;
+  if (k >= p.last) return;
   const int R = p.rank;
   uint16_t* out = reinterpret_cast<uint16_t*>(p.out[k]);
   const int rk = rank_of(p.ranks, R, k);
@@ -386,7 +387,7 @@ __global__ __launch_bounds__(kThreads) void sgmv_lora_grad_sum_kernel(LoraGradBa
   constexpr int kBatch = 8;  // planes in flight
   const int planes = zeros ? 0 : p.nsplit;
   for (int turn = 0; turn < p.turns; ++turn) {
-    const int64_t o = (((blockIdx.x - k * blocks) * p.turns + turn) * kThreads + threadIdx.x) * 4;
+    const int64_t o = ((block * p.turns + turn) * kThreads + threadIdx.x) * 4;
     if (o >= n) return;  // o: of the stored gradient
     // Planes hold [C][rank] or [rank][C]; the stored [C, r_k] has its own row length.
     const float* pl = p.planes + (int64_t)k * p.C * R + (p.rank_major || rk == R ? o : o / rk * R + o % rk);
@@ -571,41 +572,60 @@ hipError_t launch_thin_t(const ThinParams* p, int count, hipStream_t s) {
   return hipGetLastError();
 }
 
+// (Segments or LoRAs that take more workgroups than a launch holds, fewer than 2^32 threads, go in several.)
+constexpr int64_t kMostWorkgroups = ((int64_t)1 << 32) / kThreads - 1;
+
 template <class T>
 hipError_t launch_lora_grad_t(const LoraGradParams* p, int count, hipStream_t s) {
   LoraGradBatch batch{};
-  int64_t tiles = 0, items = 0, blocks = 0;
+  int64_t items = 0, ctiles = 1, quads = 0, blocks = 1;
   int nsplit = 1;
   bool sums = false;
+  const int64_t loras = p[0].meta.num_loras;
   for (int i = 0; i < count; ++i) {
-    const int64_t loras = p[i].meta.num_loras;
-    tiles = std::max(tiles, (p[i].C + kLoraGradCols - 1) / kLoraGradCols *
-                                (p[i].by_segment ? (int64_t)p[i].meta.num_segs : loras));
+    items = std::max<int64_t>(items, p[i].by_segment ? p[i].meta.num_segs : loras);
+    ctiles = std::max<int64_t>(ctiles, (p[i].C + kLoraGradCols - 1) / kLoraGradCols);
     nsplit = std::max(nsplit, p[i].nsplit);
     sums = sums || p[i].nsplit > 1 || (p[i].by_segment && !p[i].accumulate);
-    items += loras * sum_blocks(p[i].C, p[i].rank, 1);
+    quads += loras * sum_blocks(p[i].C, p[i].rank, 1);
   }
-  const int turns = (int)std::max<int64_t>(1, std::min<int64_t>(8, items / 2048));
+  const int turns = (int)std::max<int64_t>(1, std::min<int64_t>(8, quads / 2048));
   for (int i = 0; i < count; ++i) {
     batch.p[i] = p[i];
     batch.p[i].turns = turns;
-    if (sums) blocks = std::max(blocks, sum_blocks(p[i].C, p[i].rank, turns) * p[i].meta.num_loras);
+    blocks = std::max(blocks, sum_blocks(p[i].C, p[i].rank, turns));
   }
-  if (tiles > 0x7fffffff || blocks > 0x7fffffff) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)tiles, (unsigned)count, (unsigned)nsplit);
-  switch (tiles > 0 ? p[0].rank : -1) {
-    case -1: break;  // no segments
-    case 8: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 8>), grid, dim3(kThreads), 0, s, batch); break;
-    case 16: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 16>), grid, dim3(kThreads), 0, s, batch); break;
-    case 32: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 32>), grid, dim3(kThreads), 0, s, batch); break;
-    case 64: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 64>), grid, dim3(kThreads), 0, s, batch); break;
-    default: return hipErrorInvalidValue;
+  const auto part = [&](int64_t first, int64_t last) {
+    for (int i = 0; i < count; ++i) {
+      batch.p[i].first = (int32_t)first;
+      batch.p[i].last = (int32_t)last;
+    }
+  };
+  const int64_t most = kMostWorkgroups / ctiles;
+  for (int64_t first = 0; first < items; first += most) {
+    const int64_t n = std::min(most, items - first);
+    part(first, first + n);
+    const dim3 grid((unsigned)(n * ctiles), (unsigned)count, (unsigned)nsplit);
+    switch (p[0].rank) {
+      case 8: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 8>), grid, dim3(kThreads), 0, s, batch); break;
+      case 16: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 16>), grid, dim3(kThreads), 0, s, batch); break;
+      case 32: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 32>), grid, dim3(kThreads), 0, s, batch); break;
+      case 64: hipLaunchKernelGGL((sgmv_lora_grad_kernel<T, 64>), grid, dim3(kThreads), 0, s, batch); break;
+      default: return hipErrorInvalidValue;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || blocks == 0) return e;
-  hipLaunchKernelGGL((sgmv_lora_grad_sum_kernel<T>), dim3((unsigned)blocks, (unsigned)count), dim3(kThreads), 0, s,
-                     batch);
-  return hipGetLastError();
+  const int64_t most_sums = kMostWorkgroups / blocks;
+  for (int64_t first = 0; sums && first < loras; first += most_sums) {
+    const int64_t n = std::min(most_sums, loras - first);
+    part(first, first + n);
+    const dim3 grid((unsigned)(n * blocks), (unsigned)count);
+    hipLaunchKernelGGL((sgmv_lora_grad_sum_kernel<T>), grid, dim3(kThreads), 0, s, batch);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <bool HALVES, int TPR, int KEEP>
