@@ -76,9 +76,7 @@ __device__ inline int first_segment_past(const SegMeta& m, int i) {
 
 // Rank of LoRA k: the table's, or the problem's.
 __device__ inline int rank_of(const int32_t* ranks, int rank, int k) {
-  if (ranks == nullptr) return rank;
-  const int r = ranks[k];
-  return (r < 0 ? 0 : r > rank ? rank : r) & ~7;
+  return ranks == nullptr ? rank : clamp_rank(ranks[k], rank);
 }
 
 // Activations of the gated block (sgmv_act_t): value and derivative in fp32.

@@ -126,10 +126,10 @@ __device__ inline Unit resolve_unit_lanes(int lo_l, int hi_l, int num_segs, int 
 
 // Rank of a LoRA as used by the kernels: the stored value clamped to [0, R]
 // and rounded down to a multiple of 8 (one 128-bit vector of A_k per 8 ranks).
+__device__ inline int clamp_rank(int r, int most) { return (r < 0 ? 0 : r > most ? most : r) & ~7; }
 template <int R>
 __device__ inline int lora_rank(int r) {
-  return (r < 0 ? 0 : r > R ? R : r) & ~7;
+  return clamp_rank(r, R);
 }
-
 
 }  // namespace sgmv
