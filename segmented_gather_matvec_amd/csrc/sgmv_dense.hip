@@ -110,9 +110,11 @@ __device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x
     const int hi_l = end_l < sm.n_rows ? end_l : sm.n_rows;
     int k_l = sm.lora_idx[sl];
     if (k_l < 0 || k_l >= sm.num_loras) k_l = -1;
-    const uint64_t e_l = k_l >= 0 ? t.ptrs[k_l] : 0ull;
-    const uint64_t pair_l = k_l >= 0 ? t.pair[k_l] : 0ull;
-    const int r_l = k_l >= 0 && e_l != 0ull && pair_l != 0ull ? rank_of(t.ranks, R, k_l) : 0;
+    // (All loads of one LoRA at once: none under a condition of its own.)
+    const int k_in = k_l < 0 ? 0 : k_l;
+    const uint64_t e_l = t.ptrs[k_in], pair_l = t.pair[k_in];
+    const int r_in = rank_of(t.ranks, R, k_in);
+    const int r_l = k_l >= 0 && e_l != 0ull && pair_l != 0ull ? r_in : 0;
     const int ns = sm.num_segs - s0 < 64 ? sm.num_segs - s0 : 64;
     int u = 0;
     while (u < ns) {

@@ -184,6 +184,10 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
     // The window's segments of LoRA k, in order.
     const int s = s0 + t;
     const int sc = s < p.meta.num_segs ? s : p.meta.num_segs - 1;
+    // (k as a lane's value: its pointers come with the lane's other loads.)
+    int k_lane = k;
+    asm("" : "+v"(k_lane));
+    const uint64_t A = p.A[k_lane], B = p.B[k_lane];
     const int id = p.meta.lora_idx[sc], lo = p.meta.seg_indptr[sc];
     int hi = p.meta.seg_indptr[sc + 1];
     hi = hi < p.meta.n_rows ? hi : p.meta.n_rows;
@@ -207,6 +211,8 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
     __syncthreads();
     count = __builtin_amdgcn_readfirstlane(count);
     any = any || count > 0;
+    // Rows, but a matrix is missing: no gradient.  (Entries of LoRAs without rows are not used.)
+    if (any && (__ballot(A == 0 || B == 0) != 0)) return;
     // This split's steps of the window, in order: step st of segment e, which has `steps`.
     int st_first = z - counter % p.nsplit, mine = 0;
     if (st_first < 0) st_first += p.nsplit;
@@ -301,7 +307,6 @@ __device__ inline void lora_grad_body(const LoraGradParams& p, uint16_t* lds, in
   fold(0.f);
   // A LoRA without rows: zeros, written by split 0, or what it has when gradients accumulate.
   if (!any && (p.accumulate || z > 0)) return;
-  if (any && (p.A[k] == 0 || p.B[k] == 0)) return;
   const bool planes = p.nsplit > 1 && any;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
