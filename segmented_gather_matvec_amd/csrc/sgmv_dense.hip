@@ -356,8 +356,18 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
   // their bits down to 2^-21 .. 2^-28 of the largest row's largest value, and count down to 2^-32 .. 2^-40 of it).
   constexpr bool POWERS = T::kMaxFinite < 1e6f && PAIRS;
   int top = 0, low = 0;
+  // (In the ring's memory, before it is filled: a second array in LDS made the compiler wait for every load in flight.)
   if constexpr (POWERS && MODE == kDenseDw) {
     if (p.row_power != nullptr) power_range<S::NW>(p.row_power, p.K, reinterpret_cast<int*>(ring), top, low);
+  }
+  float row_w[TM];  // dX, asked for ahead of the contraction
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    row_w[i] = 1.f;
+    if constexpr (POWERS && MODE == kDenseDx) {
+      const int m = m0 + (wm * TM + i) * 16 + ml;
+      if (p.row_power != nullptr && m < p.M) row_w[i] = power_of(p.row_power[m < p.meta.n_rows ? m : m - p.meta.n_rows]);
+    }
   }
 
   f32x4 acc[TM][TN];
@@ -434,11 +444,7 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
     if (p.row_power != nullptr) {
 #pragma unroll
       for (int i = 0; i < TM; ++i) {
-        float w = power_of(top);
-        if constexpr (MODE == kDenseDx) {
-          const int m = mw + i * 16 + ml;
-          w = m < p.M ? power_of(p.row_power[m < p.meta.n_rows ? m : m - p.meta.n_rows]) : 0.f;
-        }
+        const float w = MODE == kDenseDx ? row_w[i] : power_of(top);
 #pragma unroll
         for (int j = 0; j < TN; ++j)
 #pragma unroll

@@ -502,9 +502,9 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void sgmv_gate_bac
 #pragma unroll
     for (int c = 0; c < KEEP; ++c) {  // (past the end: the row's last eight again, so that all loads are in flight at once)
       const int64_t i = at + (c * TPR + t < f8 ? c * TPR + t : f8 - 1);
-      g[c] = load_vec(G + i * 8);
-      u[c] = load_vec(U + i * 8);
-      h[c] = load_vec(dH + i * 8);
+      g[c] = load_stream(G + i * 8);
+      u[c] = load_stream(U + i * 8);
+      h[c] = load_stream(dH + i * 8);
     }
 #pragma unroll
     for (int c = 0; c < KEEP; ++c) see(g[c], u[c], h[c]);

@@ -68,7 +68,7 @@ struct ThinShape {
   static constexpr int B0 = kThinRows * kDenseK, HALF = (kThinRows + COLS) * kDenseK, SLOT = 2 * HALF;
   static constexpr int RST = COLS + 4;  // row stride of the result in LDS (floats)
   static constexpr int LDS = STAGES * SLOT;
-  static_assert(LDS * 2 >= kThinRows * RST * 4, "the result fits the ring");
+  static_assert(LDS * 2 >= kThinRows * (RST + 1) * 4, "the result and its rows' powers fit the ring");
 };
 
 template <class T, int JT, bool TRANSPOSED>
@@ -91,6 +91,9 @@ __device__ inline void thin_body(const ThinParams& p, int block, uint16_t* lds) 
   const int k0 = g * p.kc;
   const int k1 = p.K < k0 + p.kc ? p.K : k0 + p.kc;
   const int steps = rk > 0 ? (k1 - k0 + 2 * kDenseK - 1) / (2 * kDenseK) : 0;
+
+  // (The rows' powers, asked for ahead of the contraction.)
+  const int z_power = T::kMaxFinite < 1e6f && p.z_power != nullptr && t < un.L ? p.z_power[un.r0 + t] : 0;
 
   if (p.row_k != nullptr && g == 0 && t < un.L) p.row_k[un.r0 + t] = D != nullptr ? un.k : -1;
 
@@ -134,6 +137,8 @@ __device__ inline void thin_body(const ThinParams& p, int block, uint16_t* lds) 
   __syncthreads();
   // acc[j][e]: row 16 wave + ml, rank 16 j + 4 q + e.
   float* res = reinterpret_cast<float*>(lds);
+  float* row_w = res + kThinRows * RST;
+  if (T::kMaxFinite < 1e6f && t < kThinRows) row_w[t] = power_of(z_power);
 #pragma unroll
   for (int j = 0; j < JT; ++j) *reinterpret_cast<f32x4*>(&res[(wave * 16 + ml) * RST + j * 16 + q * 4]) = acc[j];
   __syncthreads();
@@ -144,11 +149,9 @@ __device__ inline void thin_body(const ThinParams& p, int block, uint16_t* lds) 
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c < rk ? res[r * RST + c + e] * scale : 0.f;
     if constexpr (T::kMaxFinite < 1e6f) {
-      if (p.z_power != nullptr) {
-        const float w = power_of(p.z_power[un.r0 + r]);
+      const float w = row_w[r];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= w;
-      }
+      for (int e = 0; e < 8; ++e) v[e] *= w;
     }
     if (p.to_planes) {
       float* dst = p.planes + ((int64_t)g * p.meta.n_rows + un.r0 + r) * p.rank + c;
