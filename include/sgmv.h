@@ -455,7 +455,9 @@ sgmv_status_t sgmv_base_lora_apply_partial(const sgmv_problem_t* problem, const 
  *
  * Punica README, LoRA paragraph: a row x gets x@W + x@A@B; multi-LoRA
  * paragraph: every row of a batch brings its own LoRA.  sgmv_base_lora_apply
- * computes that for decode-sized batches.  The entry points below take any
+ * computes that for decode-sized batches (up to 32 rows it is the faster one
+ * where no ranks or scales are needed; from about 64 rows on the calls below are).
+ * The entry points below take any
  * number of rows (a single token, a decode batch, prompts, a training
  * micro-batch), the ranks and scales of sgmv_projection_t, and add the backward pass and
  * the gated feed-forward block, whose gate and up projections are two such layers

@@ -20,8 +20,8 @@ __device__ inline void wait_loads_and_lds() {
 }
 
 // Column swizzle of a tile stored [k][cols] (the f(k) above), in 16-byte groups.  Rows of 16 groups and more are
-// read without bank conflicts; narrower ones (thin products, V16 of the LoRA gradients) have fewer places
-// to go: 24 to 33% of the thin kernels' LDS cycles are conflicts.
+// read without bank conflicts; the 2 to 8 groups of the thin products' D_k leave fewer places to go: 24 to 33% of
+// those kernels' LDS cycles are conflicts.
 template <int COLS>
 __device__ inline int swizzle_k(int k) {
   return (((k & 3) | ((k >> 1) & 4)) << 1) & (COLS / 8 - 1);
