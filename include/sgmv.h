@@ -525,10 +525,12 @@ typedef enum sgmv_act {
 
 /* Most rows a layer call takes, and most blocks of up to 64 rows of one segment
  * (num_segs where max_seg_len <= 64, else the smaller of num_segs *
- * ceil(max_seg_len / 64) and ceil(n_rows / 64) + num_segs); more give
- * SGMV_ERR_UNSUPPORTED. */
+ * ceil(max_seg_len / 64) and ceil(n_rows / 64) + num_segs); and most segments
+ * where max_seg_len > 64 (a workgroup then finds its block by walking them).
+ * More give SGMV_ERR_UNSUPPORTED. */
 #define SGMV_MAX_LAYER_ROWS (1 << 30)
 #define SGMV_MAX_LAYER_UNITS ((1 << 24) - 1)
+#define SGMV_MAX_LAYER_LONG_SEGS (1 << 18)
 
 /* Entry point a workspace is for. */
 typedef enum sgmv_layer_op {

@@ -139,10 +139,11 @@ sgmv_status_t check_layer(const sgmv_problem_t* p) {
   if (!p) return SGMV_ERR_INVALID_ARG;
   const sgmv_status_t st = check_shape(*p);
   if (st != SGMV_OK) return st;
-  int direct;
-  if (p->n_rows > SGMV_MAX_LAYER_ROWS || (!nothing_to_do(*p) && units_for(*p, sgmv::kThinRows, &direct) > SGMV_MAX_LAYER_UNITS))
-    return SGMV_ERR_UNSUPPORTED;
-  return SGMV_OK;
+  if (p->n_rows > SGMV_MAX_LAYER_ROWS) return SGMV_ERR_UNSUPPORTED;
+  if (nothing_to_do(*p)) return SGMV_OK;
+  int direct = 1;
+  const int64_t units = units_for(*p, sgmv::kThinRows, &direct);
+  return units > SGMV_MAX_LAYER_UNITS || (!direct && p->num_segs > SGMV_MAX_LAYER_LONG_SEGS) ? SGMV_ERR_UNSUPPORTED : SGMV_OK;
 }
 
 LayerPlan plan_layer(const sgmv_problem_t& p, int op) {

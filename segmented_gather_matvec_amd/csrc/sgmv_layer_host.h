@@ -45,8 +45,8 @@ struct LayerPlan {
 
 inline bool layer_gated(int op) { return op == SGMV_GATED_FORWARD || op == SGMV_GATED_BACKWARD; }
 inline bool layer_backward(int op) { return op == SGMV_DENSE_BACKWARD || op == SGMV_GATED_BACKWARD; }
-// The shape's checks, the rows that the tiles' 32-bit row numbers reach, and the units that one launch holds (a
-// workgroup each; a launch has fewer than 2^32 threads).
+// The shape's checks, the rows that the tiles' 32-bit row numbers reach, the units that one launch holds (a
+// workgroup each; a launch has fewer than 2^32 threads), and the segments that every unit may walk.
 sgmv_status_t check_layer(const sgmv_problem_t* p);
 LayerPlan plan_layer(const sgmv_problem_t& p, int op);
 

@@ -42,7 +42,8 @@ int main() {
       const sgmv_status_t st = sgmv_layer_workspace_bytes(&p, op, &bytes);
       int direct = 0;
       const bool fits = p.n_rows <= SGMV_MAX_LAYER_ROWS &&
-                        (nothing_to_do(p) || units_for(p, sgmv::kThinRows, &direct) <= SGMV_MAX_LAYER_UNITS);
+                        (nothing_to_do(p) || (units_for(p, sgmv::kThinRows, &direct) <= SGMV_MAX_LAYER_UNITS &&
+                                              (direct || p.num_segs <= SGMV_MAX_LAYER_LONG_SEGS)));
       CHECK(st == (fits ? SGMV_OK : SGMV_ERR_UNSUPPORTED));
       ++(fits ? taken : refused);
       if (st != SGMV_OK) continue;

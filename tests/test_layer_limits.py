@@ -33,6 +33,7 @@ def test_rows_and_segments_that_a_layer_takes(op, kw):
     dict(n_rows=MOST_UNITS + 1, num_segs=MOST_UNITS + 1, max_seg_len=1),
     dict(n_rows=1 << 30, num_segs=(1 << 31) - 1, max_seg_len=1 << 30),
     dict(n_rows=(1 << 30) + 1, num_segs=1, max_seg_len=1 << 30),
+    dict(n_rows=1000, num_segs=(1 << 18) + 1, max_seg_len=65),
 ])
 def test_more_is_refused(op, kw):
     p = good(**{**SMALL, **kw})
