@@ -569,6 +569,95 @@ sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* problem, const void
                                        const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
                                        void* stream);
 
+/* ---- Rows sorted by LoRA and back, on the device ----
+ *
+ * Punica README, multi-LoRA paragraph: every row of a batch brings its own LoRA;
+ * the calls above want rows that share one next to each other.
+ * sgmv_build_segments arranges that on the host for one LoRA a row; the calls
+ * below do it on the device, for the top_k LoRAs that a router chose for every
+ * row (top_k = 1: one LoRA a row), and bring the results back, weighted.
+ * Entry e = i * top_k + j is the j-th choice of row i; m = n_rows * top_k.
+ *
+ *   sgmv_route_rows             ids [m] -> slots [m], the place of every entry among the
+ *                               sorted ones; perm [m], its inverse (the builder's perm where top_k = 1);
+ *                               seg_indptr [num_loras + 1] and lora_idx [num_loras]: one segment
+ *                               per LoRA, empty ones too, for the calls above with
+ *                               n_rows = m, num_segs = num_loras, max_seg_len = m (or any bound).
+ *                               Ascending LoRA, ties by entry (a stable sort).  Entries whose id is
+ *                               outside [0, num_loras) have no LoRA: they come last, in
+ *                               their order, and no segment covers them.
+ *   sgmv_dispatch_rows          Xs[slots[e], :] = X[i, :]
+ *   sgmv_combine_rows           Y[i, :] = residual[i, :] + sum_j weights[e] * Ys[slots[e], :]
+ *   sgmv_combine_rows_backward  dYs[slots[e], :] = weights[e] * dY[i, :];  dweights[e] = <dY[i, :], Ys[slots[e], :]>
+ * The gradient of sgmv_dispatch_rows is sgmv_combine_rows of dXs without weights
+ * and residual; that of residual is dY.
+ *
+ * Layouts (device, row-major, contiguous): X, Y, dY, residual [n_rows, width] and
+ * Xs, Ys, dYs [m, width] in `dtype`, 16-byte aligned, width a multiple of 8 up to
+ * SGMV_MAX_HIDDEN; ids, slots, perm, seg_indptr, lora_idx int32; weights, dweights [m] fp32.  weights NULL:
+ * all 1; residual NULL: none; Y may be residual itself; otherwise outputs may not overlap inputs or each other.  Every output of
+ * sgmv_route_rows and of the backward call may be NULL (not wanted); Ys is read only for dweights.
+ * Precondition (not checked on the device): slots is a permutation of 0 .. m - 1, as
+ * sgmv_route_rows makes it.  Entries of slots outside of that are passed over (rows
+ * they would have filled keep their values, and nothing is added for them).
+ *
+ * Sums are fp32 in the order of j, rounded once.  An entry of weight 0 adds
+ * nothing to Y and gets a dYs of 0, whatever its row holds.  The sort uses integer
+ * counts alone: its result does not depend on timing.
+ *
+ * Limits: 1 <= top_k <= SGMV_MAX_TOP_K, m <= SGMV_MAX_LAYER_ROWS, num_loras <=
+ * SGMV_MAX_ROUTE_LORAS; beyond them SGMV_ERR_UNSUPPORTED.  ws: device workspace of
+ * sgmv_route_workspace_bytes (any contents; may be 0); calls that share one must
+ * not overlap.  Asynchronous on `stream`, can be captured into a graph.  n_rows = 0:
+ * sgmv_route_rows writes empty segments, the others do nothing. */
+#define SGMV_MAX_TOP_K 64
+#define SGMV_MAX_ROUTE_LORAS 8192
+
+sgmv_status_t sgmv_route_workspace_bytes(int32_t n_rows, int32_t top_k, int32_t num_loras, size_t* bytes);
+sgmv_status_t sgmv_route_rows(int32_t n_rows, int32_t top_k, int32_t num_loras, const int32_t* ids, int32_t* perm,
+                              int32_t* slots, int32_t* seg_indptr, int32_t* lora_idx, void* ws, size_t ws_bytes,
+                              void* stream);
+sgmv_status_t sgmv_dispatch_rows(int32_t dtype, int32_t n_rows, int32_t top_k, int32_t width, const void* X,
+                                 const int32_t* slots, void* Xs, void* stream);
+sgmv_status_t sgmv_combine_rows(int32_t dtype, int32_t n_rows, int32_t top_k, int32_t width, const void* Ys,
+                                const int32_t* slots, const float* weights, const void* residual, void* Y, void* stream);
+sgmv_status_t sgmv_combine_rows_backward(int32_t dtype, int32_t n_rows, int32_t top_k, int32_t width, const void* dY,
+                                         const void* Ys, const int32_t* slots, const float* weights, void* dYs,
+                                         float* dweights, void* stream);
+
+/* ---- Layer norm ----
+ *
+ * What stands in front of a layer's projections (the pages' layers take their
+ * input x as given):
+ *   sgmv_layer_norm_apply     mean_i = mean(X[i, :]),  rstd_i = (mean((X[i, :] - mean_i)^2) + eps)^(-1/2)
+ *                             Y[i, :] = (X[i, :] - mean_i) * rstd_i * gamma + beta
+ *   sgmv_layer_norm_backward  xh = (X[i, :] - mean_i) * rstd_i,  q = dY[i, :] * gamma
+ *                             dX[i, :] = rstd_i * (q - mean(q) - xh * mean(q * xh)) + beyond[i, :]
+ *                             dgamma = sum_i dY[i, :] * xh,  dbeta = sum_i dY[i, :]
+ * X, Y, dY, dX, beyond [n_rows, width], gamma, beta, dgamma, dbeta [width] in `dtype`,
+ * 16-byte aligned, width a multiple of 8 up to SGMV_MAX_HIDDEN; mean, rstd [n_rows] fp32.
+ * gamma NULL: ones; beta NULL: zeros; mean and rstd of the forward call: where to
+ * store them for the backward call, or NULL.  beyond: the gradient that reaches X
+ * past the norm (the residual stream's), or NULL.  dX, dgamma, dbeta: each may be
+ * NULL (not wanted).  Y may be X itself, dX may be dY or beyond; otherwise outputs may not overlap inputs or each
+ * other.  accumulate = 0: dgamma and dbeta are written; 1: added to what is there in
+ * fp32 and rounded once.  dX is always written.
+ * Sums are fp32 in a fixed order (no atomics), outputs are rounded once; the variance
+ * is the mean of squares about the mean.  A row of infinities or NaN spoils its own
+ * outputs, dgamma and dbeta only.
+ * n_rows <= SGMV_MAX_LAYER_ROWS; n_rows = 0: the forward call does nothing, the backward call
+ * writes zero dgamma and dbeta (accumulate = 0).  ws: device workspace of
+ * sgmv_layer_norm_workspace_bytes (the backward call's; any contents); calls that
+ * share one must not overlap.  Asynchronous on `stream`, can be captured into a
+ * graph.  SGMV_ERR_INVALID_ARG for an eps that is negative, infinite or NaN. */
+sgmv_status_t sgmv_layer_norm_workspace_bytes(int32_t n_rows, int32_t width, size_t* bytes);
+sgmv_status_t sgmv_layer_norm_apply(int32_t dtype, int32_t n_rows, int32_t width, const void* X, const void* gamma,
+                                    const void* beta, float eps, void* Y, float* mean, float* rstd, void* stream);
+sgmv_status_t sgmv_layer_norm_backward(int32_t dtype, int32_t n_rows, int32_t width, const void* X, const void* gamma,
+                                       const float* mean, const float* rstd, const void* dY, const void* beyond, void* dX,
+                                       void* dgamma, void* dbeta, int32_t accumulate, void* ws, size_t ws_bytes,
+                                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

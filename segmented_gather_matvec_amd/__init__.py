@@ -37,7 +37,9 @@ ENTRY_POINTS = ("sgmv_status_str", "sgmv_build_segments", "sgmv_check_problem",
                 "sgmv_base_lora_apply_packed", "sgmv_set_wait_limit", "sgmv_take_device_errors",
                 "sgmv_lora_apply_noalloc", "sgmv_base_lora_apply_partial", "sgmv_lora_apply_host_meta",
                 "sgmv_layer_workspace_bytes", "sgmv_dense_lora_apply", "sgmv_gated_lora_apply",
-                "sgmv_dense_lora_backward", "sgmv_gated_lora_backward")
+                "sgmv_dense_lora_backward", "sgmv_gated_lora_backward", "sgmv_route_workspace_bytes",
+                "sgmv_route_rows", "sgmv_dispatch_rows", "sgmv_combine_rows", "sgmv_combine_rows_backward",
+                "sgmv_layer_norm_workspace_bytes", "sgmv_layer_norm_apply", "sgmv_layer_norm_backward")
 SGMV_DEVICE_ERR_WAIT_TIMEOUT = 1
 SGMV_NOALLOC_MAX_WORKSPACE = 16 << 20
 SGMV_BASE_MAX_ROWS = 128
@@ -128,6 +130,15 @@ def load_library(path: str = LIB_PATH):
     lib.sgmv_gated_lora_apply.argtypes = [prob, P, P, P, proj, proj, I32, P, P, P, P, SZ, P]
     lib.sgmv_dense_lora_backward.argtypes = [prob, P, P, proj, P, P, grad, I32, P, P, P, SZ, P]
     lib.sgmv_gated_lora_backward.argtypes = [prob, P, P, P, proj, proj, I32, P, P, grad, grad, I32, P, P, P, SZ, P]
+    F32 = ctypes.c_float
+    lib.sgmv_route_workspace_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(SZ)]
+    lib.sgmv_route_rows.argtypes = [I32, I32, I32, P, P, P, P, P, P, SZ, P]
+    lib.sgmv_dispatch_rows.argtypes = [I32, I32, I32, I32, P, P, P, P]
+    lib.sgmv_combine_rows.argtypes = [I32, I32, I32, I32, P, P, P, P, P, P]
+    lib.sgmv_combine_rows_backward.argtypes = [I32, I32, I32, I32, P, P, P, P, P, P, P]
+    lib.sgmv_layer_norm_workspace_bytes.argtypes = [I32, I32, ctypes.POINTER(SZ)]
+    lib.sgmv_layer_norm_apply.argtypes = [I32, I32, I32, P, P, P, F32, P, P, P, P]
+    lib.sgmv_layer_norm_backward.argtypes = [I32, I32, I32, P, P, P, P, P, P, P, P, P, I32, P, SZ, P]
     for name in ENTRY_POINTS[1:]:
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
@@ -558,6 +569,163 @@ def sgmv_gated_lora_backward(problem, X, Wg, Wu, gate, up, dH, seg_indptr, lora_
     a.launch("sgmv_gated_lora_backward", stream, *a.W, ctypes.byref(a.projection(gate, "gate")),
              ctypes.byref(a.projection(up, "up")), int(act), a.rows(dH, "dH", "out"), a.rows(dX, "dX", "in"),
              ctypes.byref(a.grad(gate_grad, "gate_grad")), ctypes.byref(a.grad(up_grad, "up_grad")), int(accumulate))
+
+
+# ------------------------------------------------- rows sorted by LoRA and back, layer norm
+
+def _on_device(index, call, stream, *args):
+    """An entry point with device `index` current, on `stream` or that device's current stream."""
+    import torch
+    entry = getattr(load_library(), call)
+    if index == torch.cuda.current_device():
+        _check(entry(*args, _stream(stream)), call)
+        return
+    with torch.cuda.device(index):
+        _check(entry(*args, _stream(stream)), call)
+
+
+def _matrix(t, name):
+    """(device index, dtype, rows, columns) of a call's first matrix."""
+    _need(t, name)
+    if t is None or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D device tensor")
+    _dtype_16(t, name)
+    return t.get_device(), t.dtype, t.shape[0], t.shape[1]
+
+
+def _dtype_16(t, name):
+    import torch
+    if t.dtype is not torch.float16 and t.dtype is not torch.bfloat16:
+        raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+
+
+def _top_k(sorted_rows, n, name):
+    if n == 0:
+        return 1
+    if sorted_rows % n != 0 or sorted_rows < n:
+        raise ValueError(f"{name} must have a whole number of rows for each of {n}, got {sorted_rows}")
+    return sorted_rows // n
+
+
+def _buffer(t, name, index):
+    if t is None:
+        return None, 0
+    return _layer_ptr(t, name, index, t.dtype), t.numel() * t.element_size()
+
+
+def sgmv_route_workspace_bytes(n_rows: int, top_k: int, num_loras: int) -> int:
+    """Workspace bytes of sgmv_route_rows; may be 0."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().sgmv_route_workspace_bytes(int(n_rows), int(top_k), int(num_loras), ctypes.byref(out)),
+           "sgmv_route_workspace_bytes")
+    return int(out.value)
+
+
+def new_route_workspace(n_rows: int, top_k: int, num_loras: int, device="cuda"):
+    """Device workspace of sgmv_route_workspace_bytes(...) bytes (any contents will do)."""
+    import torch
+    return torch.empty(sgmv_route_workspace_bytes(n_rows, top_k, num_loras), dtype=torch.uint8, device=device)
+
+
+def sgmv_route_rows(ids, num_loras, perm, slots, seg_indptr, lora_idx, ws, stream=None):
+    """Device segment builder for `ids` (int32 [n_rows] or [n_rows, top_k], the LoRAs each row chose; outside
+    [0, num_loras): none): `slots` and `perm` (int32, one entry per choice), `seg_indptr` (int32 [num_loras + 1]) and
+    `lora_idx` (int32 [num_loras]), each may be None; `ws` from new_route_workspace.  Asynchronous."""
+    import torch
+    i32 = torch.int32
+    _need(ids, "ids", i32)
+    if ids is None or ids.dim() not in (1, 2):
+        raise ValueError("ids must be a [n_rows] or [n_rows, top_k] device tensor")
+    n, top_k, index = ids.shape[0], ids.shape[1] if ids.dim() == 2 else 1, ids.get_device()
+    m = n * top_k
+    out = [_layer_ptr(t, name, index, i32, None, least) for t, name, least in
+           ((perm, "perm", m), (slots, "slots", m), (seg_indptr, "seg_indptr", int(num_loras) + 1),
+            (lora_idx, "lora_idx", int(num_loras)))]
+    _on_device(index, "sgmv_route_rows", stream, n, top_k, int(num_loras), ids.data_ptr(), *out, *_buffer(ws, "ws", index))
+
+
+def sgmv_dispatch_rows(X, slots, Xs, stream=None):
+    """Xs[slots[i * top_k + j]] = X[i] (X [n_rows, width], Xs [n_rows * top_k, width], slots of sgmv_route_rows).
+    Asynchronous."""
+    import torch
+    index, dtype, n, width = _matrix(X, "X")
+    _matrix(Xs, "Xs")
+    top_k = _top_k(Xs.shape[0], n, "Xs")
+    m = n * top_k
+    out = _layer_ptr(Xs, "Xs", index, dtype, (m, width))
+    _on_device(index, "sgmv_dispatch_rows", stream, _dtype_code(dtype), n, top_k, width, X.data_ptr(),
+               _layer_ptr(slots, "slots", index, torch.int32, None, m), out)
+
+
+def sgmv_combine_rows(Ys, slots, Y, weights=None, residual=None, stream=None):
+    """Y[i] = residual[i] + sum_j weights[i * top_k + j] * Ys[slots[i * top_k + j]] (Y [n_rows, width], Ys
+    [n_rows * top_k, width], weights float32 or None for ones; Y may be residual).  Without weights and residual it is the gradient
+    of sgmv_dispatch_rows.  Asynchronous."""
+    import torch
+    index, dtype, n, width = _matrix(Y, "Y")
+    _matrix(Ys, "Ys")
+    top_k = _top_k(Ys.shape[0], n, "Ys")
+    m = n * top_k
+    args = (_layer_ptr(Ys, "Ys", index, dtype, (m, width)), _layer_ptr(slots, "slots", index, torch.int32, None, m),
+            _layer_ptr(weights, "weights", index, torch.float32, None, m),
+            _layer_ptr(residual, "residual", index, dtype, (n, width)))
+    _on_device(index, "sgmv_combine_rows", stream, _dtype_code(dtype), n, top_k, width, *args, Y.data_ptr())
+
+
+def sgmv_combine_rows_backward(dY, Ys, slots, weights=None, dYs=None, dweights=None, stream=None):
+    """Gradients of sgmv_combine_rows from dY [n_rows, width]: dYs [n_rows * top_k, width] and dweights (float32, one
+    per choice), each or None; Ys is needed for dweights only.  Asynchronous."""
+    import torch
+    index, dtype, n, width = _matrix(dY, "dY")
+    _need(slots, "slots", torch.int32)
+    m = slots.numel() if slots is not None else 0
+    top_k = _top_k(m, n, "slots")
+    m = n * top_k
+    args = (_layer_ptr(Ys, "Ys", index, dtype, (m, width)), _layer_ptr(slots, "slots", index, torch.int32, None, m),
+            _layer_ptr(weights, "weights", index, torch.float32, None, m),
+            _layer_ptr(dYs, "dYs", index, dtype, (m, width)),
+            _layer_ptr(dweights, "dweights", index, torch.float32, None, m))
+    _on_device(index, "sgmv_combine_rows_backward", stream, _dtype_code(dtype), n, top_k, width, dY.data_ptr(), *args)
+
+
+def sgmv_layer_norm_workspace_bytes(n_rows: int, width: int) -> int:
+    """Workspace bytes of sgmv_layer_norm_backward."""
+    out = ctypes.c_size_t(0)
+    _check(load_library().sgmv_layer_norm_workspace_bytes(int(n_rows), int(width), ctypes.byref(out)),
+           "sgmv_layer_norm_workspace_bytes")
+    return int(out.value)
+
+
+def new_layer_norm_workspace(n_rows: int, width: int, device="cuda"):
+    """Device workspace of sgmv_layer_norm_workspace_bytes(n_rows, width) bytes (any contents will do)."""
+    import torch
+    return torch.empty(sgmv_layer_norm_workspace_bytes(n_rows, width), dtype=torch.uint8, device=device)
+
+
+def sgmv_layer_norm_apply(X, gamma, beta, Y, eps=1e-5, mean=None, rstd=None, stream=None):
+    """Y = (X - mean) * rstd * gamma + beta, row by row (gamma, beta [width] or None; Y may be X); `mean` and `rstd`
+    (float32 [n_rows] or None) are stored for sgmv_layer_norm_backward.  Asynchronous."""
+    import torch
+    index, dtype, n, width = _matrix(X, "X")
+    args = (_layer_ptr(gamma, "gamma", index, dtype, (width,)), _layer_ptr(beta, "beta", index, dtype, (width,)), float(eps),
+            _layer_ptr(Y, "Y", index, dtype, (n, width)), _layer_ptr(mean, "mean", index, torch.float32, (n,)),
+            _layer_ptr(rstd, "rstd", index, torch.float32, (n,)))
+    _on_device(index, "sgmv_layer_norm_apply", stream, _dtype_code(dtype), n, width, X.data_ptr(), *args)
+
+
+def sgmv_layer_norm_backward(X, gamma, mean, rstd, dY, ws, dX=None, beyond=None, dgamma=None, dbeta=None,
+                             accumulate=False, stream=None):
+    """Gradients of sgmv_layer_norm_apply from dY and the stored mean and rstd: dX (written, with `beyond` added; may be dY
+    or beyond), dgamma and dbeta (written, or added to what is there with accumulate), each or None; `ws` from
+    new_layer_norm_workspace.  Asynchronous."""
+    import torch
+    index, dtype, n, width = _matrix(X, "X")
+    f32 = torch.float32
+    rows = [_layer_ptr(t, name, index, dtype, (n, width)) for t, name in ((dY, "dY"), (beyond, "beyond"), (dX, "dX"))]
+    cols = [_layer_ptr(t, name, index, dtype, (width,)) for t, name in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta"))]
+    _on_device(index, "sgmv_layer_norm_backward", stream, _dtype_code(dtype), n, width, X.data_ptr(), cols[0],
+               _layer_ptr(mean, "mean", index, f32, (n,)), _layer_ptr(rstd, "rstd", index, f32, (n,)), *rows, *cols[1:],
+               int(accumulate), *_buffer(ws, "ws", index))
 
 
 def batched_workspace_bytes(problem: sgmv_problem_t, num_projections: int) -> int:
