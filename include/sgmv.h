@@ -520,7 +520,11 @@ sgmv_status_t sgmv_base_lora_apply_partial(const sgmv_problem_t* problem, const 
  * kernels set. */
 typedef enum sgmv_act {
   SGMV_ACT_SILU = 0,      /* g / (1 + e^-g) */
-  SGMV_ACT_GELU_TANH = 1  /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+  SGMV_ACT_GELU_TANH = 1, /* 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+  /* of sgmv_dense_act_lora_apply and its backward call only: */
+  SGMV_ACT_NONE = 2,      /* z */
+  SGMV_ACT_RELU = 3,      /* max(z, 0), derivative 0 at 0 */
+  SGMV_ACT_GELU = 4       /* z Phi(z) = 0.5 z erfc(-z / sqrt 2) */
 } sgmv_act_t;
 
 /* Most rows a layer call takes, and most blocks of up to 64 rows of one segment
@@ -537,7 +541,9 @@ typedef enum sgmv_layer_op {
   SGMV_DENSE_FORWARD = 0,
   SGMV_DENSE_BACKWARD = 1,
   SGMV_GATED_FORWARD = 2,
-  SGMV_GATED_BACKWARD = 3
+  SGMV_GATED_BACKWARD = 3,
+  SGMV_DENSE_ACT_FORWARD = 5,
+  SGMV_DENSE_ACT_BACKWARD = 6
 } sgmv_layer_op_t;
 
 /* Where the gradients of one projection go (device pointers). */
@@ -568,6 +574,41 @@ sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* problem, const void
                                        const sgmv_projection_grad_t* up_grad, int32_t accumulate,
                                        const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
                                        void* stream);
+
+/* ---- A layer with bias, activation and residual, and its gradients ----
+ *
+ * A projection of a block without a gate (up, activation, down) and every
+ * projection that ends in the residual stream: the layer above with an epilogue,
+ *
+ *   sgmv_dense_act_lora_apply     Z[i, :] = X[i, :] @ W + bias + s_k (X[i, :] @ A_k) @ B_k
+ *                                 Y[i, :] = act(Z[i, :]) + residual[i, :]
+ *   sgmv_dense_act_lora_backward  dZ = dY * act'(Z), dbias = sum_i dZ[i, :], then dX, dA_k,
+ *                                 dB_k and dW from dZ as of sgmv_dense_lora_backward
+ *                                 (the gradient of residual is dY itself)
+ *
+ * act: any sgmv_act_t.  bias, dbias [h_out] and residual, Z [n_rows, h_out] in the
+ * problem's format, 16-byte aligned, each may be NULL: no bias, no residual, Z or dbias not
+ * wanted.  proj->Y of the forward call is Y; it may be residual itself, but
+ * no other output or input.  Z of the forward call: where to store Z for the backward call, which
+ * reads it (rounded once) unless act is SGMV_ACT_NONE (then it may be NULL).  proj->Y is not used by the backward call.
+ * accumulate as for sgmv_dense_lora_backward, dbias included.  Everything else
+ * (layouts, segments, NULL entries, limits, n_rows = 0, streams, errors) as for
+ * sgmv_dense_lora_apply and sgmv_dense_lora_backward; workspaces: SGMV_DENSE_ACT_FORWARD, SGMV_DENSE_ACT_BACKWARD.
+ *
+ * Precision: Y is rounded once, from the unrounded Z; the activation is good to some
+ * units in the last place of fp32.  dZ is an operand of the matrix
+ * cores and rounded once for that (or two halves, or a row divided by a power of two of its own, as dG and dU of the
+ * gated block; a value keeps its 11 bits of fp16 down to 2^-21 of the row's largest 1.13 |dY|);
+ * dbias sums the unrounded dZ.  act = SGMV_ACT_NONE takes dY as dZ. */
+sgmv_status_t sgmv_dense_act_lora_apply(const sgmv_problem_t* problem, const void* X, const void* W,
+                                        const sgmv_projection_t* proj, const void* bias, int32_t act,
+                                        const void* residual, void* Z, const int32_t* seg_indptr, const int32_t* lora_idx,
+                                        void* ws, size_t ws_bytes, void* stream);
+sgmv_status_t sgmv_dense_act_lora_backward(const sgmv_problem_t* problem, const void* X, const void* W,
+                                           const sgmv_projection_t* proj, int32_t act, const void* Z, const void* dY,
+                                           void* dX, const sgmv_projection_grad_t* grad, void* dbias, int32_t accumulate,
+                                           const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
+                                           void* stream);
 
 /* ---- Rows sorted by LoRA and back, on the device ----
  *

@@ -39,13 +39,15 @@ ENTRY_POINTS = ("sgmv_status_str", "sgmv_build_segments", "sgmv_check_problem",
                 "sgmv_layer_workspace_bytes", "sgmv_dense_lora_apply", "sgmv_gated_lora_apply",
                 "sgmv_dense_lora_backward", "sgmv_gated_lora_backward", "sgmv_route_workspace_bytes",
                 "sgmv_route_rows", "sgmv_dispatch_rows", "sgmv_combine_rows", "sgmv_combine_rows_backward",
-                "sgmv_layer_norm_workspace_bytes", "sgmv_layer_norm_apply", "sgmv_layer_norm_backward")
+                "sgmv_layer_norm_workspace_bytes", "sgmv_layer_norm_apply", "sgmv_layer_norm_backward",
+                "sgmv_dense_act_lora_apply", "sgmv_dense_act_lora_backward")
 SGMV_DEVICE_ERR_WAIT_TIMEOUT = 1
 SGMV_NOALLOC_MAX_WORKSPACE = 16 << 20
 SGMV_BASE_MAX_ROWS = 128
 SGMV_HOST_META_MAX_SEGS = 64
-SGMV_ACT_SILU, SGMV_ACT_GELU_TANH = range(2)
+SGMV_ACT_SILU, SGMV_ACT_GELU_TANH, SGMV_ACT_NONE, SGMV_ACT_RELU, SGMV_ACT_GELU = range(5)
 SGMV_DENSE_FORWARD, SGMV_DENSE_BACKWARD, SGMV_GATED_FORWARD, SGMV_GATED_BACKWARD = range(4)
+SGMV_DENSE_ACT_FORWARD, SGMV_DENSE_ACT_BACKWARD = 5, 6
 
 
 class SgmvError(RuntimeError):
@@ -130,6 +132,8 @@ def load_library(path: str = LIB_PATH):
     lib.sgmv_gated_lora_apply.argtypes = [prob, P, P, P, proj, proj, I32, P, P, P, P, SZ, P]
     lib.sgmv_dense_lora_backward.argtypes = [prob, P, P, proj, P, P, grad, I32, P, P, P, SZ, P]
     lib.sgmv_gated_lora_backward.argtypes = [prob, P, P, P, proj, proj, I32, P, P, grad, grad, I32, P, P, P, SZ, P]
+    lib.sgmv_dense_act_lora_apply.argtypes = [prob, P, P, proj, P, I32, P, P, P, P, P, SZ, P]
+    lib.sgmv_dense_act_lora_backward.argtypes = [prob, P, P, proj, I32, P, P, P, grad, P, I32, P, P, P, SZ, P]
     F32 = ctypes.c_float
     lib.sgmv_route_workspace_bytes.argtypes = [I32, I32, I32, ctypes.POINTER(SZ)]
     lib.sgmv_route_rows.argtypes = [I32, I32, I32, P, P, P, P, P, P, SZ, P]
@@ -452,7 +456,7 @@ def sgmv_base_lora_apply_packed(problem, X, Wp, A_ptrs, B_ptrs, Y, seg_indptr, l
 
 def sgmv_layer_workspace_bytes(problem: sgmv_problem_t, op: int) -> int:
     """Workspace bytes of one of the layer entry points; ``op`` is SGMV_DENSE_FORWARD, _BACKWARD,
-    SGMV_GATED_FORWARD or _BACKWARD."""
+    SGMV_GATED_FORWARD, _BACKWARD, SGMV_DENSE_ACT_FORWARD or _BACKWARD."""
     out = ctypes.c_size_t(0)
     _check(load_library().sgmv_layer_workspace_bytes(ctypes.byref(problem), int(op), ctypes.byref(out)),
            "sgmv_layer_workspace_bytes")
@@ -505,6 +509,9 @@ class _LayerArgs:
 
     def rows(self, t, name, shape):
         return _layer_ptr(t, name, self.index, self.dtype, self.shapes[shape])
+
+    def columns(self, t, name):
+        return _layer_ptr(t, name, self.index, self.dtype, (self.problem.h_out,))
 
     def table(self, t, name, dtype):
         return _layer_ptr(t, name, self.index, dtype, None, self.problem.num_loras)
@@ -569,6 +576,28 @@ def sgmv_gated_lora_backward(problem, X, Wg, Wu, gate, up, dH, seg_indptr, lora_
     a.launch("sgmv_gated_lora_backward", stream, *a.W, ctypes.byref(a.projection(gate, "gate")),
              ctypes.byref(a.projection(up, "up")), int(act), a.rows(dH, "dH", "out"), a.rows(dX, "dX", "in"),
              ctypes.byref(a.grad(gate_grad, "gate_grad")), ctypes.byref(a.grad(up_grad, "up_grad")), int(accumulate))
+
+
+def sgmv_dense_act_lora_apply(problem, X, W, proj, seg_indptr, lora_idx, ws, act=SGMV_ACT_NONE, bias=None, residual=None,
+                              Z=None, stream=None):
+    """Y[i] = act(Z[i]) + residual[i], Z[i] = X[i] @ W + bias + s_k * (X[i] @ A_k) @ B_k (Y, the projection's, written and
+    rounded once; it may be residual); `bias` [h_out], `residual` and `Z` (where to store Z for
+    sgmv_dense_act_lora_backward) [n_rows, h_out], each or None; `ws` from new_layer_workspace(problem,
+    SGMV_DENSE_ACT_FORWARD).  Asynchronous."""
+    a = _LayerArgs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws)
+    a.launch("sgmv_dense_act_lora_apply", stream, *a.W, ctypes.byref(a.projection(proj, "proj")), a.columns(bias, "bias"),
+             int(act), a.rows(residual, "residual", "out"), a.rows(Z, "Z", "out"))
+
+
+def sgmv_dense_act_lora_backward(problem, X, W, proj, dY, seg_indptr, lora_idx, ws, act=SGMV_ACT_NONE, Z=None, dX=None,
+                                 grad=None, dbias=None, accumulate=False, stream=None):
+    """Gradients of sgmv_dense_act_lora_apply from dY and the stored Z (not needed for SGMV_ACT_NONE): dX (written), `grad`
+    = (dW, dA_ptrs, dB_ptrs) and dbias, each or None, accumulated or written as in sgmv_dense_lora_backward; `ws` from
+    new_layer_workspace(problem, SGMV_DENSE_ACT_BACKWARD).  Asynchronous."""
+    a = _LayerArgs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws)
+    a.launch("sgmv_dense_act_lora_backward", stream, *a.W, ctypes.byref(a.projection(proj, "proj")), int(act),
+             a.rows(Z, "Z", "out"), a.rows(dY, "dY", "out"), a.rows(dX, "dX", "in"), ctypes.byref(a.grad(grad, "grad")),
+             a.columns(dbias, "dbias"), int(accumulate))
 
 
 # ------------------------------------------------- rows sorted by LoRA and back, layer norm

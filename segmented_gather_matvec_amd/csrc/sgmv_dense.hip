@@ -2,11 +2,12 @@
 // any number of rows.
 //
 // The LoRA paragraph of the Punica README (page "Punica：多 LoRA 模型统一服务框架")
-// gives a row x the output x@W + x@A@B.  Four products share one kernel:
+// gives a row x the output x@W + x@A@B.  Five products share one kernel:
 //     forward  Y  = X @ W + V @ B_k                       V = s_k X @ A_k
 //     gated    G, U = two forwards, H = act(G) * U
 //     dX       dX = sum_p (dY_p @ W_p^T + V_p @ A_{p,k}^T) V_p = s_k dY_p @ B_{p,k}^T
 //     dW       dW_p = X^T @ dY_p
+//     act      Z = X @ W + b + V @ B_k,  Y = act(Z) + R    (the forward product with an epilogue of its own)
 // A workgroup owns one output tile and walks the contraction in steps of 32.
 // Both operand tiles go from memory straight into LDS (no registers), one ring
 // slot per step; lanes past the matrix ask for an offset beyond the buffer
@@ -285,6 +286,88 @@ __device__ inline u32x2 round4(const f32x4& v) {
                (uint32_t)T::round(v[2]) | ((uint32_t)T::round(v[3]) << 16)};
 }
 
+// Four columns c .. c + 3 of row-major outputs at o = m N + c: Z = z + bias on request, Y = act(Z) + residual.
+template <class T>
+__device__ inline void finish_act(const DenseParams& p, int64_t o, f32x4 z, const f32x4& bias, const u32x2& res) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) z[e] += bias[e];
+  if (p.out[1]) *reinterpret_cast<u32x2*>(p.out[1] + o) = round4<T>(z);
+  act_apply<4>(p.act, z);
+  if (p.residual) {
+    z[0] += T::lo(res[0]);
+    z[1] += T::hi(res[0]);
+    z[2] += T::lo(res[1]);
+    z[3] += T::hi(res[1]);
+  }
+  *reinterpret_cast<u32x2*>(p.out[0] + o) = round4<T>(z);
+}
+template <class T>
+__device__ inline f32x4 load_bias(const DenseParams& p, int c) {
+  if (!p.bias) return f32x4{0.f, 0.f, 0.f, 0.f};
+  const u32x2 b = *reinterpret_cast<const u32x2*>(p.bias + c);
+  return f32x4{T::lo(b[0]), T::hi(b[0]), T::lo(b[1]), T::hi(b[1])};
+}
+__device__ inline u32x2 load_residual(const DenseParams& p, int64_t o) {
+  return p.residual ? *reinterpret_cast<const u32x2*>(p.residual + o) : u32x2{0u, 0u};
+}
+
+// The act epilogue of a tile.  A lane's accumulators are four columns of 16 rows here and there: 32 bytes of a row at a time, and
+// the activation inlined for each.  So they go through the ring's LDS (the product is done with it), one row of waves after the
+// other, and come back row by row: a wave reads and writes 512 (256) bytes of a row at once, the residual's rows are asked
+// for four ahead, and the activation's code is there once per four rows.  16-byte groups are swizzled by the row.
+template <class T, class S>
+__device__ inline void act_epilogue(const DenseParams& p, f32x4 (&acc)[S::TM][S::TN], uint16_t* ring, int m0, int n0,
+                                    int wave, int lane) {
+  constexpr int ROWS = S::BM / S::WM, G = S::C / 4, PER = 64 / G, STEPS = ROWS / (S::NW * PER), AHEAD = 4;
+  static_assert(ROWS * S::C * 4 <= S::STAGES * S::SLOT * 2, "a row of waves' results fit the ring");
+  static_assert(STEPS % AHEAD == 0 && ROWS % (S::NW * PER) == 0, "whole steps");
+  float* const tile = reinterpret_cast<float*>(ring);
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int q = lane >> 4, ml = lane & 15;
+  const int g = lane % G, c = n0 + g * 4;
+  const int first = wave * PER + lane / G;
+  const bool col = c < p.N;
+  const int cc = col ? c : p.N - 4;
+  const f32x4 bias = load_bias<T>(p, cc);
+  for (int h = 0; h < S::WM; ++h) {
+    const int mh = m0 + h * ROWS;
+    const auto at = [&](int s) {  // (rows past the last: the last one again, not written)
+      const int m = mh + first + s * S::NW * PER;
+      return (int64_t)(m < p.M ? m : p.M - 1) * p.N + cc;
+    };
+    u32x2 next[AHEAD];
+#pragma unroll
+    for (int u = 0; u < AHEAD; ++u) next[u] = load_residual(p, at(u));
+    __syncthreads();  // the ring, or the rows before, have been read
+    if (wm == h) {
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TNP; ++j) {
+          const int row = i * 16 + ml, group = (wn * S::TNP + j) * 4 + q;
+          *reinterpret_cast<f32x4*>(tile + row * S::C + ((group ^ (row & 7)) << 2)) = acc[i][j];
+        }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int s = 0; s < STEPS; s += AHEAD) {
+      u32x2 now[AHEAD];
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) now[u] = next[u];
+      if (s + AHEAD < STEPS) {
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) next[u] = load_residual(p, at(s + AHEAD + u));
+      }
+#pragma unroll
+      for (int u = 0; u < AHEAD; ++u) {
+        const int row = first + (s + u) * S::NW * PER;
+        const f32x4 z = *reinterpret_cast<const f32x4*>(tile + row * S::C + ((g ^ (row & 7)) << 2));
+        if (col && mh + row < p.M) finish_act<T>(p, (int64_t)(mh + row) * p.N + c, z, bias, now[u]);
+      }
+    }
+  }
+}
+
 // TERM: compiled with the LoRA term in the tiles.
 template <class T, int MODE, class S, bool TERM>
 __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* ring) {
@@ -468,6 +551,10 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
       }
     }
   }
+  if constexpr (MODE == kDenseAct) {  // (partial planes are the forward mode's)
+    act_epilogue<T, S>(p, acc, ring, m0, n0, wave, lane);
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int m = mw + i * 16 + ml;
@@ -638,7 +725,7 @@ __device__ inline void row_term(const DenseParams& p, const float* v, const uint
 
 template <class T, int MODE>
 __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) {
-  constexpr int NT = MODE == kDenseForward ? 1 : 2;  // LoRA terms
+  constexpr int NT = MODE == kDenseForward || MODE == kDenseAct ? 1 : 2;  // LoRA terms
   constexpr int NP = MODE == kDenseGated ? 2 : 1;    // projections' planes
   constexpr int kBatch = 16;
   __shared__ __attribute__((aligned(16))) float lds_v[NT][64];
@@ -673,6 +760,12 @@ __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) 
   PlaneBatch x[NP];
 #pragma unroll
   for (int n = 0; n < NP; ++n) load_planes(p, n, o, 0, x[n]);
+  f32x4 bias;
+  u32x2 res;
+  if constexpr (MODE == kDenseAct) {
+    bias = load_bias<T>(p, col ? c : 0);
+    res = load_residual(p, o);
+  }
 
   if (terms) {
     if (p.row_k == nullptr) {
@@ -732,6 +825,8 @@ __global__ __launch_bounds__(64) void sgmv_dense_epilogue_kernel(DenseParams p) 
     if (p.out[0]) *reinterpret_cast<u32x2*>(p.out[0] + o) = round4<T>(y);
     if (p.out[1]) *reinterpret_cast<u32x2*>(p.out[1] + o) = round4<T>(u);
     *reinterpret_cast<u32x2*>(p.out[2] + o) = round4<T>(h);
+  } else if constexpr (MODE == kDenseAct) {
+    finish_act<T>(p, o, y, bias, res);
   } else {
     if constexpr (MODE == kDenseDx) row_term<T, MODE>(p, lds_v[1], E[1], rk[1], c, m[1], y);
     *reinterpret_cast<u32x2*>(p.out[0] + o) = round4<T>(y);
@@ -757,7 +852,13 @@ __global__ __launch_bounds__(kThreads) void sgmv_dense_sum_kernel(DenseParams p)
       for (int e = 0; e < 4; ++e) y[n][4 * h + e] = v[e];
     }
   }
-  if constexpr (MODE == kDenseGated) {
+  if constexpr (MODE == kDenseAct) {
+    const int c = (int)(o % p.N);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      finish_act<T>(p, o + 4 * h, f32x4{y[0][4 * h], y[0][4 * h + 1], y[0][4 * h + 2], y[0][4 * h + 3]},
+                    load_bias<T>(p, c + 4 * h), load_residual(p, o + 4 * h));
+  } else if constexpr (MODE == kDenseGated) {
     float h[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = act_value(p.act, y[0][e]) * y[1][e];
@@ -819,6 +920,8 @@ hipError_t launch_t(int mode, int cfg, const DenseParams& p, hipStream_t s) {
     case kDenseForward: return launch_mode<T, kDenseForward>(cfg, p, s);
     case kDenseGated: return launch_mode<T, kDenseGated>(cfg, p, s);
     case kDenseDx: return launch_mode<T, kDenseDx>(cfg, p, s);
+    case kDenseAct:  // (planes know nothing of the epilogue)
+      return p.to_planes ? launch_mode<T, kDenseForward>(cfg, p, s) : launch_mode<T, kDenseAct>(cfg, p, s);
     case kDenseDw:
       return cfg == kTile256 ? launch_tile<T, kDenseDw, 256, 256, 2, 4, 4, 2>(p, s)
                              : launch_tile<T, kDenseDw, 128, 128, 2, 2, 4, 2>(p, s);
@@ -845,6 +948,7 @@ hipError_t launch_epilogue_t(int mode, const DenseParams& p, hipStream_t s) {
     case kDenseForward: return launch_epilogue_mode<T, kDenseForward>(p, s);
     case kDenseGated: return launch_epilogue_mode<T, kDenseGated>(p, s);
     case kDenseDx: return launch_epilogue_mode<T, kDenseDx>(p, s);
+    case kDenseAct: return launch_epilogue_mode<T, kDenseAct>(p, s);
   }
   return hipErrorInvalidValue;
 }
@@ -862,7 +966,7 @@ hipError_t launch_dense_thin(int dtype, int mode, int cfg, const DenseParams& p,
   if (mode == kDenseGated)
     return dtype == 1 ? launch_mode_thin<BF16, kDenseGated>(cfg, p, t, count, stream)
                       : launch_mode_thin<F16, kDenseGated>(cfg, p, t, count, stream);
-  if (mode == kDenseForward)
+  if (mode == kDenseForward || mode == kDenseAct)
     return dtype == 1 ? launch_mode_thin<BF16, kDenseForward>(cfg, p, t, count, stream)
                       : launch_mode_thin<F16, kDenseForward>(cfg, p, t, count, stream);
   return hipErrorInvalidValue;

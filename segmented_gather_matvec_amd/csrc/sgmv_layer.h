@@ -35,7 +35,8 @@ enum DenseMode : int {
   kDenseForward = 0,  // Y = X @ W + term                  A: X, B[0]: W
   kDenseGated = 1,    // G, U two forwards, H = act(G) * U A: X, B[0], B[1]: Wg, Wu
   kDenseDx = 2,       // dX = sum_p dY_p @ W_p^T + terms    A[p]: dY_p, B[p]: W_p
-  kDenseDw = 3        // dW_p = X^T @ dY_p                  A[0]: X, B[p]: dY_p, p = blockIdx.y
+  kDenseDw = 3,       // dW_p = X^T @ dY_p                  A[0]: X, B[p]: dY_p, p = blockIdx.y
+  kDenseAct = 4       // Z = X @ W + bias + term, Y = act(Z) + residual   A: X, B[0]: W
 };
 
 struct DenseParams {
@@ -58,7 +59,9 @@ struct DenseParams {
   int64_t plane_stride;  // floats between planes of one projection's output (M * N)
   const uint16_t* A[2];
   const uint16_t* B[2];
-  uint16_t* out[3];      // forward: Y; gated: G, U (both may be null), H; dX: dX; dW: dW_0, dW_1
+  uint16_t* out[3];      // forward: Y; gated: G, U (both may be null), H; dX: dX; dW: dW_0, dW_1; act: Y, Z (may be null)
+  const uint16_t* bias;      // act: [N], or null
+  const uint16_t* residual;  // act: [M, N] (may be Y itself), or null
   float* planes;         // [projection][ksplit][M][N] (gated: projections g, u)
   SegMeta meta;
   LowRankTerm term[2];
@@ -127,5 +130,20 @@ hipError_t launch_lora_grad(int dtype, const LoraGradParams* p, int count, hipSt
 hipError_t launch_gate_backward(int dtype, int act, bool halves, const uint16_t* G, const uint16_t* U,
                                 const uint16_t* dH, uint16_t* dG, uint16_t* dU, int8_t* row_power, int32_t n, int32_t F,
                                 hipStream_t stream);
+
+// dZ = dY * act'(Z) ([n, F]), rounded once to the 16-bit format, or (halves) as hi halves followed by lo halves; fp16:
+// every row divided by its power_of(row_power[i]), written.  planes: null, or [blocks][F], the column sums of the
+// unrounded dZ over each block of rows.  act none: dY's column sums alone.
+struct ActBackwardParams {
+  const uint16_t* Z;
+  const uint16_t* dY;
+  uint16_t* dZ;       // null: act none
+  int8_t* row_power;  // fp16
+  float* planes;
+  int32_t n, F, act;
+  int32_t halves;
+  int32_t rows_per_block;
+};
+hipError_t launch_act_backward(int dtype, const ActBackwardParams& p, hipStream_t stream);
 
 }  // namespace sgmv

@@ -4,6 +4,7 @@
 #include <cstdint>
 
 #include "../../include/sgmv.h"
+#include "sgmv_block.h"
 #include "sgmv_layer.h"
 #include "sgmv_layer_host.h"
 
@@ -160,21 +161,26 @@ sgmv_status_t run_dense(const Call& c, int mode, const DensePlan& d, const sgmv:
   return sgmv::launch_dense_epilogue(c.p.dtype, mode, e, c.stream) == hipSuccess ? SGMV_OK : SGMV_ERR_HIP;
 }
 
-sgmv_status_t forward(const Call& c, void* const* out) {
+// epilogue: null, or the bias and residual of a dense layer with an activation (out: Y, Z).
+sgmv_status_t forward(const Call& c, void* const* out, const void* const* epilogue = nullptr) {
   const void* Z[2] = {c.X, c.X};
   if (c.plan.lora && !c.plan.one_launch) {
     const sgmv_status_t st = thin(c, false, Z, !c.plan.out.term_in_tile, c.plan.out.term_in_tile);
     if (st != SGMV_OK) return st;
   }
   const bool gated = layer_gated(c.op);
-  const int mode = gated ? sgmv::kDenseGated : sgmv::kDenseForward;
+  const int mode = gated ? sgmv::kDenseGated : epilogue ? sgmv::kDenseAct : sgmv::kDenseForward;
   sgmv::DenseParams q = dense_params(c, c.plan.out, c.p.n_rows, c.p.h_out, c.p.h_in, c.p.h_in, c.p.h_out);
   q.A[0] = half(c.X);
   for (int i = 0; i < c.np; ++i) {
     q.B[i] = half(c.W[i]);
     if (c.plan.lora) q.term[i] = term(c, i, false);
   }
-  for (int i = 0; i < (gated ? 3 : 1); ++i) q.out[i] = static_cast<uint16_t*>(out[i]);
+  for (int i = 0; i < (gated ? 3 : epilogue ? 2 : 1); ++i) q.out[i] = static_cast<uint16_t*>(out[i]);
+  if (epilogue) {
+    q.bias = half(epilogue[0]);
+    q.residual = half(epilogue[1]);
+  }
   if (!c.plan.one_launch) return run_dense(c, mode, c.plan.out, q);
   sgmv::ThinParams t[2];
   thin_params(c, false, Z, true, false, t);
@@ -288,6 +294,8 @@ sgmv_status_t check_grads(const sgmv_projection_grad_t* const* grad, int np, con
   return SGMV_OK;
 }
 
+bool epilogue_act(int32_t act) { return act >= SGMV_ACT_SILU && act <= SGMV_ACT_GELU; }
+
 }  // namespace
 
 extern "C" {
@@ -390,6 +398,75 @@ sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* p, const void* X, c
     return SGMV_ERR_HIP;
   const void* dY[2] = {d[0], d[1]};
   return backward(c, dY, dX, g, accumulate);
+}
+
+sgmv_status_t sgmv_dense_act_lora_apply(const sgmv_problem_t* p, const void* X, const void* W,
+                                        const sgmv_projection_t* proj, const void* bias, int32_t act,
+                                        const void* residual, void* Z, const int32_t* seg_indptr, const int32_t* lora_idx,
+                                        void* ws, size_t ws_bytes, void* stream) {
+  sgmv_status_t st = check_layer(p);
+  if (st != SGMV_OK) return st;
+  if (!epilogue_act(act)) return SGMV_ERR_INVALID_ARG;
+  if (p->n_rows == 0) return SGMV_OK;
+  if (!proj || !proj->Y) return SGMV_ERR_INVALID_ARG;
+  const LayerPlan plan = plan_layer(*p, SGMV_DENSE_ACT_FORWARD);
+  st = check_call(X, &W, &proj, 1, seg_indptr, lora_idx, ws, ws_bytes, plan);
+  if (st != SGMV_OK) return st;
+  if (misaligned(bias, 16) || misaligned(residual, 16) || misaligned(Z, 16)) return SGMV_ERR_UNSUPPORTED;
+  const Call c{*p, SGMV_DENSE_ACT_FORWARD, plan, 1, X, {W, nullptr}, {proj, nullptr},
+               seg_meta(*p, plan.lora, seg_indptr, lora_idx), static_cast<char*>(ws),
+               static_cast<hipStream_t>(stream), act};
+  void* out[2] = {proj->Y, Z};
+  const void* epilogue[2] = {bias, residual};
+  return forward(c, out, epilogue);
+}
+
+sgmv_status_t sgmv_dense_act_lora_backward(const sgmv_problem_t* p, const void* X, const void* W,
+                                           const sgmv_projection_t* proj, int32_t act, const void* Z, const void* dY,
+                                           void* dX, const sgmv_projection_grad_t* grad, void* dbias, int32_t accumulate,
+                                           const int32_t* seg_indptr, const int32_t* lora_idx, void* ws, size_t ws_bytes,
+                                           void* stream) {
+  sgmv_status_t st = check_layer(p);
+  if (st != SGMV_OK) return st;
+  if (!epilogue_act(act)) return SGMV_ERR_INVALID_ARG;
+  if (accumulate != 0 && accumulate != 1) return SGMV_ERR_INVALID_ARG;
+  const sgmv_projection_grad_t none{};
+  const sgmv_projection_grad_t* g = grad ? grad : &none;
+  const bool rows = p->n_rows > 0, slopes = act != SGMV_ACT_NONE;
+  if (!proj || (rows && (!dY || (slopes && !Z)))) return SGMV_ERR_INVALID_ARG;
+  const ActPlan a = plan_act_backward(*p, act);
+  if (rows) {
+    st = check_call(X, &W, &proj, 1, seg_indptr, lora_idx, ws, ws_bytes, a.layer);
+    if (st != SGMV_OK) return st;
+    if (dbias && (!ws || ws_bytes < a.total)) return SGMV_ERR_WORKSPACE;
+  }
+  if (misaligned(dY, 16) || misaligned(Z, 16) || misaligned(dbias, 16)) return SGMV_ERR_UNSUPPORTED;
+  st = check_grads(&g, 1, dX);
+  if (st != SGMV_OK) return st;
+  const Call c{*p, slopes ? SGMV_DENSE_ACT_BACKWARD : SGMV_DENSE_BACKWARD, a.layer, 1, X, {W, nullptr}, {proj, nullptr},
+               seg_meta(*p, a.layer.lora, seg_indptr, lora_idx), static_cast<char*>(ws),
+               static_cast<hipStream_t>(stream), act};
+  float* planes = dbias ? c.at(a.planes_off) : nullptr;
+  uint16_t* dZ = slopes ? reinterpret_cast<uint16_t*>(c.at(a.layer.gate_off[0])) : nullptr;
+  if (rows) {
+    sgmv::ActBackwardParams e{};
+    e.Z = half(Z);
+    e.dY = half(dY);
+    e.dZ = dZ;
+    e.row_power = c.row_power();
+    e.planes = planes;
+    e.n = p->n_rows;
+    e.F = p->h_out;
+    e.act = act;
+    e.halves = a.layer.halves > 1;
+    e.rows_per_block = a.rows_per_block;
+    if (sgmv::launch_act_backward(p->dtype, e, c.stream) != hipSuccess) return SGMV_ERR_HIP;
+  }
+  if (sgmv::launch_plane_sum(p->dtype, planes, rows ? a.blocks : 0, 1, p->h_out, static_cast<uint16_t*>(dbias), nullptr,
+                             accumulate, c.stream) != hipSuccess)
+    return SGMV_ERR_HIP;
+  const void* d = slopes ? dZ : dY;
+  return backward(c, &d, dX, &g, accumulate);
 }
 
 }  // extern "C"

@@ -151,7 +151,7 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   l.projections = layer_gated(op) ? 2 : 1;
   l.lora = !nothing_to_do(p);
   const int64_t n = p.n_rows;
-  l.halves = op == SGMV_GATED_BACKWARD && n <= kHalvesRows && n * p.h_out <= kHalvesValues ? 2 : 1;
+  l.halves = layer_elementwise(op) && n <= kHalvesRows && n * p.h_out <= kHalvesValues ? 2 : 1;
   const bool back = layer_backward(op);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
@@ -172,8 +172,8 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
       }
     }
   }
-  if (op == SGMV_GATED_BACKWARD) {
-    for (int i = 0; i < 2; ++i) l.gate_off[i] = take((size_t)n * l.halves * p.h_out * 2);
+  if (layer_elementwise(op)) {
+    for (int i = 0; i < l.projections; ++i) l.gate_off[i] = take((size_t)n * l.halves * p.h_out * 2);
     l.row_powers = p.dtype == SGMV_F16;
     if (l.row_powers) l.row_power_off = take((size_t)n);
   }
@@ -181,7 +181,7 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   const bool in_tile = l.lora && tiles_add_term(p, back, l.projections, N);
   const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK);
   const int cols = op == SGMV_GATED_FORWARD ? 2 : 1;
-  l.out = plan_dense(M, N, kt * (op == SGMV_GATED_BACKWARD ? 2 : 1), cols, true);
+  l.out = plan_dense(M, N, kt * (back ? l.projections : 1), cols, true);
   l.out.term_in_tile = in_tile ? 1 : 0;
   l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile) || l.halves > 1;
   // (The large tiles' workgroups are too big to share a launch with.)
@@ -205,6 +205,19 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   return l;
 }
 
+ActPlan plan_act_backward(const sgmv_problem_t& p, int act) {
+  ActPlan a;
+  a.layer = plan_layer(p, act == SGMV_ACT_NONE ? SGMV_DENSE_BACKWARD : SGMV_DENSE_ACT_BACKWARD);
+  // Blocks of rows by 2048 columns: some workgroups a CU, each of eight rows and more (their sums are written and read).
+  const int64_t chunks = ceil_div(p.h_out, 2048);
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(ceil_div(1536, chunks), ceil_div(p.n_rows, 8)));
+  a.rows_per_block = (int32_t)std::max<int64_t>(1, ceil_div(p.n_rows, blocks));
+  a.blocks = (int32_t)ceil_div(p.n_rows, a.rows_per_block);
+  a.planes_off = (size_t)round_up((int64_t)a.layer.total, 256);
+  a.total = a.planes_off + (size_t)a.blocks * p.h_out * sizeof(float);
+  return a;
+}
+
 }  // namespace sgmv_host
 
 using namespace sgmv_host;
@@ -214,8 +227,18 @@ extern "C" {
 sgmv_status_t sgmv_layer_workspace_bytes(const sgmv_problem_t* p, int32_t op, size_t* bytes) {
   const sgmv_status_t st = check_layer(p);
   if (st != SGMV_OK) return st;
-  if (!bytes || op < SGMV_DENSE_FORWARD || op > SGMV_GATED_BACKWARD) return SGMV_ERR_INVALID_ARG;
-  *bytes = plan_layer(*p, op).total;
+  if (!bytes) return SGMV_ERR_INVALID_ARG;
+  switch (op) {
+    case SGMV_DENSE_FORWARD:
+    case SGMV_DENSE_BACKWARD:
+    case SGMV_GATED_FORWARD:
+    case SGMV_GATED_BACKWARD:
+    case SGMV_DENSE_ACT_FORWARD: *bytes = plan_layer(*p, op).total; break;
+    case SGMV_DENSE_ACT_BACKWARD:  // of any activation
+      *bytes = std::max(plan_act_backward(*p, SGMV_ACT_NONE).total, plan_act_backward(*p, SGMV_ACT_SILU).total);
+      break;
+    default: return SGMV_ERR_INVALID_ARG;
+  }
   return SGMV_OK;
 }
 

@@ -44,10 +44,23 @@ struct LayerPlan {
 };
 
 inline bool layer_gated(int op) { return op == SGMV_GATED_FORWARD || op == SGMV_GATED_BACKWARD; }
-inline bool layer_backward(int op) { return op == SGMV_DENSE_BACKWARD || op == SGMV_GATED_BACKWARD; }
+inline bool layer_backward(int op) {
+  return op == SGMV_DENSE_BACKWARD || op == SGMV_GATED_BACKWARD || op == SGMV_DENSE_ACT_BACKWARD;
+}
+// The backward pass starts from elementwise products of its own (dG and dU, dZ).
+inline bool layer_elementwise(int op) { return op == SGMV_GATED_BACKWARD || op == SGMV_DENSE_ACT_BACKWARD; }
 // The shape's checks, the rows that the tiles' 32-bit row numbers reach, the units that one launch holds (a
 // workgroup each; a launch has fewer than 2^32 threads), and the segments that every unit may walk.
 sgmv_status_t check_layer(const sgmv_problem_t* p);
 LayerPlan plan_layer(const sgmv_problem_t& p, int op);
+
+// The backward call of a dense layer with an activation: the layer's plan (without an activation it is the plain dense
+// layer's) and the planes of the bias's gradient behind its workspace.
+struct ActPlan {
+  LayerPlan layer;
+  int32_t rows_per_block = 1, blocks = 1;
+  size_t planes_off = 0, total = 0;
+};
+ActPlan plan_act_backward(const sgmv_problem_t& p, int act);
 
 }  // namespace sgmv_host

@@ -101,4 +101,40 @@ __device__ inline void act_both(int act, float g, float& value, float& slope) {
   slope = t == 0.f ? s : __builtin_fmaf(g * d, t, s);
 }
 
+// Activations of the dense call with an epilogue (sgmv_act_t).  The logistic function by the hardware's exponential and
+// reciprocal, good to some units in the last place (and |x| 2^-24 of the argument's own rounding): far below a 16-bit output's
+// rounding, at a third of the instructions of expf and a division, which show in a tile's epilogue.
+__device__ inline float fast_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.4426950408889634f * x));
+}
+constexpr int kActSilu = 0, kActGeluTanh = 1, kActNone = 2, kActRelu = 3, kActGelu = 4;
+template <int N, class V>
+__device__ inline void act_apply(int act, V& z) {
+  if (act == kActRelu) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) z[e] = z[e] < 0.f ? 0.f : z[e];  // (NaN stays)
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) z[e] *= fast_sigmoid(z[e]);
+  } else if (act == kActGeluTanh) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) z[e] *= fast_sigmoid(gelu_arg2(z[e]));
+  } else if (act == kActGelu) {
+    // z Phi(z), Phi(z) = erfc(-z / sqrt 2) / 2: no cancellation far below 0.
+#pragma unroll
+    for (int e = 0; e < N; ++e) z[e] *= 0.5f * erfcf(-0.70710678118654752f * z[e]);
+  }
+}
+// The derivative at z.
+__device__ inline float act_slope(int act, float z) {
+  if (act == kActRelu) return z > 0.f ? 1.f : z != z ? z : 0.f;
+  if (act == kActGelu) {
+    const float bell = 0.3989422804014327f * expf(-0.5f * z * z);  // 0 far out, where z may be infinite
+    return 0.5f * erfcf(-0.70710678118654752f * z) + (bell == 0.f ? 0.f : z * bell);
+  }
+  float value, slope;
+  act_both(act, z, value, slope);
+  return slope;
+}
+
 }  // namespace sgmv
