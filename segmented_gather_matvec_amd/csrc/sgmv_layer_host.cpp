@@ -208,9 +208,9 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
 ActPlan plan_act_backward(const sgmv_problem_t& p, int act) {
   ActPlan a;
   a.layer = plan_layer(p, act == SGMV_ACT_NONE ? SGMV_DENSE_BACKWARD : SGMV_DENSE_ACT_BACKWARD);
-  // Blocks of rows by 2048 columns: some workgroups a CU, each of eight rows and more (their sums are written and read).
+  // Blocks of rows by 2048 columns: some workgroups a CU, each of four rows and more (their sums are written and read).
   const int64_t chunks = ceil_div(p.h_out, 2048);
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(ceil_div(1536, chunks), ceil_div(p.n_rows, 8)));
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(ceil_div(1536, chunks), ceil_div(p.n_rows, 4)));
   a.rows_per_block = (int32_t)std::max<int64_t>(1, ceil_div(p.n_rows, blocks));
   a.blocks = (int32_t)ceil_div(p.n_rows, a.rows_per_block);
   a.planes_off = (size_t)round_up((int64_t)a.layer.total, 256);
