@@ -7,6 +7,7 @@ namespace sgmv_host {
 
 namespace {
 
+constexpr int64_t kCus = 256;                 // compute units of an MI355X
 constexpr int kRouteWaves = 16;
 constexpr int64_t kRouteTile = 2048;          // entries of a workgroup, at least
 constexpr int64_t kRouteCounts = 1 << 16;     // counts that every workgroup reads, at most
@@ -47,11 +48,11 @@ NormPlan plan_norm(int32_t n_rows, int32_t width, bool back) {
   const sgmv::NormVariant& s = v[p.variant];
   const int64_t groups = std::max<int64_t>(1, ceil_div(n_rows, s.rows));
   if (!back) {
-    p.grid = (int32_t)std::min<int64_t>(groups, 2048);
+    p.grid = (int32_t)std::min<int64_t>(groups, kCus * s.per_cu);
     return p;
   }
   if (s.keep > 0) {
-    p.grid = (int32_t)std::min<int64_t>(groups, 512);
+    p.grid = (int32_t)std::min<int64_t>(groups, kCus * s.per_cu);
   } else {
     // Wide rows: (column chunks) x (row blocks).
     const int64_t chunks = ceil_div(width, sgmv::kNormWideCols);

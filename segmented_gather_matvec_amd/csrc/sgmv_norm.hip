@@ -120,7 +120,7 @@ __global__ __launch_bounds__(W * 64 > kThreads ? W * 64 : kThreads) void sgmv_la
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[k][e] *= f[e];
       }
-      if (live[k]) store_vec(p.Y + row * width + c[k], pack8<T>(x[k]));
+      if (live[k]) store_stream(p.Y + row * width + c[k], pack8<T>(x[k]));
     }
   }
 }
@@ -180,7 +180,7 @@ template <class T, int W, int KEEP, int ROWS>
 __global__ __launch_bounds__(W * 64 * ROWS) void sgmv_layer_norm_backward_kernel(NormParams p) {
   constexpr int TPR = W * 64;
   __shared__ float red[ROWS][2][W][2];
-  __shared__ __attribute__((aligned(16))) float joined[ROWS > 1 ? TPR * KEEP * 8 : 1];
+  __shared__ float joined[ROWS > 1 ? ROWS / 2 : 1][2][ROWS > 1 ? TPR * KEEP * 8 : 1];
   const int t = (int)threadIdx.x % TPR;
   const int sub = __builtin_amdgcn_readfirstlane(threadIdx.x / TPR);
   const float count = (float)(p.w8 * 8);
@@ -270,46 +270,47 @@ __global__ __launch_bounds__(W * 64 * ROWS) void sgmv_layer_norm_backward_kernel
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[e] += o[e];
       }
-      if (on && live[k]) store_vec(p.dX + row * width + c[k], pack8<T>(d));
+      if (on && live[k]) store_stream(p.dX + row * width + c[k], pack8<T>(d));
     }
   }
   if (p.planes == nullptr) return;
-  float* const plane = p.planes + (int64_t)blockIdx.x * 2 * width;
+  // The rows' sums of the workgroup, halves onto halves.
+  if constexpr (ROWS > 1) {
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    if constexpr (ROWS > 1) {
-      for (int from = ROWS - 1; from > 0; --from) {  // the last group's sums onto the one before it
-        __syncthreads();
-        if (sub == from) {
+    for (int s = ROWS / 2; s > 0; s /= 2) {
+      __syncthreads();
+      if (sub >= s && sub < 2 * s) {
 #pragma unroll
-          for (int k = 0; k < KEEP; ++k)
+        for (int k = 0; k < KEEP; ++k)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) joined[(k * 8 + e) * TPR + t] = half ? sb[k][e] : sg[k][e];
-        }
-        __syncthreads();
-        if (sub == from - 1) {
+          for (int e = 0; e < 8; ++e) {
+            joined[sub - s][0][(k * 8 + e) * TPR + t] = sg[k][e];
+            joined[sub - s][1][(k * 8 + e) * TPR + t] = sb[k][e];
+          }
+      }
+      __syncthreads();
+      if (sub < s) {
 #pragma unroll
-          for (int k = 0; k < KEEP; ++k)
+        for (int k = 0; k < KEEP; ++k)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float v = joined[(k * 8 + e) * TPR + t];
-              if (half)
-                sb[k][e] += v;
-              else
-                sg[k][e] += v;
-            }
-        }
+          for (int e = 0; e < 8; ++e) {
+            sg[k][e] += joined[sub][0][(k * 8 + e) * TPR + t];
+            sb[k][e] += joined[sub][1][(k * 8 + e) * TPR + t];
+          }
       }
     }
-    if (sub == 0) {
+  }
+  if (sub > 0) return;
+  float* const plane = p.planes + (int64_t)blockIdx.x * 2 * width;
 #pragma unroll
-      for (int k = 0; k < KEEP; ++k) {
-        if (!live[k]) continue;
-        float* dst = plane + half * width + c[k];
-        const float(&v)[8] = half ? sb[k] : sg[k];
-        *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
-        *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
-      }
+  for (int k = 0; k < KEEP; ++k) {
+    if (!live[k]) continue;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float* dst = plane + half * width + c[k];
+      const float(&v)[8] = half ? sb[k] : sg[k];
+      *reinterpret_cast<f32x4*>(dst) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4*>(dst + 4) = f32x4{v[4], v[5], v[6], v[7]};
     }
   }
 }

@@ -58,12 +58,20 @@ __global__ __launch_bounds__(kRouteThreads) void sgmv_route_kernel(RouteParams p
   int* const mine = hist + wave * keys;
   for (int64_t e = first + lane; e < last; e += 64) atomicAdd(&mine[route_key(p, (int)e)], 1);
   if (p.blocks > 1) {
-    // (Sums of integers: their order does not show.)
-    for (int x = t; x < p.blocks * keys; x += kRouteThreads) {
-      const int b = x / keys, k = x - b * keys, c = p.counts[x];
-      if (c == 0) continue;
-      atomicAdd(&total[k], c);
-      if (b < (int)blockIdx.x) atomicAdd(&before[k], c);
+    // With few keys several threads share one, each with every slices-th tile.  (Sums of integers: their order does not show.)
+    int lanes = 64;
+    while (lanes < keys && lanes < kRouteThreads) lanes *= 2;
+    const int slices = kRouteThreads / lanes;
+    for (int k = t & (lanes - 1); k < keys; k += kRouteThreads) {
+      int all = 0, early = 0;
+#pragma unroll 4
+      for (int b = t / lanes; b < p.blocks; b += slices) {
+        const int c = p.counts[(int64_t)b * keys + k];
+        all += c;
+        early += b < (int)blockIdx.x ? c : 0;
+      }
+      atomicAdd(&total[k], all);
+      atomicAdd(&before[k], early);
     }
   }
   __syncthreads();
@@ -159,12 +167,14 @@ __global__ __launch_bounds__(kThreads) void sgmv_dispatch_kernel(RowsParams p) {
       uint16_t* dst = p.out + (int64_t)slot * p.w8 * 8;
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        if (c0 + v * L < p.w8) store_vec(dst + (int64_t)(c0 + v * L) * 8, x[v]);
+        if (c0 + v * L < p.w8) store_stream(dst + (int64_t)(c0 + v * L) * 8, x[v]);
     }
   }
 }
 
-// JB: choices whose rows are asked for together.
+// JB: choices whose rows are asked for together.  V: 4 of a wave's vectors where rows are wide and many (one choice, 16384 rows of 4096:
+// 61 us with 2, 49 with 4, and 45 with stores past the caches, which cost two choices 37 -> 43), 2 for a few rows (one row
+// 2.5 -> 2.2 us).
 template <class T, int L, int V, int JB>
 __global__ __launch_bounds__(kThreads) void sgmv_combine_kernel(RowsParams p) {
   constexpr int ROWS = kThreads / L;
@@ -217,19 +227,23 @@ __global__ __launch_bounds__(kThreads) void sgmv_combine_kernel(RowsParams p) {
     }
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (c0 + v * L < p.w8) store_vec(p.out + (row * p.w8 + c[v]) * 8, pack8<T>(y[v]));
+      if (c0 + v * L < p.w8) {
+        uint16_t* const dst = p.out + (row * p.w8 + c[v]) * 8;
+        JB == 1 ? store_stream(dst, pack8<T>(y[v])) : store_vec(dst, pack8<T>(y[v]));
+      }
   }
 }
 
-// W waves an entry (its dot product needs the whole row): one where there are entries enough.
-template <class T, int W>
+// TPE threads an entry (its dot product needs the whole row): a wave where there are entries enough, fewer lanes for narrow
+// rows (131072 entries of 64 values: 60 us with a wave each, 10 with eight lanes).
+template <class T, int TPE>
 __global__ __launch_bounds__(kThreads) void sgmv_combine_backward_kernel(RowsParams p) {
-  constexpr int TPE = W * 64, ENTRIES = kThreads / TPE, V = 4;
+  constexpr int ENTRIES = kThreads / TPE, V = TPE < 64 ? 1 : 4;
   __shared__ float part[kWaves];
   const int t = threadIdx.x % TPE;
   const int64_t m = (int64_t)p.n * p.top_k;
   for (int64_t e0 = (int64_t)blockIdx.x * ENTRIES; e0 < m; e0 += (int64_t)gridDim.x * ENTRIES) {
-    const int64_t e = e0 + __builtin_amdgcn_readfirstlane(threadIdx.x / TPE);
+    const int64_t e = e0 + (TPE < 64 ? (int)threadIdx.x / TPE : __builtin_amdgcn_readfirstlane(threadIdx.x / TPE));
     float dot = 0.f;
     if (e < m) {
       const int64_t row = e / p.top_k;
@@ -258,21 +272,21 @@ __global__ __launch_bounds__(kThreads) void sgmv_combine_backward_kernel(RowsPar
             dot = live ? __builtin_fmaf(f[x], g[x], dot) : dot;
             f[x] = w != 0.f ? f[x] * w : 0.f;
           }
-          if (live && dys != nullptr) store_vec(dys + (int64_t)(c0 + v * TPE) * 8, pack8<T>(f));
+          if (live && dys != nullptr) store_stream(dys + (int64_t)(c0 + v * TPE) * 8, pack8<T>(f));
         }
       }
       if (!there) dot = 0.f;
     }
     if (p.dweights == nullptr) continue;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) dot += shfl_xor(dot, d);
-    if constexpr (W > 1) {
+    for (int d = 1; d < (TPE < 64 ? TPE : 64); d <<= 1) dot += shfl_xor(dot, d);
+    if constexpr (TPE > 64) {
       __syncthreads();  // the entry before has been read
       if ((t & 63) == 0) part[t >> 6] = dot;
       __syncthreads();
       dot = 0.f;
 #pragma unroll
-      for (int x = 0; x < W; ++x) dot += part[x];
+      for (int x = 0; x < TPE / 64; ++x) dot += part[x];
     }
     if (t == 0 && e < m) p.dweights[e] = dot;
   }
@@ -307,17 +321,22 @@ hipError_t launch_combine_t(const RowsParams& p, hipStream_t s) {
     case 16: return launch_combine_l<T, 16, 1>(p, s);
     case 32: return launch_combine_l<T, 32, 1>(p, s);
   }
-  return launch_combine_l<T, 64, 2>(p, s);
+  if (p.w8 <= 64) return launch_combine_l<T, 64, 1>(p, s);
+  if (p.w8 <= 128 || (int64_t)p.n * p.w8 < (1 << 18)) return launch_combine_l<T, 64, 2>(p, s);
+  return launch_combine_l<T, 64, 4>(p, s);
 }
 
 template <class T>
 hipError_t launch_combine_backward_t(const RowsParams& p, hipStream_t s) {
   const int64_t m = (int64_t)p.n * p.top_k;
-  if (m < 2048 && p.w8 > 64) {
-    hipLaunchKernelGGL((sgmv_combine_backward_kernel<T, 4>), dim3((unsigned)m), dim3(kThreads), 0, s, p);
-  } else {
-    const int64_t blocks = std::min<int64_t>((m + kWaves - 1) / kWaves, kMostBlocks);
-    hipLaunchKernelGGL((sgmv_combine_backward_kernel<T, 1>), dim3((unsigned)blocks), dim3(kThreads), 0, s, p);
+  const int lanes = m < 2048 && p.w8 > 64 ? kThreads : lanes_of(p.w8), per = kThreads / lanes;
+  const dim3 grid((unsigned)std::min<int64_t>((m + per - 1) / per, kMostBlocks)), block(kThreads);
+  switch (lanes) {
+    case 8: hipLaunchKernelGGL((sgmv_combine_backward_kernel<T, 8>), grid, block, 0, s, p); break;
+    case 16: hipLaunchKernelGGL((sgmv_combine_backward_kernel<T, 16>), grid, block, 0, s, p); break;
+    case 32: hipLaunchKernelGGL((sgmv_combine_backward_kernel<T, 32>), grid, block, 0, s, p); break;
+    case 64: hipLaunchKernelGGL((sgmv_combine_backward_kernel<T, 64>), grid, block, 0, s, p); break;
+    default: hipLaunchKernelGGL((sgmv_combine_backward_kernel<T, kThreads>), grid, block, 0, s, p);
   }
   return hipGetLastError();
 }
