@@ -910,6 +910,9 @@ hipError_t launch_mode(int cfg, const DenseParams& p, hipStream_t s) {
     case kTile128: return launch_tile<T, MODE, 128, 128, 2, 2, 4, 2>(p, s);
     case kTile64: return launch_tile<T, MODE, 64, 256, 1, 4, 4, 2>(p, s);
     case kTile32: return launch_tile<T, MODE, 32, 256, 1, 4, 4, 2>(p, s);
+    case kTile128Wide:
+      if constexpr (MODE == kDenseAct || MODE == kDenseDx) return launch_tile<T, MODE, 128, 256, 2, 4, 4, 2>(p, s);
+      break;
   }
   return hipErrorInvalidValue;
 }

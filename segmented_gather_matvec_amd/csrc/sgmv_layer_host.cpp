@@ -38,7 +38,7 @@ bool tiles_add_term(const sgmv_problem_t& p, bool back, int terms, int64_t N) {
 }
 
 // Workgroups of a tile shape that run at once on one CU (LDS).
-int resident(int cfg) { return cfg <= sgmv::kTile192 ? 1 : 2; }
+int resident(int cfg) { return cfg <= sgmv::kTile192 || cfg == sgmv::kTile128Wide ? 1 : 2; }
 
 // The model that picks between tile shapes and splits; only ratios matter.
 // Large tiles are bound by the matrix cores: microseconds of one contraction
@@ -48,8 +48,12 @@ int resident(int cfg) { return cfg <= sgmv::kTile192 ? 1 : 2; }
 // CU), 1300 rows 4096 -> 11008 146 us (four), but dX of 5000 rows 11008 -> 4096 590 us (five; 192 rows: 520).
 // Without the 192-row tile (it fills rounds that 256 rows leave short) and with it: 1500 rows 4096 -> 11008
 // 199 and 166 us; 5000 rows 4096 -> 4096 208 and 174; 2400 gated rows 4096 -> 4096 216 and 179.
-constexpr double kStep256Us = 0.8, kStep192Us = 0.68, kStep128Us = 0.33, kStep128PairUs = 0.3;
+// 128 x 256 fills the device where 256 x 256 leave it half empty or split the contraction: without it and with it, forward,
+// 2048 rows 4096 -> 4096 81 and 65 us, 1300 rows 5120 -> 5120 81 and 71, 600 rows 4096 -> 11008 68 and 56, 2011 rows
+// 11008 -> 4096 172 and 175; dX of 2048 rows 4096 -> 4096 90 and 71, of 1300 rows 5120 -> 5120 90 and 84.
+constexpr double kStep256Us = 0.8, kStep192Us = 0.68, kStep128Us = 0.33, kStep128PairUs = 0.3, kStep128WideUs = 0.5;
 double step_us(int cfg, int64_t per_cu) {
+  if (cfg == sgmv::kTile128Wide) return kStep128WideUs;
   if (cfg == sgmv::kTile256) return kStep256Us;
   if (cfg == sgmv::kTile192) return kStep192Us;
   return per_cu < 2 ? kStep128Us : kStep128PairUs;
@@ -58,15 +62,16 @@ double step_us(int cfg, int64_t per_cu) {
 constexpr double kStreamBytesPerUs = 5.2e6;  // B of the small tiles, with every slot of the device taken
 constexpr double kPlaneBytesPerUs = 4.0e6;   // partial planes, written and read again
 
-DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, bool may_split) {
-  // columns_per_n: 2 for a gated tile (gate and up columns side by side).
+DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, bool may_split, bool wide128 = false) {
+  // columns_per_n: 2 for a gated tile (gate and up columns side by side).  wide128: 128 x 256 tiles may write the outputs.
   DensePlan best;
   double best_cost = -1;
   steps = std::max<int64_t>(steps, 1);
-  for (int cfg = sgmv::kTile256; cfg <= sgmv::kTile32; ++cfg) {
+  for (int cfg = sgmv::kTile256; cfg <= (wide128 ? sgmv::kTile128Wide : sgmv::kTile32); ++cfg) {
     const int bm = sgmv::dense_tile_rows(cfg);
     // A tile with more than half of its rows empty only where none is smaller.
     if (cfg <= sgmv::kTile192 && M <= 128) continue;
+    if (cfg == sgmv::kTile128Wide && M <= 64) continue;
     if (cfg == sgmv::kTile192 && !may_split) continue;
     if (cfg == sgmv::kTile128 && M <= 64 && may_split) continue;  // dW has no smaller tile
     if (cfg == sgmv::kTile64 && (M <= 32 || M > 64)) continue;
@@ -74,13 +79,13 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
     if (!may_split && cfg > sgmv::kTile128) continue;
     const int64_t tm = ceil_div(M, bm), tn = ceil_div(N, sgmv::dense_tile_cols(cfg) / columns_per_n);
     const int64_t slots = kCus * resident(cfg);
-    const int64_t most = may_split ? std::max<int64_t>(1, std::min<int64_t>(16, steps / 8)) : 1;
+    const int64_t most = may_split && cfg != sgmv::kTile128Wide ? std::max<int64_t>(1, std::min<int64_t>(16, steps / 8)) : 1;
     for (int64_t ks = 1; ks <= most; ++ks) {
       const int64_t per = ceil_div(steps, ks);
       if (ceil_div(steps, per) != ks) continue;
       const int64_t wgs = tm * tn * ks, rounds = ceil_div(wgs, slots);
       double cost;
-      if (cfg <= sgmv::kTile128) {
+      if (cfg <= sgmv::kTile128 || cfg == sgmv::kTile128Wide) {
         const int64_t per_cu = ceil_div(wgs, kCus);
         cost = (double)per_cu * (double)per * step_us(cfg, per_cu) + 4.0;
       } else {
@@ -146,7 +151,7 @@ sgmv_status_t check_layer(const sgmv_problem_t* p) {
   return units > SGMV_MAX_LAYER_UNITS || (!direct && p->num_segs > SGMV_MAX_LAYER_LONG_SEGS) ? SGMV_ERR_UNSUPPORTED : SGMV_OK;
 }
 
-LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
+LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128) {
   LayerPlan l;
   l.projections = layer_gated(op) ? 2 : 1;
   l.lora = !nothing_to_do(p);
@@ -181,7 +186,7 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
   const bool in_tile = l.lora && tiles_add_term(p, back, l.projections, N);
   const int64_t kt = ceil_div(back ? p.h_out : p.h_in, sgmv::kDenseK);
   const int cols = op == SGMV_GATED_FORWARD ? 2 : 1;
-  l.out = plan_dense(M, N, kt * (back ? l.projections : 1), cols, true);
+  l.out = plan_dense(M, N, kt * (back ? l.projections : 1), cols, true, wide128 && (!l.lora || in_tile) && l.halves == 1);
   l.out.term_in_tile = in_tile ? 1 : 0;
   l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile) || l.halves > 1;
   // (The large tiles' workgroups are too big to share a launch with.)
@@ -207,7 +212,7 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op) {
 
 ActPlan plan_act_backward(const sgmv_problem_t& p, int act) {
   ActPlan a;
-  a.layer = plan_layer(p, act == SGMV_ACT_NONE ? SGMV_DENSE_BACKWARD : SGMV_DENSE_ACT_BACKWARD);
+  a.layer = plan_layer(p, act == SGMV_ACT_NONE ? SGMV_DENSE_BACKWARD : SGMV_DENSE_ACT_BACKWARD, true);
   // Blocks of rows by 2048 columns: some workgroups a CU, each of four rows and more (their sums are written and read).
   const int64_t chunks = ceil_div(p.h_out, 2048);
   const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(ceil_div(1536, chunks), ceil_div(p.n_rows, 4)));

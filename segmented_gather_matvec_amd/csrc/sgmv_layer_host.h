@@ -52,7 +52,10 @@ inline bool layer_elementwise(int op) { return op == SGMV_GATED_BACKWARD || op =
 // The shape's checks, the rows that the tiles' 32-bit row numbers reach, the units that one launch holds (a
 // workgroup each; a launch has fewer than 2^32 threads), and the segments that every unit may walk.
 sgmv_status_t check_layer(const sgmv_problem_t* p);
-LayerPlan plan_layer(const sgmv_problem_t& p, int op);
+// wide128: 128 x 256 tiles too (the calls with an activation).
+inline bool layer_act(int op) { return op == SGMV_DENSE_ACT_FORWARD || op == SGMV_DENSE_ACT_BACKWARD; }
+LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128);
+inline LayerPlan plan_layer(const sgmv_problem_t& p, int op) { return plan_layer(p, op, layer_act(op)); }
 
 // The backward call of a dense layer with an activation: the layer's plan (without an activation it is the plain dense
 // layer's) and the planes of the bias's gradient behind its workspace.

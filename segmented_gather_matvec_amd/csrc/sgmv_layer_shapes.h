@@ -13,10 +13,11 @@ enum DenseTile : int {
   kTile192 = 1,  // 192 x 256, 8 waves (not for dW)
   kTile128 = 2,  // 128 x 128, 4 waves
   kTile64 = 3,   // 64 x 256, 4 waves
-  kTile32 = 4    // 32 x 256, 4 waves
+  kTile32 = 4,   // 32 x 256, 4 waves
+  kTile128Wide = 5  // 128 x 256, 8 waves (the calls with an activation: outputs, and dX)
 };
 constexpr int dense_tile_rows(int t) {
-  return t == kTile256 ? 256 : t == kTile192 ? 192 : t == kTile128 ? 128 : t == kTile64 ? 64 : 32;
+  return t == kTile256 ? 256 : t == kTile192 ? 192 : t == kTile128 || t == kTile128Wide ? 128 : t == kTile64 ? 64 : 32;
 }
 constexpr int dense_tile_cols(int t) { return t == kTile128 ? 128 : 256; }
 

@@ -1,0 +1,34 @@
+"""GPU parity of the layer with an activation at sizes whose outputs, or dX, are written by 128 x 256 tiles, with and without the LoRA
+term in them (tests/test_act_plans.py checks that they are)."""
+import pytest
+
+from tests import layer_reference as lr
+from tests.test_gpu_act import Extra, check_back, ref, run, run_back
+
+pytestmark = pytest.mark.gpu
+
+# rows, h_in, h_out, rank, segments (0: no LoRAs)
+FORWARD = [(600, 1032, 11008, 64, 4), (1300, 264, 5128, 16, 0), (300, 520, 11016, 32, 4), (1800, 136, 4104, 8, 4), (700, 136, 9000, 8, 4)]
+BACKWARD = [(1300, 5128, 1032, 64, 4), (1300, 5128, 264, 16, 0), (600, 11008, 520, 32, 4)]
+
+
+def layer(case, dtype):
+    n, h_in, h_out, rank, segs = case
+    layout = "none" if segs == 0 else "uncovered"
+    return lr.Layer(n + h_in, dtype, n, h_in, h_out, rank, 4, layout, 1, None, segs > 0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", FORWARD, ids=str)
+def test_forward(case, dtype):
+    c = layer(case, dtype)
+    e = Extra(c)
+    for g, r, what in zip(run(c, dtype, "gelu_tanh", e), ref(c, "gelu_tanh", e), "YZ"):
+        lr.check(g, *r, c.dtype, what)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("case", BACKWARD, ids=str)
+def test_backward(case, dtype):
+    c = layer(case, dtype)
+    check_back(c, "silu", run_back(c, dtype, "silu"))
