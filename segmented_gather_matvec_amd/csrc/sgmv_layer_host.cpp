@@ -109,11 +109,11 @@ DensePlan plan_dense(int64_t M, int64_t N, int64_t steps, int columns_per_n, boo
 }
 
 // products: that share the launch; summed: whose planes make one V.
-ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products, int summed) {
+ThinPlan plan_thin(const sgmv_problem_t& p, int64_t K, int products, int summed, int64_t workgroups = 1024) {
   ThinPlan t;
   t.units = (int)units_for(p, sgmv::kThinRows, &t.direct);
-  // About four workgroups per CU, each of at least 256 contraction steps.
-  const int64_t want = ceil_div(1024, std::max<int64_t>(1, (int64_t)t.units * products));
+  // About four workgroups per CU (or as many as said), each of at least 256 contraction steps.
+  const int64_t want = ceil_div(workgroups, std::max<int64_t>(1, (int64_t)t.units * products));
   const int64_t ks = std::max<int64_t>(1, std::min<int64_t>(want, ceil_div(K, 256)));
   t.kc = (int)round_up(ceil_div(K, ks), sgmv::kDenseK);
   t.ksplit = (int)ceil_div(K, t.kc);
@@ -166,8 +166,11 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128) {
   };
   if (l.lora) {
     const size_t v = (size_t)n * p.rank * sizeof(float);
-    l.down = plan_thin(p, p.h_in, l.projections, 1);
-    if (back) l.up = plan_thin(p, p.h_out, l.projections * l.halves, l.halves);
+    // The calls with an activation: half the splits beyond decode's rows, half the planes to sum (2011 rows, K = 11008, r = 64:
+    // product and sum 23 + 9 us and 21 + 6; 8192 rows, K = 4096, r = 16: 30 + 5 either way).
+    const int64_t workgroups = wide128 && n > kDecodeRows ? 512 : 1024;
+    l.down = plan_thin(p, p.h_in, l.projections, 1, workgroups);
+    if (back) l.up = plan_thin(p, p.h_out, l.projections * l.halves, l.halves, workgroups);
     for (int i = 0; i < l.projections; ++i) {
       for (int d = 0; d < (back ? 2 : 1); ++d) {
         l.v_off[d][i] = take(v);
