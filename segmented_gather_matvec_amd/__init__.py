@@ -242,7 +242,7 @@ def _stream(stream) -> Optional[int]:
     if stream is None:
         # (Without a Stream object where torch has the call for it: 0.1 us of host time instead of 2.6.)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
+        if raw is not None:
             return raw(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -611,25 +611,31 @@ def _on_device(index, call, stream, *args):
     import torch
     entry = getattr(load_library(), call)
     if index == torch.cuda.current_device():
-        _check(entry(*args, _stream(stream)), call)
-        return
-    with torch.cuda.device(index):
-        _check(entry(*args, _stream(stream)), call)
+        status = entry(*args, _stream(stream))
+    else:
+        with torch.cuda.device(index):
+            status = entry(*args, _stream(stream))
+    if status != SGMV_OK:
+        raise SgmvError(status, call)
+
+
+_codes = {}     # of the 16-bit formats, by torch dtype
 
 
 def _matrix(t, name):
-    """(device index, dtype, rows, columns) of a call's first matrix."""
-    _need(t, name)
+    """(device index, dtype, its code, rows, columns) of a call's first matrix."""
+    if not _codes:
+        import torch
+        _codes.update({torch.float16: SGMV_F16, torch.bfloat16: SGMV_BF16})
     if t is None or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-D device tensor")
-    _dtype_16(t, name)
-    return t.get_device(), t.dtype, t.shape[0], t.shape[1]
-
-
-def _dtype_16(t, name):
-    import torch
-    if t.dtype is not torch.float16 and t.dtype is not torch.bfloat16:
+    if not t.is_cuda or not t.is_contiguous():
+        _need(t, name)
+    code = _codes.get(t.dtype)
+    if code is None:
         raise ValueError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    n, width = t.shape
+    return t.get_device(), t.dtype, code, n, width
 
 
 def _top_k(sorted_rows, n, name):
@@ -681,12 +687,12 @@ def sgmv_dispatch_rows(X, slots, Xs, stream=None):
     """Xs[slots[i * top_k + j]] = X[i] (X [n_rows, width], Xs [n_rows * top_k, width], slots of sgmv_route_rows).
     Asynchronous."""
     import torch
-    index, dtype, n, width = _matrix(X, "X")
+    index, dtype, code, n, width = _matrix(X, "X")
     _matrix(Xs, "Xs")
     top_k = _top_k(Xs.shape[0], n, "Xs")
     m = n * top_k
     out = _layer_ptr(Xs, "Xs", index, dtype, (m, width))
-    _on_device(index, "sgmv_dispatch_rows", stream, _dtype_code(dtype), n, top_k, width, X.data_ptr(),
+    _on_device(index, "sgmv_dispatch_rows", stream, code, n, top_k, width, X.data_ptr(),
                _layer_ptr(slots, "slots", index, torch.int32, None, m), out)
 
 
@@ -695,21 +701,21 @@ def sgmv_combine_rows(Ys, slots, Y, weights=None, residual=None, stream=None):
     [n_rows * top_k, width], weights float32 or None for ones; Y may be residual).  Without weights and residual it is the gradient
     of sgmv_dispatch_rows.  Asynchronous."""
     import torch
-    index, dtype, n, width = _matrix(Y, "Y")
+    index, dtype, code, n, width = _matrix(Y, "Y")
     _matrix(Ys, "Ys")
     top_k = _top_k(Ys.shape[0], n, "Ys")
     m = n * top_k
     args = (_layer_ptr(Ys, "Ys", index, dtype, (m, width)), _layer_ptr(slots, "slots", index, torch.int32, None, m),
             _layer_ptr(weights, "weights", index, torch.float32, None, m),
             _layer_ptr(residual, "residual", index, dtype, (n, width)))
-    _on_device(index, "sgmv_combine_rows", stream, _dtype_code(dtype), n, top_k, width, *args, Y.data_ptr())
+    _on_device(index, "sgmv_combine_rows", stream, code, n, top_k, width, *args, Y.data_ptr())
 
 
 def sgmv_combine_rows_backward(dY, Ys, slots, weights=None, dYs=None, dweights=None, stream=None):
     """Gradients of sgmv_combine_rows from dY [n_rows, width]: dYs [n_rows * top_k, width] and dweights (float32, one
     per choice), each or None; Ys is needed for dweights only.  Asynchronous."""
     import torch
-    index, dtype, n, width = _matrix(dY, "dY")
+    index, dtype, code, n, width = _matrix(dY, "dY")
     _need(slots, "slots", torch.int32)
     m = slots.numel() if slots is not None else 0
     top_k = _top_k(m, n, "slots")
@@ -718,7 +724,7 @@ def sgmv_combine_rows_backward(dY, Ys, slots, weights=None, dYs=None, dweights=N
             _layer_ptr(weights, "weights", index, torch.float32, None, m),
             _layer_ptr(dYs, "dYs", index, dtype, (m, width)),
             _layer_ptr(dweights, "dweights", index, torch.float32, None, m))
-    _on_device(index, "sgmv_combine_rows_backward", stream, _dtype_code(dtype), n, top_k, width, dY.data_ptr(), *args)
+    _on_device(index, "sgmv_combine_rows_backward", stream, code, n, top_k, width, dY.data_ptr(), *args)
 
 
 def sgmv_layer_norm_workspace_bytes(n_rows: int, width: int) -> int:
@@ -739,11 +745,11 @@ def sgmv_layer_norm_apply(X, gamma, beta, Y, eps=1e-5, mean=None, rstd=None, str
     """Y = (X - mean) * rstd * gamma + beta, row by row (gamma, beta [width] or None; Y may be X); `mean` and `rstd`
     (float32 [n_rows] or None) are stored for sgmv_layer_norm_backward.  Asynchronous."""
     import torch
-    index, dtype, n, width = _matrix(X, "X")
+    index, dtype, code, n, width = _matrix(X, "X")
     args = (_layer_ptr(gamma, "gamma", index, dtype, (width,)), _layer_ptr(beta, "beta", index, dtype, (width,)), float(eps),
             _layer_ptr(Y, "Y", index, dtype, (n, width)), _layer_ptr(mean, "mean", index, torch.float32, (n,)),
             _layer_ptr(rstd, "rstd", index, torch.float32, (n,)))
-    _on_device(index, "sgmv_layer_norm_apply", stream, _dtype_code(dtype), n, width, X.data_ptr(), *args)
+    _on_device(index, "sgmv_layer_norm_apply", stream, code, n, width, X.data_ptr(), *args)
 
 
 def sgmv_layer_norm_backward(X, gamma, mean, rstd, dY, ws, dX=None, beyond=None, dgamma=None, dbeta=None,
@@ -752,11 +758,11 @@ def sgmv_layer_norm_backward(X, gamma, mean, rstd, dY, ws, dX=None, beyond=None,
     or beyond), dgamma and dbeta (written, or added to what is there with accumulate), each or None; `ws` from
     new_layer_norm_workspace.  Asynchronous."""
     import torch
-    index, dtype, n, width = _matrix(X, "X")
+    index, dtype, code, n, width = _matrix(X, "X")
     f32 = torch.float32
     rows = [_layer_ptr(t, name, index, dtype, (n, width)) for t, name in ((dY, "dY"), (beyond, "beyond"), (dX, "dX"))]
     cols = [_layer_ptr(t, name, index, dtype, (width,)) for t, name in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta"))]
-    _on_device(index, "sgmv_layer_norm_backward", stream, _dtype_code(dtype), n, width, X.data_ptr(), cols[0],
+    _on_device(index, "sgmv_layer_norm_backward", stream, code, n, width, X.data_ptr(), cols[0],
                _layer_ptr(mean, "mean", index, f32, (n,)), _layer_ptr(rstd, "rstd", index, f32, (n,)), *rows, *cols[1:],
                int(accumulate), *_buffer(ws, "ws", index))
 
