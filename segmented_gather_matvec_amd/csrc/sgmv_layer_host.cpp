@@ -217,8 +217,10 @@ ActPlan plan_act_backward(const sgmv_problem_t& p, int act) {
   ActPlan a;
   a.layer = plan_layer(p, act == SGMV_ACT_NONE ? SGMV_DENSE_BACKWARD : SGMV_DENSE_ACT_BACKWARD, true);
   // Blocks of rows by 2048 columns: some workgroups a CU, each of four rows and more (their sums are written and read).
-  const int64_t chunks = ceil_div(p.h_out, 2048);
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(ceil_div(1536, chunks), ceil_div(p.n_rows, 4)));
+  // Whole rows of fp16 have more waves a workgroup: two on a CU.
+  const bool whole = p.dtype == SGMV_F16 && act != SGMV_ACT_NONE && p.h_out > 2048 && p.h_out <= sgmv::kActRowCols;
+  const int64_t most = whole ? 2 * kCus : ceil_div(6 * kCus, ceil_div(p.h_out, 2048));
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(most, ceil_div(p.n_rows, 4)));
   a.rows_per_block = (int32_t)std::max<int64_t>(1, ceil_div(p.n_rows, blocks));
   a.blocks = (int32_t)ceil_div(p.n_rows, a.rows_per_block);
   a.planes_off = (size_t)round_up((int64_t)a.layer.total, 256);

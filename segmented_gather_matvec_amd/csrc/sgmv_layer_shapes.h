@@ -27,4 +27,7 @@ constexpr int kLoraGradCols = 256; // columns of X or dY per LoRA-gradient workg
 // fp16 dG and dU of a row are kept divided by 2^(8 b), -kMaxRowPower <= b <= kMaxRowPower; b of a row of zeros.
 constexpr int kMaxRowPower = 15, kZeroRow = -128;
 
+// fp16 rows up to this wide are one workgroup's in the activation's backward, which finds their powers on its way.
+constexpr int kActRowCols = 16384;
+
 }  // namespace sgmv

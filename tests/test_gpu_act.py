@@ -257,6 +257,16 @@ def test_fp16_rows_of_small_gradients(n, ratio):
     check_back(c, "gelu_tanh", run_back(c, "f16", "gelu_tanh"))
 
 
+@pytest.mark.parametrize("n,h_out", [(5, 2048), (9, 2056), (150, 4096), (40, 4104), (131, 8192), (7, 8200), (133, 16384), (6, 16392), (140, 20008)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_widths_of_the_activation_backward(n, h_out, dtype):
+    """Either side of every width that changes how a row of dZ is shared out, with rows of zeros and of tiny values among them."""
+    c = lr.Layer(n, dtype, n, 16, h_out, 8, 2, "one", 1, None, False)
+    c.dY[1] = 0
+    c.dY[2] *= 2.0 ** -12
+    check_back(c, "silu", run_back(c, dtype, "silu"))
+
+
 @pytest.mark.parametrize("act", sorted(set(ACTS) - {"relu"}))
 def test_gradient_against_differences(act):
     """dX, dA, dB and dbias against central differences of the 64-bit layer along random directions; the backward reads Z rounded
