@@ -1,14 +1,14 @@
 // sgmv_act.hip - the elementwise backward of a dense layer's activation (gfx950): dZ = dY * act'(Z), and the bias's
 // gradient, the column sums of dZ.
 //
-// Bound by memory: Z and dY are read once, dZ is written once, and the column sums ride along in registers.  A thread has eight
-// columns of a block of rows, four rows of both operands in flight; the blocks' sums are written as planes and
-// added up by a launch of their own (no atomics: one order).
+// Bound by memory: Z and dY are read once, dZ is written once, and the column sums ride along in registers; the blocks' sums
+// are written as planes and added up by a launch of their own (no atomics: one order).  bf16, 8192 x 11008 with the bias's
+// gradient: 100 us relu, 104 to 109 the others (5.2 TB/s; the sums alone, without an activation, 37).
 // fp16 rows carry a power of two each (as in the gated block's backward): dZ is an operand of the matrix cores,
 // and a row whose values are small must not lose them to fp16's denormals.  The power comes from the row's largest |dY|
-// (no activation here has a slope beyond 1.13), so a
-// workgroup that has whole rows (up to 16384 columns) finds it on its way (4096 rows of 4096, 8192 and
-// 11008: 33, 51 and 110 us with the bias's sums; with a launch ahead that looks at dY, as wider rows have it, 43, 70 and 122).
+// (no activation here has a slope beyond 1.13).  Rows of up to 16384 columns are one workgroup's, which finds it on its way; wider ones
+// have a launch ahead that looks at dY (4096 rows of 4096, 8192 and 11008 with the bias's sums: 32, 50 and 96 us, and 43, 70 and
+// 122 that way).
 #include <algorithm>
 
 #include "sgmv_layer_ops.h"
@@ -68,22 +68,76 @@ __global__ __launch_bounds__(kThreads) void sgmv_row_power_kernel(const uint16_t
   }
 }
 
-// Workgroup: a block of rows by THREADS x KEEP eights of columns, U rows in flight.  POWER: it has whole rows and finds
-// their powers itself.
-template <class T, bool HALVES, bool POWER, int THREADS, int KEEP, int U>
-__global__ __launch_bounds__(THREADS) void sgmv_act_backward_kernel(ActBackwardParams p) {
+// Any width: a thread has eight columns of a block of rows, U in flight (fp16: the rows' powers are there already).
+template <class T, bool HALVES>
+__global__ __launch_bounds__(kThreads) void sgmv_act_backward_kernel(ActBackwardParams p) {
+  constexpr int U = 4;  // rows in flight
+  const int c = (blockIdx.y * kThreads + threadIdx.x) * 8;
+  if (c >= p.F) return;
+  const int64_t r0 = (int64_t)blockIdx.x * p.rows_per_block;
+  const int64_t r1 = r0 + p.rows_per_block < p.n ? r0 + p.rows_per_block : p.n;
+  float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int64_t row = r0; row < r1; row += U) {
+    u32x4 z[U], y[U];
+    int power[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t o = (row + u < r1 ? row + u : r1 - 1) * p.F + c;
+      y[u] = load_stream(p.dY + o);
+      if (p.dZ != nullptr) z[u] = load_stream(p.Z + o);
+      if (T::kMaxFinite < 1e6f && p.dZ != nullptr) power[u] = p.row_power[row + u < r1 ? row + u : r1 - 1];
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (row + u >= r1) continue;
+      float d[8];
+      unpack8<T>(y[u], d);
+      if (p.dZ != nullptr) {
+        float zv[8];
+        unpack8<T>(z[u], zv);
+        act_slopes<8>(p.act, zv, d);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += d[e];
+      if (p.dZ == nullptr) continue;
+      const int64_t o = (row + u) * p.F + c;
+      if constexpr (T::kMaxFinite < 1e6f) {
+        const float down = power_of(power[u] == kZeroRow ? 0 : -power[u]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d[e] *= down;
+      }
+      if constexpr (HALVES) {
+        u32x4 hi, lo;
+        split8<T>(d, hi, lo);
+        store_vec(p.dZ + o, hi);
+        store_vec(p.dZ + (int64_t)p.n * p.F + o, lo);
+      } else {
+        store_vec(p.dZ + o, pack8<T>(d));
+      }
+    }
+  }
+  if (p.planes == nullptr) return;
+  float* const dst = p.planes + (int64_t)blockIdx.x * p.F + c;
+  *reinterpret_cast<f32x4*>(dst) = f32x4{sum[0], sum[1], sum[2], sum[3]};
+  *reinterpret_cast<f32x4*>(dst + 4) = f32x4{sum[4], sum[5], sum[6], sum[7]};
+}
+
+// fp16 rows up to THREADS x KEEP eights wide: a workgroup has whole rows of a block, U at a time, and finds their powers
+// itself; the next ones are asked for ahead of the barrier that this costs.
+template <bool HALVES, int THREADS, int KEEP, int U>
+__global__ __launch_bounds__(THREADS) void sgmv_act_backward_rows_kernel(ActBackwardParams p) {
+  using T = F16;
   constexpr int WAVES = THREADS / 64;
-  __shared__ uint32_t most[POWER ? 2 : 1][WAVES][U];
+  __shared__ uint32_t most[2][WAVES][U];
   const int t = threadIdx.x;
   bool live[KEEP];
   int c[KEEP];
 #pragma unroll
   for (int k = 0; k < KEEP; ++k) {
-    const int x = ((int)blockIdx.y * KEEP + k) * THREADS + t;
+    const int x = k * THREADS + t;
     live[k] = x * 8 < p.F;
     c[k] = live[k] ? x * 8 : p.F - 8;
   }
-  if (!POWER && !live[0]) return;
   const int64_t r0 = (int64_t)blockIdx.x * p.rows_per_block;
   const int64_t r1 = r0 + p.rows_per_block < p.n ? r0 + p.rows_per_block : p.n;
   float sum[KEEP][8];
@@ -99,16 +153,15 @@ __global__ __launch_bounds__(THREADS) void sgmv_act_backward_kernel(ActBackwardP
 #pragma unroll
       for (int k = 0; k < KEEP; ++k) {
         ny[u][k] = load_stream(p.dY + at * p.F + c[k]);
-        if (p.dZ != nullptr) nz[u][k] = load_stream(p.Z + at * p.F + c[k]);
+        nz[u][k] = load_stream(p.Z + at * p.F + c[k]);
       }
     }
   };
-  if (POWER) ask(r0);
+  ask(r0);
   int turn = 0;
   for (int64_t row = r0; row < r1; row += U, turn ^= 1) {
     u32x4 z[U][KEEP], y[U][KEEP];
     int power[U];
-    if (!POWER) ask(row);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -116,28 +169,24 @@ __global__ __launch_bounds__(THREADS) void sgmv_act_backward_kernel(ActBackwardP
         y[u][k] = ny[u][k];
         z[u][k] = nz[u][k];
       }
-      const int64_t at = row + u < r1 ? row + u : r1 - 1;
-      power[u] = T::kMaxFinite < 1e6f && !POWER && p.dZ != nullptr ? p.row_power[at] : 0;
     }
-    if (POWER && row + U < r1) ask(row + U);  // ahead of this rows' barrier
-    if constexpr (POWER) {
-      uint32_t big[U];
+    if (row + U < r1) ask(row + U);
+    uint32_t big[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        big[u] = 0;
+    for (int u = 0; u < U; ++u) {
+      big[u] = 0;
 #pragma unroll
-        for (int k = 0; k < KEEP; ++k) big[u] = largest(y[u][k], big[u]);
-        big[u] = wave_max(largest_bits(big[u]));
-        if ((t & 63) == 0) most[turn][t >> 6][u] = big[u];
-      }
-      __syncthreads();  // (the other half's readers are past the barrier before)
+      for (int k = 0; k < KEEP; ++k) big[u] = largest(y[u][k], big[u]);
+      big[u] = wave_max(largest_bits(big[u]));
+      if ((t & 63) == 0) most[turn][t >> 6][u] = big[u];
+    }
+    __syncthreads();  // (the other half's readers are past the barrier before)
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) big[u] = big[u] > most[turn][w][u] ? big[u] : most[turn][w][u];
-        power[u] = power_for(big[u]);
-        if (t == 0 && row + u < r1) p.row_power[row + u] = (int8_t)power[u];
-      }
+      for (int w = 0; w < WAVES; ++w) big[u] = big[u] > most[turn][w][u] ? big[u] : most[turn][w][u];
+      power[u] = power_for(big[u]);
+      if (t == 0 && row + u < r1) p.row_power[row + u] = (int8_t)power[u];
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -146,20 +195,16 @@ __global__ __launch_bounds__(THREADS) void sgmv_act_backward_kernel(ActBackwardP
       for (int k = 0; k < KEEP; ++k) {
         float d[8];
         unpack8<T>(y[u][k], d);
-        if (p.dZ != nullptr) {
-          float zv[8];
-          unpack8<T>(z[u][k], zv);
-          act_slopes<8>(p.act, zv, d);
-        }
+        float zv[8];
+        unpack8<T>(z[u][k], zv);
+        act_slopes<8>(p.act, zv, d);
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[k][e] += d[e];
-        if (p.dZ == nullptr || !live[k]) continue;
+        if (!live[k]) continue;
         const int64_t o = (row + u) * p.F + c[k];
-        if constexpr (T::kMaxFinite < 1e6f) {
-          const float down = power_of(power[u] == kZeroRow ? 0 : -power[u]);
+        const float down = power_of(power[u] == kZeroRow ? 0 : -power[u]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) d[e] *= down;
-        }
+        for (int e = 0; e < 8; ++e) d[e] *= down;
         if constexpr (HALVES) {
           u32x4 hi, lo;
           split8<T>(d, hi, lo);
@@ -181,15 +226,28 @@ __global__ __launch_bounds__(THREADS) void sgmv_act_backward_kernel(ActBackwardP
   }
 }
 
-template <class T, bool POWER, int THREADS, int KEEP, int U>
-hipError_t launch_act_backward_t(const ActBackwardParams& p, hipStream_t s) {
-  const int per = THREADS * KEEP * 8;
-  const dim3 grid((unsigned)((p.n + p.rows_per_block - 1) / p.rows_per_block), (unsigned)((p.F + per - 1) / per));
-  if (POWER && grid.y != 1) return hipErrorInvalidValue;
+dim3 act_grid(const ActBackwardParams& p, int columns) {
+  return dim3((unsigned)((p.n + p.rows_per_block - 1) / p.rows_per_block), (unsigned)((p.F + columns - 1) / columns));
+}
+
+template <class T>
+hipError_t launch_act_columns(const ActBackwardParams& p, hipStream_t s) {
+  const dim3 grid = act_grid(p, kThreads * 8);
   if (p.halves)
-    hipLaunchKernelGGL((sgmv_act_backward_kernel<T, true, POWER, THREADS, KEEP, U>), grid, dim3(THREADS), 0, s, p);
+    hipLaunchKernelGGL((sgmv_act_backward_kernel<T, true>), grid, dim3(kThreads), 0, s, p);
   else
-    hipLaunchKernelGGL((sgmv_act_backward_kernel<T, false, POWER, THREADS, KEEP, U>), grid, dim3(THREADS), 0, s, p);
+    hipLaunchKernelGGL((sgmv_act_backward_kernel<T, false>), grid, dim3(kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
+template <int THREADS, int KEEP, int U>
+hipError_t launch_act_rows(const ActBackwardParams& p, hipStream_t s) {
+  const dim3 grid = act_grid(p, THREADS * KEEP * 8);
+  if (grid.y != 1) return hipErrorInvalidValue;
+  if (p.halves)
+    hipLaunchKernelGGL((sgmv_act_backward_rows_kernel<true, THREADS, KEEP, U>), grid, dim3(THREADS), 0, s, p);
+  else
+    hipLaunchKernelGGL((sgmv_act_backward_rows_kernel<false, THREADS, KEEP, U>), grid, dim3(THREADS), 0, s, p);
   return hipGetLastError();
 }
 
@@ -198,17 +256,17 @@ hipError_t launch_act_backward_t(const ActBackwardParams& p, hipStream_t s) {
 hipError_t launch_act_backward(int dtype, const ActBackwardParams& p, hipStream_t stream) {
   if (p.n <= 0 || (p.dZ == nullptr && p.planes == nullptr)) return hipSuccess;
   if (p.rows_per_block < 1) return hipErrorInvalidValue;
-  if (dtype == 1) return launch_act_backward_t<BF16, false, kThreads, 1, 4>(p, stream);
-  if (p.dZ == nullptr) return launch_act_backward_t<F16, false, kThreads, 1, 4>(p, stream);
-  if (p.F <= 2048) return launch_act_backward_t<F16, true, 256, 1, 2>(p, stream);
-  if (p.F <= 4096) return launch_act_backward_t<F16, true, 256, 2, 1>(p, stream);
-  if (p.F <= 8192) return launch_act_backward_t<F16, true, 512, 2, 1>(p, stream);
-  if (p.F <= kActRowCols) return launch_act_backward_t<F16, true, 1024, 2, 1>(p, stream);
+  if (dtype == 1) return launch_act_columns<BF16>(p, stream);
+  if (p.dZ == nullptr) return launch_act_columns<F16>(p, stream);
+  if (p.F <= 2048) return launch_act_rows<256, 1, 2>(p, stream);
+  if (p.F <= 4096) return launch_act_rows<256, 2, 1>(p, stream);
+  if (p.F <= 8192) return launch_act_rows<512, 2, 1>(p, stream);
+  if (p.F <= kActRowCols) return launch_act_rows<1024, 2, 1>(p, stream);
   hipLaunchKernelGGL(sgmv_row_power_kernel, dim3((unsigned)std::min(p.n, 8192)), dim3(kThreads), 0, stream, p.dY, p.row_power,
                      p.n, p.F / 8);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_act_backward_t<F16, false, kThreads, 1, 4>(p, stream);
+  return launch_act_columns<F16>(p, stream);
 }
 
 }  // namespace sgmv
