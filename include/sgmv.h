@@ -542,7 +542,7 @@ typedef enum sgmv_layer_op {
   SGMV_DENSE_BACKWARD = 1,
   SGMV_GATED_FORWARD = 2,
   SGMV_GATED_BACKWARD = 3,
-  SGMV_DENSE_ACT_FORWARD = 5,
+  SGMV_DENSE_ACT_FORWARD = 5,  /* (4 is none) */
   SGMV_DENSE_ACT_BACKWARD = 6
 } sgmv_layer_op_t;
 

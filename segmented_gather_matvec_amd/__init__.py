@@ -45,6 +45,7 @@ SGMV_DEVICE_ERR_WAIT_TIMEOUT = 1
 SGMV_NOALLOC_MAX_WORKSPACE = 16 << 20
 SGMV_BASE_MAX_ROWS = 128
 SGMV_HOST_META_MAX_SEGS = 64
+SGMV_MAX_TOP_K, SGMV_MAX_ROUTE_LORAS = 64, 8192
 SGMV_ACT_SILU, SGMV_ACT_GELU_TANH, SGMV_ACT_NONE, SGMV_ACT_RELU, SGMV_ACT_GELU = range(5)
 SGMV_DENSE_FORWARD, SGMV_DENSE_BACKWARD, SGMV_GATED_FORWARD, SGMV_GATED_BACKWARD = range(4)
 SGMV_DENSE_ACT_FORWARD, SGMV_DENSE_ACT_BACKWARD = 5, 6

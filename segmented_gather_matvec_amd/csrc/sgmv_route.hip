@@ -133,7 +133,8 @@ __global__ __launch_bounds__(kRouteThreads) void sgmv_route_kernel(RouteParams p
     if (live && rank == 0)
       __hip_atomic_store(&mine[key], place + (int)__builtin_popcountll(same), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    if (live) {
+    // (Counts that another call wrote over, or ids that changed under way, must not become places elsewhere.)
+    if (live && place >= 0 && place < p.m) {
       if (p.perm != nullptr) p.perm[place] = e;
       if (p.slots != nullptr) p.slots[e] = place;
     }

@@ -17,6 +17,10 @@ MOST_TOP_K = int(re.search(r"#define SGMV_MAX_TOP_K (\d+)", HEADER).group(1))
 MOST_LORAS = int(re.search(r"#define SGMV_MAX_ROUTE_LORAS (\d+)", HEADER).group(1))
 MOST_ROWS = 1 << int(re.search(r"#define SGMV_MAX_LAYER_ROWS \(1 << (\d+)\)", HEADER).group(1))
 
+def test_limits_match_the_header():
+    assert (sg.SGMV_MAX_TOP_K, sg.SGMV_MAX_ROUTE_LORAS) == (MOST_TOP_K, MOST_LORAS)
+
+
 ARGS = {
     "sgmv_route_rows": dict(n=6000, k=2, P=40, ids=FAKE, perm=FAKE, slots=FAKE, seg=FAKE, idx=FAKE, ws=FAKE, bytes=1 << 40),
     "sgmv_dispatch_rows": dict(dtype=0, n=10, k=2, w=64, X=FAKE, slots=FAKE, Xs=FAKE),

@@ -92,6 +92,18 @@ def test_outputs_are_optional_and_no_rows_give_empty_segments():
     assert (seg == 0).all() and torch.equal(idx, torch.arange(50, dtype=I32, device="cuda"))
 
 
+@pytest.mark.parametrize("n,P", [(900, 40), (7000, 40)])
+def test_an_order_over_its_own_ids_stays_inside(n, P):
+    """perm written over ids, which the header forbids: the values are anything, the neighbours are not touched."""
+    buffer = torch.full((n + 128,), 12345, dtype=I32, device="cuda")
+    ids = buffer[64:64 + n]
+    ids.copy_(choices("uniform", n, 1, P, 3)[:, 0])
+    slots = torch.full((n + 128,), 12345, dtype=I32, device="cuda")
+    sg.sgmv_route_rows(ids, P, ids, slots[64:64 + n], None, None, sg.new_route_workspace(n, 1, P))
+    for t in (buffer, slots):
+        assert (t[:64] == 12345).all() and (t[-64:] == 12345).all()
+
+
 class Rows:
     def __init__(self, seed, dtype, n, k, w, P=5):
         g = torch.Generator().manual_seed(seed)
