@@ -91,7 +91,7 @@ __device__ inline void issue_e(const uint16_t* E, int rk, int R, int k0, int N, 
 // runs go through the ring's slots (the product is done with them), behind one barrier.
 template <class T, int MODE, class S, int J0>
 __device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x4 (&acc)[S::TM][S::TN], uint16_t* ring,
-                                int m0, int n0, int wave, int lane) {
+                                int m0, int n0, int wave, int lane, int share) {
   constexpr int TM = S::TM, TNP = S::TNP, C = S::C, B0 = S::BM * kDenseK, SLOTS = 4;
   constexpr int LE = C / 16 < S::NW ? 1 : C / 16 / S::NW;
   static_assert(S::STAGES >= SLOTS, "ring slots");
@@ -115,7 +115,10 @@ __device__ inline void add_term(const DenseParams& p, const LowRankTerm& t, f32x
     const int k_in = k_l < 0 ? 0 : k_l;
     const uint64_t e_l = t.ptrs[k_in], pair_l = t.pair[k_in];
     const int r_in = rank_of(t.ranks, R, k_in);
-    const int r_l = k_l >= 0 && e_l != 0ull && pair_l != 0ull ? r_in : 0;
+    // (share: where the splits of a tile share the term, every ksplit-th segment is this one's; -1: all are.)
+    bool mine = true;
+    if constexpr (MODE == kDenseForward) mine = share < 0 || sl % p.ksplit == share;
+    const int r_l = k_l >= 0 && e_l != 0ull && pair_l != 0ull && mine ? r_in : 0;
     const int ns = sm.num_segs - s0 < 64 ? sm.num_segs - s0 : 64;
     int u = 0;
     while (u < ns) {
@@ -546,17 +549,19 @@ __device__ inline void dense_body(const DenseParams& p, int block, uint16_t* rin
     }
   }
   if constexpr (TERM) {
-    if (p.term_in_tile && g == 0) {
+    const bool spread = MODE == kDenseForward && p.term_spread;
+    if (p.term_in_tile && (g == 0 || spread)) {
+      const int share = spread ? g : -1;
       if constexpr (S::GATED) {
-        if (p.term[0].V16 != nullptr) add_term<T, MODE, S, 0>(p, p.term[0], acc, ring, m0, n0, wave, lane);
-        if (p.term[1].V16 != nullptr) add_term<T, MODE, S, TNP>(p, p.term[1], acc, ring, m0, n0, wave, lane);
+        if (p.term[0].V16 != nullptr) add_term<T, MODE, S, 0>(p, p.term[0], acc, ring, m0, n0, wave, lane, share);
+        if (p.term[1].V16 != nullptr) add_term<T, MODE, S, TNP>(p, p.term[1], acc, ring, m0, n0, wave, lane, share);
       } else {
         for (int t = 0; t < (MODE == kDenseDx ? p.pairs : 1); ++t) {
           const LowRankTerm term{nullptr, t ? p.term[1].V16 : p.term[0].V16,
                                  t ? p.term[1].row_scale : p.term[0].row_scale,
                                  t ? p.term[1].ptrs : p.term[0].ptrs, t ? p.term[1].pair : p.term[0].pair,
                                  t ? p.term[1].ranks : p.term[0].ranks};
-          if (term.V16 != nullptr) add_term<T, MODE, S, 0>(p, term, acc, ring, m0, n0, wave, lane);
+          if (term.V16 != nullptr) add_term<T, MODE, S, 0>(p, term, acc, ring, m0, n0, wave, lane, share);
         }
       }
     }

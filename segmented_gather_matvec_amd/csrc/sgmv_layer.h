@@ -52,6 +52,7 @@ struct DenseParams {
   int32_t accumulate;    // dW: add to what is there
   int32_t to_planes;     // 1: fp32 partial planes instead of the outputs (ksplit > 1, or the epilogue adds a term)
   int32_t term_in_tile;  // 1: split 0 of every tile adds the LoRA term
+  int32_t term_spread;   // 1: forward: the splits of a tile share the term's segments, each adding its own to its plane
   int32_t v_planes;      // partial planes of term[].V that the epilogue sums
   const int32_t* row_k;  // [term][n_rows] LoRA of each covered row (see ThinParams); null: the epilogue searches
   const int8_t* row_power;  // null, or [n_rows] (32-byte aligned, readable to the next 32) the powers that the rows of

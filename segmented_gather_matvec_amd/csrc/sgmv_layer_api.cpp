@@ -128,6 +128,7 @@ sgmv::DenseParams dense_params(const Call& c, const DensePlan& d, int64_t M, int
   q.act = c.act;
   q.to_planes = d.to_planes;
   q.term_in_tile = d.term_in_tile;
+  q.term_spread = d.term_spread;
   q.plane_stride = M * N;
   q.v_planes = 1;
   q.planes = c.at(c.plan.planes_off);

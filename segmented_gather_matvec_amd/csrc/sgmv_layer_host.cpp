@@ -191,6 +191,9 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128) {
   const int cols = op == SGMV_GATED_FORWARD ? 2 : 1;
   l.out = plan_dense(M, N, kt * (back ? l.projections : 1), cols, true, wide128 && (!l.lora || in_tile) && l.halves == 1);
   l.out.term_in_tile = in_tile ? 1 : 0;
+  // (132 rows 6224 -> 11080, r = 64, 17 segments, in splits: 81 us with all of the term in the first, 55 with its
+  // segments shared out.)
+  l.out.term_spread = wide128 && in_tile && !back && l.out.ksplit > 1 ? 1 : 0;
   l.out.to_planes = l.out.ksplit > 1 || (l.lora && !in_tile) || l.halves > 1;
   // (The large tiles' workgroups are too big to share a launch with.)
   l.one_launch = l.lora && !back && l.out.to_planes && !in_tile && l.out.cfg > sgmv::kTile192;

@@ -15,6 +15,7 @@ struct DensePlan {
   int ktiles_per_split = 1;
   int to_planes = 0;     // fp32 planes and an epilogue launch
   int term_in_tile = 0;  // the tiles add the LoRA term
+  int term_spread = 0;   // all splits of a tile share it (forward calls with an activation)
   size_t plane_bytes = 0;
 };
 

@@ -43,6 +43,8 @@ static void check(const sgmv_problem_t& p) {
   CHECK(forward == f.total && f.halves == 1 && !f.row_powers);
   if (p.n_rows > 0) check_dense(f.out, p.n_rows, p.h_out, ceil_div(p.h_in, sgmv::kDenseK));
   CHECK(!f.one_launch || f.out.to_planes);
+  CHECK(f.out.term_spread == (f.out.term_in_tile && f.out.ksplit > 1 ? 1 : 0));
+  CHECK(!plan_layer(p, SGMV_DENSE_FORWARD).out.term_spread && !plan_act_backward(p, SGMV_ACT_SILU).layer.out.term_spread);
   for (int act : {SGMV_ACT_NONE, SGMV_ACT_RELU, SGMV_ACT_GELU}) {
     const ActPlan a = plan_act_backward(p, act);
     CHECK(a.total <= backward && a.layer.total <= a.planes_off && a.planes_off % 256 == 0);
@@ -67,8 +69,8 @@ int main(int argc, char** argv) {
       sgmv_problem_t p{SGMV_BF16, std::atoi(argv[i]), std::atoi(argv[i + 1]), std::atoi(argv[i + 2]), std::atoi(argv[i + 3]), 4,
                        std::atoi(argv[i + 4]), std::atoi(argv[i]), 0, 0};
       if (p.num_segs == 0) p.max_seg_len = 0;
-      std::printf("%d %d %d\n", plan_layer(p, SGMV_DENSE_ACT_FORWARD).out.cfg, plan_act_backward(p, SGMV_ACT_SILU).layer.out.cfg,
-                  plan_layer(p, SGMV_DENSE_ACT_FORWARD).out.term_in_tile);
+      std::printf("%d %d %d %d\n", plan_layer(p, SGMV_DENSE_ACT_FORWARD).out.cfg, plan_act_backward(p, SGMV_ACT_SILU).layer.out.cfg,
+                  plan_layer(p, SGMV_DENSE_ACT_FORWARD).out.term_in_tile, plan_layer(p, SGMV_DENSE_ACT_FORWARD).out.term_spread);
     }
     return 0;
   }

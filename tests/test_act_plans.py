@@ -33,3 +33,10 @@ def test_sizes_of_the_wide_tiles(driver):
         lines = subprocess.run([driver] + args, capture_output=True, text=True, check=True).stdout.split("\n")
         for case, line in zip(cases, lines):
             assert int(line.split()[column]) == WIDE, case
+
+
+def test_sizes_of_the_shared_term(driver):
+    from tests.test_gpu_act_wide import SHARED
+    lines = subprocess.run([driver] + [str(v) for c in SHARED for v in c], capture_output=True, text=True, check=True).stdout.split("\n")
+    for case, line in zip(SHARED, lines):
+        assert line.split()[3] == "1", case
