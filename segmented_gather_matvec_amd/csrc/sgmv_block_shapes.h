@@ -17,8 +17,8 @@ struct NormVariant {
 constexpr NormVariant kNormForward[] = {{1, 1, 4, 8}, {1, 2, 4, 5}, {4, 1, 1, 6}, {4, 2, 1, 4}, {4, 3, 1, 3},
                                         {8, 2, 1, 2}, {16, 2, 1, 1}, {16, 3, 1, 1}, {16, 0, 1, 2}};
 constexpr NormVariant kNormBackward[] = {{1, 1, 8, 2}, {1, 2, 8, 1}, {4, 1, 2, 2}, {4, 2, 2, 1}, {4, 3, 2, 1},
-                                         {8, 2, 1, 1}, {8, 3, 1, 1}, {16, 0, 1, 0}};
-constexpr int kNormForwardVariants = 9, kNormBackwardVariants = 8;
+                                         {8, 2, 1, 1}, {8, 3, 1, 1}, {8, 4, 1, 1}, {16, 0, 1, 0}};
+constexpr int kNormForwardVariants = 9, kNormBackwardVariants = 9;
 constexpr int kNormWideCols = 2048;  // columns of a workgroup of the wide backward
 
 }  // namespace sgmv

@@ -7,7 +7,7 @@
 // that are still in registers (a sum of squares about 0 would lose them to a large mean).
 // Bound by memory: x (and dy) are read once, y (dx) is written once.  A row is held in registers by one wave (up to 1024
 // values) or by 4 to 16, so that every lane has up to four 16-byte loads in flight and the next row's are asked
-// for before this row's sums.  Rows beyond that are read again.
+// for before this row's sums.  Rows beyond that (24576 values, of the gradients 16384) are read again.
 #include <algorithm>
 
 #include "sgmv_block.h"
@@ -179,6 +179,10 @@ __global__ __launch_bounds__(1024) void sgmv_layer_norm_wide_kernel(NormParams p
 template <class T, int W, int KEEP, int ROWS>
 __global__ __launch_bounds__(W * 64 * ROWS) void sgmv_layer_norm_backward_kernel(NormParams p) {
   constexpr int TPR = W * 64;
+  // The next row is asked for before this one's sums, and gamma stays in registers.  Four eights a lane leave none for that: no row
+  // ahead, and each thread keeps its gamma in LDS (read again from memory 1500 x 16384 took 60 us instead of 55).
+  constexpr bool AHEAD = KEEP < 4;
+  __shared__ u32x4 own[AHEAD ? 1 : KEEP][AHEAD ? 1 : TPR];
   __shared__ float red[ROWS][2][W][2];
   __shared__ float joined[ROWS > 1 ? ROWS / 2 : 1][2][ROWS > 1 ? TPR * KEEP * 8 : 1];
   const int t = (int)threadIdx.x % TPR;
@@ -192,7 +196,7 @@ __global__ __launch_bounds__(W * 64 * ROWS) void sgmv_layer_norm_backward_kernel
   for (int k = 0; k < KEEP; ++k) {
     live[k] = k * TPR + t < p.w8;
     c[k] = live[k] ? (k * TPR + t) * 8 : (p.w8 - 1) * 8;
-    if (p.gamma != nullptr) g[k] = load_vec(p.gamma + c[k]);
+    if (p.gamma != nullptr) (AHEAD ? g[k] : own[k][t]) = load_vec(p.gamma + c[k]);
   }
   float sg[KEEP][8], sb[KEEP][8];
 #pragma unroll
@@ -213,10 +217,11 @@ __global__ __launch_bounds__(W * 64 * ROWS) void sgmv_layer_norm_backward_kernel
     }
   };
   int64_t row = (int64_t)blockIdx.x * ROWS + sub;
-  ask(row);
+  if (AHEAD) ask(row);
   int turn = 0;
   for (int64_t group = (int64_t)blockIdx.x * ROWS; group < p.n; group += step, row += step, turn ^= 1) {
     const bool on = ROWS == 1 || row < p.n;
+    if (!AHEAD) ask(row);
     u32x4 x[KEEP], y[KEEP], past[KEEP];
     const float mean = nmean, r = nr;
 #pragma unroll
@@ -228,7 +233,7 @@ __global__ __launch_bounds__(W * 64 * ROWS) void sgmv_layer_norm_backward_kernel
       for (int w = 0; w < 4; ++w) y[k][w] = on && live[k] ? ny[k][w] : 0u;
       if (p.beyond != nullptr) past[k] = load_stream(p.beyond + (on ? row : p.n - 1) * width + c[k]);
     }
-    if (group + step < p.n) ask(row + step);
+    if (AHEAD && group + step < p.n) ask(row + step);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < KEEP; ++k) {
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(W * 64 * ROWS) void sgmv_layer_norm_backward_kernel
       unpack8<T>(x[k], xv);
       unpack8<T>(y[k], yv);
       fill8(gv, 1.f);
-      if (p.gamma != nullptr) unpack8<T>(g[k], gv);
+      if (p.gamma != nullptr) unpack8<T>(AHEAD ? g[k] : own[k][t], gv);
       float a = 0.f, b = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -258,7 +263,7 @@ __global__ __launch_bounds__(W * 64 * ROWS) void sgmv_layer_norm_backward_kernel
       unpack8<T>(x[k], xv);
       unpack8<T>(y[k], yv);
       fill8(gv, 1.f);
-      if (p.gamma != nullptr) unpack8<T>(g[k], gv);
+      if (p.gamma != nullptr) unpack8<T>(AHEAD ? g[k] : own[k][t], gv);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float xh = (xv[e] - mean) * r, q = yv[e] * gv[e];
@@ -468,6 +473,7 @@ hipError_t launch_norm_back_t(const NormParams& p, hipStream_t s) {
     case 4: return launch_norm_back<T, 4>(p, s);
     case 5: return launch_norm_back<T, 5>(p, s);
     case 6: return launch_norm_back<T, 6>(p, s);
+    case 7: return launch_norm_back<T, 7>(p, s);
   }
   if (p.dX != nullptr) {
     hipLaunchKernelGGL((sgmv_layer_norm_stats_kernel<T>), dim3((unsigned)std::min(p.n, 8192)), dim3(1024), 0, s, p);

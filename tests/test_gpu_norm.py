@@ -128,6 +128,23 @@ def test_without_parameters(n, w, gamma, beta):
         check(g, ref, bound, what)
 
 
+# Rows of four eights a lane, several to a workgroup, whose gamma stays in LDS; gradients over their own inputs.
+@pytest.mark.parametrize("gamma", [False, True])
+@pytest.mark.parametrize("n,w,dtype", [(600, 12296, "bf16"), (520, 14344, "f16"), (300, 16384, "bf16")])
+def test_wide_rows_one_after_another(n, w, dtype, gamma):
+    c = Case(n + w, dtype, n, w, gamma=gamma)
+    _, mean, rstd = c.forward()
+    dX, dg, db = c.backward(mean, rstd)
+    for g, (ref, bound), what in zip((dX, dg, db), c.ref_backward(mean, rstd), ("dX", "dgamma", "dbeta")):
+        check(g, ref, bound, what)
+    ws = sg.new_layer_norm_workspace(n, w)
+    for into in ("dY", "beyond"):
+        t = getattr(c, into).clone()
+        sg.sgmv_layer_norm_backward(c.X, c.gamma, mean, rstd, t if into == "dY" else c.dY, ws, dX=t,
+                                    beyond=t if into == "beyond" else c.beyond)
+        assert torch.equal(t, dX)
+
+
 @pytest.mark.parametrize("w", [520, 4096, 40000])
 @pytest.mark.parametrize("scale,shift", [(2.0 ** -9, 0.0), (1.0, 300.0), (2.0 ** -6, -40.0), (500.0, 0.0), (2.0 ** -20, 0.0)])
 def test_small_large_and_shifted_rows(w, scale, shift):
