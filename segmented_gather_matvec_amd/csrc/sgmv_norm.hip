@@ -86,7 +86,9 @@ __global__ __launch_bounds__(W * 64 > kThreads ? W * 64 : kThreads) void sgmv_la
       s[0] += live[k] ? a : 0.f;
     }
     row_sums<W, 1>(s, red, 0, t);
-    const float mean = s[0] / count;  // (a division: the mean of equal values is that value)
+    // (A division: the mean of equal values is that value, since a row that fits here has at most 3072 eights and 12 bits of
+    // them times 11 of a value are exact.)
+    const float mean = s[0] / count;
     s[0] = 0.f;
 #pragma unroll
     for (int k = 0; k < KEEP; ++k) {
@@ -125,35 +127,49 @@ __global__ __launch_bounds__(W * 64 > kThreads ? W * 64 : kThreads) void sgmv_la
   }
 }
 
-// Rows beyond what 16 waves hold: read three times, the last two from the caches.
+// Rows beyond what 16 waves hold: read three times, the last two from the caches.  Sums of so many values round even where all
+// are alike (100008 equal fp16 values: 63 of 200 such rows had a mean beside their value, which made normalised values of up to
+// 0.78 where 0 is right), so the second pass also sums what is left about the first mean: that corrects the mean, exactly where
+// all values are alike, and the mean of squares about it.
 template <class T>
 __global__ __launch_bounds__(1024) void sgmv_layer_norm_wide_kernel(NormParams p) {
   constexpr int TPR = 1024, W = TPR / 64;
-  __shared__ float red[2][W][1];
+  __shared__ float red_first[2][W][1], red_rest[2][W][2];  // (two barriers a row: one half of each is enough)
   const int t = threadIdx.x;
   const float count = (float)(p.w8 * 8);
   for (int64_t row = blockIdx.x; row < p.n; row += gridDim.x) {
     const uint16_t* const x = p.X + row * p.w8 * 8;
-    float s[1] = {0.f};
+    float total[1] = {0.f};
 #pragma unroll 4
     for (int k = t; k < p.w8; k += TPR) {
-      float v[8];
+      float v[8], a = 0.f;
       unpack8<T>(load_vec(x + (int64_t)k * 8), v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += v[e];
+      for (int e = 0; e < 8; ++e) a += v[e];
+      total[0] += a;
     }
-    row_sums<W, 1>(s, red, 0, t);
-    const float mean = s[0] / count;  // (a division: the mean of equal values is that value)
-    s[0] = 0.f;
+    row_sums<W, 1>(total, red_first, 0, t);
+    const float first = total[0] / count;
+    float s[2] = {0.f, 0.f};
 #pragma unroll 4
     for (int k = t; k < p.w8; k += TPR) {
-      float v[8];
+      float v[8], a = 0.f, b = 0.f;
       unpack8<T>(load_vec(x + (int64_t)k * 8), v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] = __builtin_fmaf(v[e] - mean, v[e] - mean, s[0]);
+      for (int e = 0; e < 8; ++e) {
+        const float d = v[e] - first;
+        a = __builtin_fmaf(d, d, a);
+        b += d;
+      }
+      s[0] += a;
+      s[1] += b;
     }
-    row_sums<W, 1>(s, red, 1, t);
-    const float r = 1.f / sqrtf(s[0] / count + p.eps);
+    row_sums<W, 2>(s, red_rest, 0, t);
+    float rest = s[1] / count, var = s[0] / count;
+    rest = rest == rest ? rest : 0.f;  // (a row of infinities: its mean stays infinite, its variance NaN)
+    const float mean = first + rest;
+    var = __builtin_fmaf(-rest, rest, var);
+    const float r = 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps);  // (NaN stays)
     if (t == 0) {
       if (p.mean != nullptr) p.mean[row] = mean;
       if (p.rstd != nullptr) p.rstd[row] = r;
