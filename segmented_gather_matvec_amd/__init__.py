@@ -714,12 +714,18 @@ def sgmv_combine_rows(Ys, slots, Y, weights=None, residual=None, stream=None):
 
 def sgmv_combine_rows_backward(dY, Ys, slots, weights=None, dYs=None, dweights=None, stream=None):
     """Gradients of sgmv_combine_rows from dY [n_rows, width]: dYs [n_rows * top_k, width] and dweights (float32, one
-    per choice), each or None; Ys is needed for dweights only.  Asynchronous."""
+    per choice), each or None; Ys [n_rows * top_k, width] is needed for dweights only.  dYs says how many choices a row has
+    (without it Ys and dweights do, which then have to agree); slots and weights may be longer.  Asynchronous."""
     import torch
     index, dtype, code, n, width = _matrix(dY, "dY")
-    _need(slots, "slots", torch.int32)
-    m = slots.numel() if slots is not None else 0
-    top_k = _top_k(m, n, "slots")
+    if dYs is not None:
+        _matrix(dYs, "dYs")
+        top_k = _top_k(dYs.shape[0], n, "dYs")
+    elif Ys is not None:
+        _matrix(Ys, "Ys")
+        top_k = _top_k(max(Ys.shape[0], dweights.numel() if dweights is not None else 0), n, "Ys and dweights")
+    else:       # (nothing can be wanted)
+        top_k = _top_k(slots.numel() if slots is not None else 0, n, "slots")
     m = n * top_k
     args = (_layer_ptr(Ys, "Ys", index, dtype, (m, width)), _layer_ptr(slots, "slots", index, torch.int32, None, m),
             _layer_ptr(weights, "weights", index, torch.float32, None, m),
