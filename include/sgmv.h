@@ -527,6 +527,10 @@ typedef enum sgmv_act {
   SGMV_ACT_GELU = 4       /* z Phi(z) = 0.5 z erfc(-z / sqrt 2) */
 } sgmv_act_t;
 
+/* Added to the act of sgmv_dense_act_lora_backward, and to SGMV_DENSE_ACT_BACKWARD where its workspace is asked for: dZ is
+ * carried as two 16-bit halves whatever the number of rows (see that call's precision). */
+#define SGMV_DZ_HALVES 0x100
+
 /* Most rows a layer call takes, and most blocks of up to 64 rows of one segment
  * (num_segs where max_seg_len <= 64, else the smaller of num_segs *
  * ceil(max_seg_len / 64) and ceil(n_rows / 64) + num_segs); and most segments
@@ -599,7 +603,12 @@ sgmv_status_t sgmv_gated_lora_backward(const sgmv_problem_t* problem, const void
  * units in the last place of fp32.  dZ is an operand of the matrix
  * cores and rounded once for that (or two halves, or a row divided by a power of two of its own, as dG and dU of the
  * gated block; a value keeps its 11 bits of fp16 down to 2^-21 of the row's largest 1.13 |dY|);
- * dbias sums the unrounded dZ.  act = SGMV_ACT_NONE takes dY as dZ. */
+ * dbias sums the unrounded dZ.  act = SGMV_ACT_NONE takes dY as dZ.
+ * One rounding of dZ to bf16 moves dX, dA_k, dB_k and dW of a large batch by as much again as their own rounding does (0.0023 of
+ * the gradient's 2-norm off the exact one instead of 0.0017).  act + SGMV_DZ_HALVES carries dZ as two halves at any size, as
+ * up to 128 rows and 2^18 values of dZ do by themselves: 16 significant bits of bf16, 22 of fp16, at about twice the
+ * time; at most SGMV_MAX_LAYER_ROWS / 2 rows (SGMV_ERR_UNSUPPORTED), and the workspace of SGMV_DENSE_ACT_BACKWARD +
+ * SGMV_DZ_HALVES. */
 sgmv_status_t sgmv_dense_act_lora_apply(const sgmv_problem_t* problem, const void* X, const void* W,
                                         const sgmv_projection_t* proj, const void* bias, int32_t act,
                                         const void* residual, void* Z, const int32_t* seg_indptr, const int32_t* lora_idx,

@@ -49,6 +49,7 @@ SGMV_MAX_TOP_K, SGMV_MAX_ROUTE_LORAS = 64, 8192
 SGMV_ACT_SILU, SGMV_ACT_GELU_TANH, SGMV_ACT_NONE, SGMV_ACT_RELU, SGMV_ACT_GELU = range(5)
 SGMV_DENSE_FORWARD, SGMV_DENSE_BACKWARD, SGMV_GATED_FORWARD, SGMV_GATED_BACKWARD = range(4)
 SGMV_DENSE_ACT_FORWARD, SGMV_DENSE_ACT_BACKWARD = 5, 6
+SGMV_DZ_HALVES = 0x100      # added to the act of sgmv_dense_act_lora_backward and to its op: dZ in two halves at any size
 
 
 class SgmvError(RuntimeError):
@@ -598,7 +599,9 @@ def sgmv_dense_act_lora_backward(problem, X, W, proj, dY, seg_indptr, lora_idx, 
                                  grad=None, dbias=None, accumulate=False, stream=None):
     """Gradients of sgmv_dense_act_lora_apply from dY and the stored Z (not needed for SGMV_ACT_NONE): dX (written), `grad`
     = (dW, dA_ptrs, dB_ptrs) and dbias, each or None, accumulated or written as in sgmv_dense_lora_backward; `ws` from
-    new_layer_workspace(problem, SGMV_DENSE_ACT_BACKWARD).  Asynchronous."""
+    new_layer_workspace(problem, SGMV_DENSE_ACT_BACKWARD).  With SGMV_DZ_HALVES added to `act` and to the workspace's op, dZ is
+    carried as two 16-bit halves at any size (large batches: gradients as exact as from a 32-bit dZ, about twice the time).
+    Asynchronous."""
     a = _LayerArgs(problem, X, [(W, "W")], seg_indptr, lora_idx, ws)
     a.launch("sgmv_dense_act_lora_backward", stream, *a.W, ctypes.byref(a.projection(proj, "proj")), int(act),
              a.rows(Z, "Z", "out"), a.rows(dY, "dY", "out"), a.rows(dX, "dX", "in"), ctypes.byref(a.grad(grad, "grad")),

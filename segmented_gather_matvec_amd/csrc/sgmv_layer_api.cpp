@@ -429,13 +429,16 @@ sgmv_status_t sgmv_dense_act_lora_backward(const sgmv_problem_t* p, const void* 
                                            void* stream) {
   sgmv_status_t st = check_layer(p);
   if (st != SGMV_OK) return st;
+  const bool all_halves = (act & SGMV_DZ_HALVES) != 0;
+  act &= ~SGMV_DZ_HALVES;
   if (!epilogue_act(act)) return SGMV_ERR_INVALID_ARG;
+  if (all_halves && !halves_fit(*p)) return SGMV_ERR_UNSUPPORTED;
   if (accumulate != 0 && accumulate != 1) return SGMV_ERR_INVALID_ARG;
   const sgmv_projection_grad_t none{};
   const sgmv_projection_grad_t* g = grad ? grad : &none;
   const bool rows = p->n_rows > 0, slopes = act != SGMV_ACT_NONE;
   if (!proj || (rows && (!dY || (slopes && !Z)))) return SGMV_ERR_INVALID_ARG;
-  const ActPlan a = plan_act_backward(*p, act);
+  const ActPlan a = plan_act_backward(*p, act, all_halves);
   if (rows) {
     st = check_call(X, &W, &proj, 1, seg_indptr, lora_idx, ws, ws_bytes, a.layer);
     if (st != SGMV_OK) return st;

@@ -151,12 +151,12 @@ sgmv_status_t check_layer(const sgmv_problem_t* p) {
   return units > SGMV_MAX_LAYER_UNITS || (!direct && p->num_segs > SGMV_MAX_LAYER_LONG_SEGS) ? SGMV_ERR_UNSUPPORTED : SGMV_OK;
 }
 
-LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128) {
+LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128, bool all_halves) {
   LayerPlan l;
   l.projections = layer_gated(op) ? 2 : 1;
   l.lora = !nothing_to_do(p);
   const int64_t n = p.n_rows;
-  l.halves = layer_elementwise(op) && n <= kHalvesRows && n * p.h_out <= kHalvesValues ? 2 : 1;
+  l.halves = layer_elementwise(op) && (all_halves || (n <= kHalvesRows && n * p.h_out <= kHalvesValues)) ? 2 : 1;
   const bool back = layer_backward(op);
   size_t at = 0;
   const auto take = [&](size_t bytes) {
@@ -216,9 +216,9 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128) {
   return l;
 }
 
-ActPlan plan_act_backward(const sgmv_problem_t& p, int act) {
+ActPlan plan_act_backward(const sgmv_problem_t& p, int act, bool all_halves) {
   ActPlan a;
-  a.layer = plan_layer(p, act == SGMV_ACT_NONE ? SGMV_DENSE_BACKWARD : SGMV_DENSE_ACT_BACKWARD, true);
+  a.layer = plan_layer(p, act == SGMV_ACT_NONE ? SGMV_DENSE_BACKWARD : SGMV_DENSE_ACT_BACKWARD, true, all_halves);
   // Blocks of rows by 2048 columns: some workgroups a CU, each of four rows and more (their sums are written and read).
   // Whole rows of fp16 have more waves a workgroup: two on a CU.
   const bool whole = p.dtype == SGMV_F16 && act != SGMV_ACT_NONE && p.h_out > 2048 && p.h_out <= sgmv::kActRowCols;
@@ -249,6 +249,10 @@ sgmv_status_t sgmv_layer_workspace_bytes(const sgmv_problem_t* p, int32_t op, si
     case SGMV_DENSE_ACT_FORWARD: *bytes = plan_layer(*p, op).total; break;
     case SGMV_DENSE_ACT_BACKWARD:  // of any activation
       *bytes = std::max(plan_act_backward(*p, SGMV_ACT_NONE).total, plan_act_backward(*p, SGMV_ACT_SILU).total);
+      break;
+    case SGMV_DENSE_ACT_BACKWARD | SGMV_DZ_HALVES:
+      if (!halves_fit(*p)) return SGMV_ERR_UNSUPPORTED;
+      *bytes = std::max(plan_act_backward(*p, SGMV_ACT_NONE, true).total, plan_act_backward(*p, SGMV_ACT_SILU, true).total);
       break;
     default: return SGMV_ERR_INVALID_ARG;
   }

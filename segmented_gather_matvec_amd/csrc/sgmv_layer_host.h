@@ -29,7 +29,7 @@ struct LayerPlan {
   bool lora = false;
   int projections = 1;
   DensePlan out;       // forward, or dX
-  int halves = 1;      // 2: the gated backward keeps dG and dU as hi and lo halves, 2 n rows (few rows)
+  int halves = 1;      // 2: dG and dU, or dZ, are kept as hi and lo halves, 2 n rows (few rows, or on request)
   bool one_launch = false;  // the thin products run in the dense product's launch, the epilogue sums their planes
   DensePlan dw;        // dW
   ThinPlan down;       // V = s_k X @ A_k        (K = h_in)
@@ -55,7 +55,8 @@ inline bool layer_elementwise(int op) { return op == SGMV_GATED_BACKWARD || op =
 sgmv_status_t check_layer(const sgmv_problem_t* p);
 // wide128: 128 x 256 tiles too (the calls with an activation).
 inline bool layer_act(int op) { return op == SGMV_DENSE_ACT_FORWARD || op == SGMV_DENSE_ACT_BACKWARD; }
-LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128);
+// all_halves: the elementwise products are kept as two halves at any size (SGMV_DZ_HALVES).
+LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128, bool all_halves = false);
 inline LayerPlan plan_layer(const sgmv_problem_t& p, int op) { return plan_layer(p, op, layer_act(op)); }
 
 // The backward call of a dense layer with an activation: the layer's plan (without an activation it is the plain dense
@@ -65,6 +66,8 @@ struct ActPlan {
   int32_t rows_per_block = 1, blocks = 1;
   size_t planes_off = 0, total = 0;
 };
-ActPlan plan_act_backward(const sgmv_problem_t& p, int act);
+// all_halves: as of plan_layer; at most half of SGMV_MAX_LAYER_ROWS rows then (dX's product has 2 n).
+ActPlan plan_act_backward(const sgmv_problem_t& p, int act, bool all_halves = false);
+inline bool halves_fit(const sgmv_problem_t& p) { return p.n_rows <= SGMV_MAX_LAYER_ROWS / 2; }
 
 }  // namespace sgmv_host
