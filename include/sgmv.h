@@ -632,7 +632,8 @@ sgmv_status_t sgmv_dense_act_lora_backward(const sgmv_problem_t* problem, const 
  *                               sorted ones; perm [m], its inverse (the builder's perm where top_k = 1);
  *                               seg_indptr [num_loras + 1] and lora_idx [num_loras]: one segment
  *                               per LoRA, empty ones too, for the calls above with
- *                               n_rows = m, num_segs = num_loras, max_seg_len = m (or any bound).
+ *                               n_rows = m, num_segs = num_loras, max_seg_len = m (or a smaller
+ *                               number that no segment's length passes).
  *                               Ascending LoRA, ties by entry (a stable sort).  Entries whose id is
  *                               outside [0, num_loras) have no LoRA: they come last, in
  *                               their order, and no segment covers them.
@@ -693,7 +694,9 @@ sgmv_status_t sgmv_combine_rows_backward(int32_t dtype, int32_t n_rows, int32_t 
  * other.  accumulate = 0: dgamma and dbeta are written; 1: added to what is there in
  * fp32 and rounded once.  dX is always written.
  * Sums are fp32 in a fixed order (no atomics), outputs are rounded once; the variance
- * is the mean of squares about the mean.  A row of infinities or NaN spoils its own
+ * is the mean of squares about the mean, and the mean of equal values is that value.  (bf16 rows whose
+ * sum, or sum of squares about the mean, leaves fp32 have a mean or variance of infinity, or a variance of 0.)
+ * A row of infinities or NaN spoils its own
  * outputs, dgamma and dbeta only.
  * n_rows <= SGMV_MAX_LAYER_ROWS; n_rows = 0: the forward call does nothing, the backward call
  * writes zero dgamma and dbeta (accumulate = 0).  ws: device workspace of

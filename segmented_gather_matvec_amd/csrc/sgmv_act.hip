@@ -3,7 +3,8 @@
 //
 // Bound by memory: Z and dY are read once, dZ is written once, and the column sums ride along in registers; the blocks' sums
 // are written as planes and added up by a launch of their own (no atomics: one order).  bf16, 8192 x 11008 with the bias's
-// gradient: 100 us relu, 104 to 109 the others (5.2 TB/s; the sums alone, without an activation, 37).
+// gradient: 100 us relu, 104 to 109 the others (5.2 TB/s; the sums alone, without an activation, 37).  dZ takes
+// ordinary stores, not those past the caches: the products of the same call read it next.
 // fp16 rows carry a power of two each (as in the gated block's backward): dZ is an operand of the matrix cores,
 // and a row whose values are small must not lose them to fp16's denormals.  The power comes from the row's largest |dY|
 // (no activation here has a slope beyond 1.13).  Rows of up to 16384 columns are one workgroup's, which finds it on its way; wider ones

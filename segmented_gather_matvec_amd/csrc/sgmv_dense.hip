@@ -291,7 +291,8 @@ __device__ inline u32x2 round4(const f32x4& v) {
 
 // Four columns c .. c + 3 of row-major outputs at o = m N + c: Z = z + bias on request, Y = act(Z) + residual.
 // STREAM: past the caches.  (Outputs as large as the Infinity Cache that stay in it dirty are written back while the next
-// call reads: 8192 x 4096 -> 11008 with Z 642 -> 620 us, and the thin products of the call after it 30 -> 22.)
+// call reads: 8192 x 4096 -> 11008 with Z 642 -> 620 us, and the thin products of the call after it 30 -> 22.  The tiles store
+// so at every size; what that costs a call that reads a small output right after has not been measured.)
 typedef __attribute__((address_space(1))) u32x2* global_u32x2_wptr;
 template <bool STREAM>
 __device__ inline void store4(uint16_t* p, const u32x2& v) {

@@ -166,9 +166,9 @@ LayerPlan plan_layer(const sgmv_problem_t& p, int op, bool wide128, bool all_hal
   };
   if (l.lora) {
     const size_t v = (size_t)n * p.rank * sizeof(float);
-    // The forward call with an activation, beyond decode's rows: half the splits, half the planes to sum (2011 rows, K = 11008,
-    // r = 64: product and sum 23 + 9 us and 21 + 6; 8192 rows, K = 4096, r = 16: 30 + 5 either way; the two products of a
-    // backward pass, 4096 rows 4096 -> 11008, r = 16, would lose by it: 35 + 5 and 39 + 5).
+    // The forward call with an activation, beyond decode's rows: half the splits, half the planes to sum.  It rests on two shapes:
+    // 2011 rows, K = 11008, r = 64 gain (product and sum 23 + 9 us and 21 + 6), 8192 rows, K = 4096, r = 16 take 30 + 5
+    // either way.  (The two products of a backward pass, 4096 rows 4096 -> 11008, r = 16, would lose by it: 35 + 5 and 39 + 5.)
     l.down = plan_thin(p, p.h_in, l.projections, 1, wide128 && !back && n > kDecodeRows ? 512 : 1024);
     if (back) l.up = plan_thin(p, p.h_out, l.projections * l.halves, l.halves);
     for (int i = 0; i < l.projections; ++i) {

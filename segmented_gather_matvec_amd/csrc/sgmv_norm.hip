@@ -86,8 +86,8 @@ __global__ __launch_bounds__(W * 64 > kThreads ? W * 64 : kThreads) void sgmv_la
       s[0] += live[k] ? a : 0.f;
     }
     row_sums<W, 1>(s, red, 0, t);
-    // (A division: the mean of equal values is that value, since a row that fits here has at most 3072 eights and 12 bits of
-    // them times 11 of a value are exact.)
+    // (A division: the mean of equal values is that value, since a row that fits here has fewer than 2^12 eights, and their
+    // number times the 11 bits of a value is exact.)
     const float mean = s[0] / count;
     s[0] = 0.f;
 #pragma unroll
