@@ -166,7 +166,7 @@ __global__ __launch_bounds__(1024) void sgmv_layer_norm_wide_kernel(NormParams p
     }
     row_sums<W, 2>(s, red_rest, 0, t);
     float rest = s[1] / count, var = s[0] / count;
-    rest = rest == rest ? rest : 0.f;  // (a row of infinities: its mean stays infinite, its variance NaN)
+    rest = rest - rest == 0.f ? rest : 0.f;  // (infinities, or a sum beyond fp32: the mean stays infinite)
     const float mean = first + rest;
     var = __builtin_fmaf(-rest, rest, var);
     const float r = 1.f / sqrtf((var < 0.f ? 0.f : var) + p.eps);  // (NaN stays)

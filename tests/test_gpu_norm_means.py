@@ -86,3 +86,17 @@ def test_nearly_constant_rows(w, dtype):
     y = d * r[:, None] * g + b
     ey = g.abs() * r[:, None] * (em[:, None] + (d.abs() + em[:, None]) * (er[:, None] + 5 * u)) + 2 * u * (b.abs() + y.abs())
     check(Y, y, ey, "Y")
+
+
+@pytest.mark.parametrize("w", [4096, 24584, 100008])
+def test_sums_beyond_fp32(w):
+    """A row whose sum leaves fp32, with and without infinities in it, has a mean of infinity; the others are as they were."""
+    gamma, beta = parameters(w, torch.bfloat16)
+    X = torch.randn(7, w, generator=torch.Generator().manual_seed(w)).bfloat16().cuda()
+    clean = forward(X, gamma, beta)
+    X[1], X[4], X[5, 3] = 3e38, -3e38, float("inf")
+    got = forward(X, gamma, beta)
+    assert torch.equal(got[1][[1, 4, 5]], torch.tensor([float("inf"), -float("inf"), float("inf")], device="cuda"))
+    for a, b in zip(got, clean):
+        assert torch.equal(a[[0, 2, 3, 6]], b[[0, 2, 3, 6]])
+    assert got[0][[1, 4, 5]].isnan().any(1).all()
